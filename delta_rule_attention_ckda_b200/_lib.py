@@ -17,7 +17,8 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libckda.so")
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported request", 3: "pointer not 16-byte aligned",
-          4: "CUDA error", 5: "device wait timed out", 6: "workspace missing or too small"}
+          4: "CUDA error", 5: "device wait timed out", 6: "workspace missing or too small",
+          7: "index on the device out of range or named twice"}
 F32, BF16 = 0, 1
 PATH_RECURRENT, PATH_CHUNK_TC = 0, 1
 
@@ -80,6 +81,25 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     lib.ckda_decode_step.restype = i
     lib.ckda_decode_step_ex.argtypes = [vp, vp, vp, fp, fp, fp, fp] + [i] * 6 + [vp]
     lib.ckda_decode_step_ex.restype = i
+    ll, f = ctypes.c_longlong, ctypes.c_float
+    lib.ckda_gated_fwd_workspace_bytes.argtypes = [i] * 7
+    lib.ckda_gated_fwd_workspace_bytes.restype = sz
+    lib.ckda_gated_fwd.argtypes = [vp] * 9 + [i] * 7 + [ll] * 3 + [i, vp, sz, vp]
+    lib.ckda_gated_fwd.restype = i
+    lib.ckda_gated_bwd_workspace_bytes.argtypes = [i] * 7
+    lib.ckda_gated_bwd_workspace_bytes.restype = sz
+    lib.ckda_gated_bwd.argtypes = [vp] * 15 + [i] * 7 + [ll] * 3 + [i, vp, sz, vp]
+    lib.ckda_gated_bwd.restype = i
+    lib.ckda_gated_decode_step.argtypes = [vp] * 8 + [i] * 6 + [ll] * 3 + [i, vp]
+    lib.ckda_gated_decode_step.restype = i
+    lib.ckda_qk_prep.argtypes = [vp] * 7 + [i, vp] + [i] * 6 + [ll] * 2 + [i] * 3 + [f] * 3 + [vp]
+    lib.ckda_qk_prep.restype = i
+    lib.ckda_qk_prep_bwd_workspace_bytes.argtypes = [i]
+    lib.ckda_qk_prep_bwd_workspace_bytes.restype = sz
+    lib.ckda_qk_prep_bwd.argtypes = [vp] * 11 + [i, vp] + [i] * 6 + [ll] * 2 + [i] * 3 + [f] * 3 + [vp, sz, vp]
+    lib.ckda_qk_prep_bwd.restype = i
+    lib.ckda_state_copy.argtypes = [vp] * 3 + [i] * 3 + [ll, vp]
+    lib.ckda_state_copy.restype = i
     lib.ckda_get_device_error.argtypes = [vp]
     lib.ckda_get_device_error.restype = i
     _lib = lib

@@ -1,8 +1,8 @@
 """Build libckda.so (the CKDA C-ABI library) in-tree with nvcc for sm_100a."""
 from __future__ import annotations
 
-import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -13,37 +13,75 @@ LIB = os.path.join(PKG, "libckda.so")
 SELFTEST_LIB = os.path.join(PKG, "libckda_selftest.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
-FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-         "-shared", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
+ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
+FLAGS = [*ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
          "-Xptxas", "-warn-spills"]
 
 
-TARGETS = {LIB: "ckda_api.cu", SELFTEST_LIB: "selftest.cu"}
+TARGETS = {LIB: ["ckda_api.cu", "gated_api.cu"], SELFTEST_LIB: ["selftest.cu"]}
+OBJ = os.path.join(PKG, "_build")
 
 
-def _newest_input():
-    files = glob.glob(os.path.join(CSRC, "**", "*.cu*"), recursive=True)
-    files += glob.glob(os.path.join(ROOT, "include", "*.h"))
-    files.append(os.path.abspath(__file__))
-    return max(os.path.getmtime(f) for f in files)
+def _inputs(src: str):
+    """The files `src` is compiled from: itself and every file of this package it includes."""
+    seen, todo = set(), [os.path.join(CSRC, src)]
+    while todo:
+        f = todo.pop()
+        if f in seen:
+            continue
+        seen.add(f)
+        for name in re.findall(r'^\s*#include "([^"]+)"', open(f).read(), re.M):
+            for d in (os.path.dirname(f), CSRC, os.path.join(ROOT, "include")):
+                if os.path.exists(os.path.join(d, name)):
+                    todo.append(os.path.normpath(os.path.join(d, name)))
+                    break
+    return seen | {os.path.abspath(__file__)}
 
 
-def _build_one(lib: str, src: str, force: bool, verbose: bool, extra) -> None:
-    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _newest_input():
-        return
-    tmp = lib + f".tmp{os.getpid()}"
-    cmd = [NVCC, *FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-           os.path.join(CSRC, src), "-o", tmp]
+def _newer(out: str, files) -> bool:
+    return os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(f) for f in files)
+
+
+def _run(cmd, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
+
+
+def _build_one(lib: str, sources, force: bool, verbose: bool, extra) -> None:
+    inputs = {src: _inputs(src) for src in sources}
+    if not force and _newer(lib, set().union(*inputs.values())):
+        return
+    os.makedirs(OBJ, exist_ok=True)
+    objects, procs = [], []
+    for src in sources:                        # one object per source, compiled side by side
+        obj = os.path.join(OBJ, src + ".o")
+        objects.append(obj)
+        if not force and _newer(obj, inputs[src]):
+            continue
+        tmp = obj + f".tmp{os.getpid()}"
+        cmd = [NVCC, *FLAGS, *extra, "-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c",
+               os.path.join(CSRC, src), "-o", tmp]
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        procs.append((subprocess.Popen(cmd), tmp, obj, cmd))
+    failed = None
+    for p, tmp, obj, cmd in procs:
+        if p.wait() != 0:
+            failed = subprocess.CalledProcessError(p.returncode, cmd)
+        else:
+            os.replace(tmp, obj)
+    if failed:
+        raise failed
+    tmp = lib + f".tmp{os.getpid()}"
+    _run([NVCC, *ARCH, "-shared", "-Xcompiler", "-fPIC", *objects, "-o", tmp], verbose)
     os.replace(tmp, lib)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     """Build libckda.so and the test-only libckda_selftest.so; returns libckda.so's path."""
-    for lib, src in TARGETS.items():
-        _build_one(lib, src, force, verbose, extra)
+    for lib, sources in TARGETS.items():
+        _build_one(lib, sources, force, verbose, extra)
     return LIB
 
 

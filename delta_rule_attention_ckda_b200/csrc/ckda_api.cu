@@ -117,6 +117,8 @@ bool parse_mode(int mode, bool* log_gate, bool* norm_qk) {
 
 extern "C" {
 
+cudaError_t ckda_gated_take_error(unsigned int* word);       // gated_api.cu
+
 int ckda_abi_version(void) { return CKDA_ABI_VERSION; }
 
 const char* ckda_status_string(ckda_status_t s) {
@@ -128,6 +130,7 @@ const char* ckda_status_string(ckda_status_t s) {
         case CKDA_ERR_CUDA: return "CUDA error";
         case CKDA_ERR_TIMEOUT: return "device wait timed out";
         case CKDA_ERR_WORKSPACE: return "workspace missing or too small";
+        case CKDA_ERR_INDEX: return "index on the device out of range or named twice";
     }
     return "unknown status";
 }
@@ -452,8 +455,10 @@ ckda_status_t ckda_get_device_error(void* stream) {
         return CKDA_ERR_CUDA;
     if (word != 0 && cudaMemcpyToSymbol(ckda::g_error_word, &zero, sizeof(zero)) != cudaSuccess)
         return CKDA_ERR_CUDA;
+    unsigned int gated = 0;
+    if (ckda_gated_take_error(&gated) != cudaSuccess) return CKDA_ERR_CUDA;
     if (word & ckda::kErrTimeout) return CKDA_ERR_TIMEOUT;
-    return CKDA_OK;
+    return gated != 0 ? CKDA_ERR_INDEX : CKDA_OK;
 }
 
 }  // extern "C"

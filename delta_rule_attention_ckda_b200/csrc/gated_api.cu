@@ -1,0 +1,414 @@
+// Host side of the scalar-gate operators of the C ABI (see include/ckda.h): the gated delta
+// rule with one decay per head (chunked forward, backward, single-token step on a pool of
+// states), the preparation of queries and keys, and copies of states within a pool.
+// Argument validation, path selection, workspace layout and launches.
+#include "ckda.h"
+
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "kernels/gated_common.cuh"
+#include "kernels/gated_simt.cuh"
+#include "kernels/gated_decode.cuh"
+#include "kernels/qk_prep.cuh"
+#include "kernels/state_copy.cuh"
+
+namespace {
+
+using namespace ckda::gated;
+typedef __nv_bfloat16 bf16;
+
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }   // indexes, gates
+inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
+inline ckda_status_t launch_status() { return cudaGetLastError() == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA; }
+inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();                    // no device: plan for a B200
+        return 148;
+    }
+    return n;
+}
+
+// Opt in to more than 48 KB of dynamic shared memory, once per kernel and device.
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes) {
+    return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+struct Shape {
+    int N, T, total, Hk, Hv, dk, dv;
+    ckda_dtype_t dt;
+};
+
+ckda_status_t check_shape(const Shape& s, bool packed) {
+    if (s.N < 0 || s.T < 0 || s.total < 0 || s.Hk < 1 || s.Hv < 1) return CKDA_ERR_INVALID_ARG;
+    if (s.dk < 1 || s.dk > CKDA_MAX_D || s.dv < 1 || s.dv > CKDA_MAX_D) return CKDA_ERR_INVALID_ARG;
+    if (s.dt != CKDA_F32 && s.dt != CKDA_BF16) return CKDA_ERR_INVALID_ARG;
+    if (s.Hv % s.Hk != 0) return CKDA_ERR_INVALID_ARG;
+    if (!packed && (long long)s.N * s.T != s.total) return CKDA_ERR_INVALID_ARG;
+    if ((long long)s.N * s.Hv > 0x7fffffffLL || (long long)s.total + (long long)s.N * C > 0x7fffffffLL) return CKDA_ERR_UNSUPPORTED;
+    return CKDA_OK;
+}
+
+// Token strides cover at least one token's heads.
+bool strides_ok(const Shape& s, long long qs, long long ks, long long vs) {
+    return qs >= (long long)s.Hk * s.dk && ks >= (long long)s.Hk * s.dk && vs >= (long long)s.Hv * s.dv;
+}
+
+ckda_status_t clear_or_copy(const float* from, float* to, size_t n, cudaStream_t st) {
+    if (to == nullptr || to == from || n == 0) return CKDA_OK;
+    cudaError_t e = from ? cudaMemcpyAsync(to, from, n * sizeof(float), cudaMemcpyDeviceToDevice, st)
+                         : cudaMemsetAsync(to, 0, n * sizeof(float), st);
+    return e == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
+}
+
+template <typename TIn>
+ckda_status_t simt_fwd(const Shape& s, const void* q, const void* k, const void* v, const float* g, const float* beta,
+                       const float* S0, void* o, float* ST, const Seqs& seqs, const int* slots, int pool, long long qs,
+                       long long ks, long long vs, cudaStream_t st) {
+    const int cols = s.dv <= 32 ? 32 : (s.dv <= 64 ? 64 : 128);
+    const dim3 grid((unsigned)(s.N * s.Hv), (unsigned)((s.dv + cols - 1) / cols));
+#define GATED_SIMT(D)                                                                                                \
+    simt_fwd_kernel<D, TIn><<<grid, cols, 0, st>>>(static_cast<const TIn*>(q), static_cast<const TIn*>(k),            \
+                                                   static_cast<const TIn*>(v), g, beta, S0, static_cast<TIn*>(o), ST, \
+                                                   seqs, slots, pool, s.Hk, s.Hv, s.dk, s.dv, qs, ks, vs)
+    if (s.dk <= 16) GATED_SIMT(16);
+    else if (s.dk <= 32) GATED_SIMT(32);
+    else if (s.dk <= 64) GATED_SIMT(64);
+    else GATED_SIMT(128);
+#undef GATED_SIMT
+    return launch_status();
+}
+
+// Workspace of the CUDA-core backward.
+struct SimtBwdLayout {
+    size_t ckpt, scratch, pq, pk, total;
+};
+SimtBwdLayout simt_bwd_layout(const Shape& s) {
+    SimtBwdLayout l;
+    const size_t mat = (size_t)s.dk * s.dv * sizeof(float);
+    l.ckpt = 0;
+    l.scratch = up256(l.ckpt + Seqs::slots(s.N, s.total) * (C / KB) * s.Hv * mat);
+    l.pq = up256(l.scratch + (size_t)s.N * s.Hv * KB * mat);
+    l.pk = up256(l.pq + (size_t)s.total * s.Hv * s.dk * sizeof(float));
+    l.total = up256(l.pk + (size_t)s.total * s.Hv * s.dk * sizeof(float));
+    return l;
+}
+
+template <typename TIn>
+ckda_status_t simt_bwd(const Shape& s, const void* q, const void* k, const void* v, const float* g, const float* beta,
+                       const float* S0, const void* grad_o, const float* dST, void* gq, void* gk, void* gv, float* gg,
+                       float* gb, float* gS0, const Seqs& seqs, long long qs, long long ks, long long vs, char* ws,
+                       cudaStream_t st) {
+    const SimtBwdLayout l = simt_bwd_layout(s);
+    auto F = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    if (allow_smem(simt_bwd_kernel<TIn>, kSimtBwdSmem) != cudaSuccess) return CKDA_ERR_CUDA;
+    simt_bwd_kernel<TIn><<<(unsigned)(s.N * s.Hv), NTB, kSimtBwdSmem, st>>>(
+        static_cast<const TIn*>(q), static_cast<const TIn*>(k), static_cast<const TIn*>(v), g, beta, S0,
+        static_cast<const TIn*>(grad_o), dST, F(l.ckpt), F(l.scratch), F(l.pq), F(l.pk), static_cast<TIn*>(gv), gg, gb,
+        gS0, seqs, s.Hk, s.Hv, s.dk, s.dv, qs, ks, vs);
+    if (cudaPeekAtLastError() != cudaSuccess) return launch_status();
+    const size_t n = (size_t)s.total * s.Hk * s.dk;
+    simt_share_kernel<TIn><<<(unsigned)std::min<size_t>((n + 255) / 256, 148 * 16), 256, 0, st>>>(
+        F(l.pq), F(l.pk), static_cast<TIn*>(gq), static_cast<TIn*>(gk), seqs, s.Hk, s.Hv, s.dk);
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+// Reads and clears the error word of this file's kernels (for ckda_get_device_error, after it
+// synchronised the stream). Not part of the ABI.
+cudaError_t ckda_gated_take_error(unsigned int* word) {
+    unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(word, g_gated_error_word, sizeof(*word));
+    if (e == cudaSuccess && *word != 0) e = cudaMemcpyToSymbol(g_gated_error_word, &zero, sizeof(zero));
+    return e;
+}
+
+size_t ckda_gated_fwd_workspace_bytes(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt) {
+    (void)N; (void)total; (void)Hk; (void)Hv; (void)dk; (void)dv; (void)dt;
+    return 0;
+}
+
+ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                             const float* S0, void* o, float* S_T, const int* cu_seqlens, int N, int T, int total, int Hk,
+                             int Hv, int dk, int dv, long long q_stride, long long k_stride, long long v_stride,
+                             ckda_dtype_t dt, void* workspace, size_t workspace_bytes, void* stream) {
+    const Shape s{N, T, total, Hk, Hv, dk, dv, dt};
+    ckda_status_t c = check_shape(s, cu_seqlens != nullptr);
+    if (c != CKDA_OK) return c;
+    if (total > 0 && (!q || !k || !v || !g || !beta || !o)) return CKDA_ERR_INVALID_ARG;
+    if (!strides_ok(s, q_stride, k_stride, v_stride)) return CKDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k, v, S0, o, S_T, workspace};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return CKDA_ERR_MISALIGNED;
+    if (!aligned4(cu_seqlens) || !aligned4(g) || !aligned4(beta)) return CKDA_ERR_MISALIGNED;
+    const size_t need = ckda_gated_fwd_workspace_bytes(N, total, Hk, Hv, dk, dv, dt);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return CKDA_ERR_WORKSPACE;
+    cudaStream_t st = as_stream(stream);
+    if (N == 0) return CKDA_OK;
+    if (total == 0) return clear_or_copy(S0, S_T, (size_t)N * Hv * dk * dv, st);
+    const Seqs seqs{cu_seqlens, N, T, total};
+    if (dt == CKDA_BF16) return simt_fwd<bf16>(s, q, k, v, g, beta, S0, o, S_T, seqs, nullptr, N, q_stride, k_stride, v_stride, st);
+    return simt_fwd<float>(s, q, k, v, g, beta, S0, o, S_T, seqs, nullptr, N, q_stride, k_stride, v_stride, st);
+}
+
+size_t ckda_gated_bwd_workspace_bytes(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt) {
+    const Shape s{N, 0, total, Hk, Hv, dk, dv, dt};
+    if (check_shape(s, true) != CKDA_OK || N == 0 || total == 0) return 0;
+    return simt_bwd_layout(s).total;
+}
+
+ckda_status_t ckda_gated_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                             const float* S0, const void* grad_o, const float* grad_S_T, void* grad_q, void* grad_k,
+                             void* grad_v, float* grad_g, float* grad_beta, float* grad_S0, const int* cu_seqlens, int N,
+                             int T, int total, int Hk, int Hv, int dk, int dv, long long q_stride, long long k_stride,
+                             long long v_stride, ckda_dtype_t dt, void* workspace, size_t workspace_bytes, void* stream) {
+    const Shape s{N, T, total, Hk, Hv, dk, dv, dt};
+    ckda_status_t c = check_shape(s, cu_seqlens != nullptr);
+    if (c != CKDA_OK) return c;
+    if (total > 0 && (!q || !k || !v || !g || !beta || !grad_o || !grad_q || !grad_k || !grad_v || !grad_g || !grad_beta))
+        return CKDA_ERR_INVALID_ARG;
+    if (!strides_ok(s, q_stride, k_stride, v_stride)) return CKDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k, v, S0, grad_o, grad_S_T, grad_q, grad_k, grad_v, grad_S0, workspace};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return CKDA_ERR_MISALIGNED;
+    const void* words[] = {cu_seqlens, g, beta, grad_g, grad_beta};
+    for (const void* p : words)
+        if (!aligned4(p)) return CKDA_ERR_MISALIGNED;
+    const size_t need = ckda_gated_bwd_workspace_bytes(N, total, Hk, Hv, dk, dv, dt);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return CKDA_ERR_WORKSPACE;
+    cudaStream_t st = as_stream(stream);
+    if (N == 0) return CKDA_OK;
+    if (total == 0) return clear_or_copy(grad_S_T, grad_S0, (size_t)N * Hv * dk * dv, st);
+    const Seqs seqs{cu_seqlens, N, T, total};
+    char* ws = static_cast<char*>(workspace);
+    if (dt == CKDA_BF16)
+        return simt_bwd<bf16>(s, q, k, v, g, beta, S0, grad_o, grad_S_T, grad_q, grad_k, grad_v, grad_g, grad_beta, grad_S0,
+                              seqs, q_stride, k_stride, v_stride, ws, st);
+    return simt_bwd<float>(s, q, k, v, g, beta, S0, grad_o, grad_S_T, grad_q, grad_k, grad_v, grad_g, grad_beta, grad_S0,
+                           seqs, q_stride, k_stride, v_stride, ws, st);
+}
+
+ckda_status_t ckda_gated_decode_step(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                                     float* S, void* o, const int* slots, int N, int pool, int Hk, int Hv, int dk, int dv,
+                                     long long q_stride, long long k_stride, long long v_stride, ckda_dtype_t dt,
+                                     void* stream) {
+    const Shape s{N, 1, N, Hk, Hv, dk, dv, dt};
+    ckda_status_t c = check_shape(s, false);
+    if (c != CKDA_OK) return c;
+    if (pool < 0 || (slots == nullptr && pool < N)) return CKDA_ERR_INVALID_ARG;
+    if (N == 0) return CKDA_OK;
+    if (!q || !k || !v || !g || !beta || !o || !S || pool == 0) return CKDA_ERR_INVALID_ARG;
+    if (!strides_ok(s, q_stride, k_stride, v_stride)) return CKDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {q, k, v, S, o};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return CKDA_ERR_MISALIGNED;
+    if (!aligned4(slots) || !aligned4(g) || !aligned4(beta)) return CKDA_ERR_MISALIGNED;
+    cudaStream_t st = as_stream(stream);
+    // Column slab of a CTA: the widest that still gives two CTAs per SM.
+    if ((dk == 64 || dk == 128) && dv % 32 == 0) {
+        const long long want = 2LL * sm_count(), rows = (long long)N * Hv;
+        int cw = 32;
+        if (dv % 128 == 0 && rows * (dv / 128) >= want) cw = 128;
+        else if (dv % 64 == 0 && rows * (dv / 64) >= want) cw = 64;
+        const dim3 grid((unsigned)rows, (unsigned)(dv / cw));
+#define GATED_DECODE(D, W, TIN)                                                                                     \
+    decode_kernel<D, W, TIN><<<grid, 256, 0, st>>>(static_cast<const TIN*>(q), static_cast<const TIN*>(k),           \
+                                                   static_cast<const TIN*>(v), g, beta, S, static_cast<TIN*>(o),     \
+                                                   slots, pool, Hk, Hv, dv, q_stride, k_stride, v_stride)
+#define GATED_DECODE2(D, TIN)                                                                                       \
+    do {                                                                                                            \
+        if (cw == 128) GATED_DECODE(D, 128, TIN);                                                                   \
+        else if (cw == 64) GATED_DECODE(D, 64, TIN);                                                                \
+        else GATED_DECODE(D, 32, TIN);                                                                              \
+    } while (0)
+        if (dk == 128) {
+            if (dt == CKDA_BF16) GATED_DECODE2(128, bf16);
+            else GATED_DECODE2(128, float);
+        } else {
+            if (dt == CKDA_BF16) GATED_DECODE2(64, bf16);
+            else GATED_DECODE2(64, float);
+        }
+#undef GATED_DECODE2
+#undef GATED_DECODE
+        return launch_status();
+    }
+    const Seqs seqs{nullptr, N, 1, N};
+    if (dt == CKDA_BF16) return simt_fwd<bf16>(s, q, k, v, g, beta, S, o, S, seqs, slots, pool, q_stride, k_stride, v_stride, st);
+    return simt_fwd<float>(s, q, k, v, g, beta, S, o, S, seqs, slots, pool, q_stride, k_stride, v_stride, st);
+}
+
+}  // extern "C"
+
+namespace {
+
+constexpr int kPrepMaxBlocks = 148 * 4;
+
+// Blocks of the backward pass: fixed by the sizes alone, so the weights' sums have one order.
+int prep_blocks(int tokens, int tpb) { return std::max(1, std::min((tokens + tpb - 1) / tpb, kPrepMaxBlocks)); }
+
+ckda_status_t prep_args(PrepArgs& a, const void* q, const void* k, const float* qw, const float* kw, const void* pos,
+                        int pos64, const double* inv_freq, int tokens, int period, int Hq, int Hk, int d, int rotary,
+                        long long qs, long long ks, ckda_dtype_t dt, int norm, int interleaved, float eps, float q_scale,
+                        float rope_scale) {
+    if (tokens < 0 || Hq < 1 || Hk < 0 || d < 1 || d > CKDA_PREP_MAX_D || rotary < 0 || rotary > d || rotary % 2 != 0)
+        return CKDA_ERR_INVALID_ARG;
+    if (dt != CKDA_F32 && dt != CKDA_BF16) return CKDA_ERR_INVALID_ARG;
+    if (norm < kNormNone || norm > kNormRms || interleaved < 0 || interleaved > 1 || pos64 < 0 || pos64 > 1)
+        return CKDA_ERR_INVALID_ARG;
+    if (qs < (long long)Hq * d || (Hk > 0 && ks < (long long)Hk * d)) return CKDA_ERR_INVALID_ARG;
+    if (rotary > 0 && !inv_freq) return CKDA_ERR_INVALID_ARG;
+    if (rotary > 0 && !pos && period < 1) return CKDA_ERR_INVALID_ARG;
+    if (tokens > 0 && (!q || (Hk > 0 && !k))) return CKDA_ERR_INVALID_ARG;
+    if ((long long)Hq + Hk > 4096) return CKDA_ERR_UNSUPPORTED;
+    a = PrepArgs{};
+    a.x[0] = q; a.x[1] = k;
+    a.w[0] = qw; a.w[1] = kw;
+    a.stride[0] = qs; a.stride[1] = ks;
+    a.heads[0] = Hq; a.heads[1] = Hk;
+    a.pos = rotary > 0 ? pos : nullptr;
+    a.inv_freq = inv_freq;
+    a.pos64 = pos64;
+    a.period = std::max(period, 1);
+    a.tokens = tokens; a.d = d; a.rotary = rotary; a.norm = norm; a.interleaved = interleaved;
+    a.eps = eps; a.q_scale = q_scale; a.rope_scale = rope_scale;
+    const void* ptrs[] = {q, k, qw, kw};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return CKDA_ERR_MISALIGNED;
+    if ((reinterpret_cast<uintptr_t>(pos) & (pos64 ? 7u : 3u)) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u))
+        return CKDA_ERR_MISALIGNED;
+    return CKDA_OK;
+}
+
+// Whether rows can be read 16 bytes a lane (see qk_prep.cuh).
+bool prep_vector(const PrepArgs& a, ckda_dtype_t dt) {
+    const int per16 = dt == CKDA_BF16 ? 8 : 4;
+    if (a.d % 8 != 0 || a.stride[0] % per16 != 0 || (a.heads[1] > 0 && a.stride[1] % per16 != 0)) return false;
+    return a.interleaved || a.rotary % 16 == 0;
+}
+
+// Tokens a block takes at a time: enough rows for the block's lanes, not more than spread the
+// tokens over the SMs.
+int prep_tpb(const PrepArgs& a, int groups, int ur) {
+    const int H = a.heads[0] + a.heads[1], sms = sm_count();
+    int tpb = std::max(1, groups * ur / H);
+    while (tpb > 1 && (long long)sms * 2 * tpb > a.tokens) tpb /= 2;
+    return std::min(tpb, 16);
+}
+
+template <typename TIn, bool kBack>
+ckda_status_t prep_launch(const PrepArgs& a, ckda_dtype_t dt, int* blocks_out, cudaStream_t st) {
+    constexpr int UR = kBack ? 2 : 4;
+    if (prep_vector(a, dt)) {
+        const int G = a.d <= 64 ? 8 : (a.d <= 128 ? 16 : 32);
+        const int groups = 256 / G, tpb = prep_tpb(a, groups, UR);
+        const int blocks = kBack ? prep_blocks(a.tokens, tpb) : (a.tokens + tpb - 1) / tpb;
+        size_t smem = ((size_t)tpb * a.rotary + 2 * a.d) * sizeof(float);
+        if (kBack) smem = std::max(smem, (size_t)groups * a.d * sizeof(float));
+        *blocks_out = blocks;
+        if (G == 8) prep_vec_kernel<TIn, 8, UR, kBack><<<blocks, 256, smem, st>>>(a, tpb);
+        else if (G == 16) prep_vec_kernel<TIn, 16, UR, kBack><<<blocks, 256, smem, st>>>(a, tpb);
+        else prep_vec_kernel<TIn, 32, UR, kBack><<<blocks, 256, smem, st>>>(a, tpb);
+    } else {
+        *blocks_out = prep_blocks(a.tokens, 1);
+        prep_row_kernel<TIn, kBack><<<*blocks_out, 256, 0, st>>>(a);
+    }
+    return launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+ckda_status_t ckda_qk_prep(const void* q, const void* k, void* q_out, void* k_out, const float* q_weight,
+                           const float* k_weight, const void* positions, int positions64, const double* inv_freq,
+                           int tokens, int period, int Hq, int Hk, int d, int rotary, long long q_stride,
+                           long long k_stride, ckda_dtype_t dt, int norm, int interleaved, float eps, float q_scale,
+                           float rope_scale, void* stream) {
+    PrepArgs a;
+    ckda_status_t c = prep_args(a, q, k, q_weight, k_weight, positions, positions64, inv_freq, tokens, period, Hq, Hk, d,
+                                rotary, q_stride, k_stride, dt, norm, interleaved, eps, q_scale, rope_scale);
+    if (c != CKDA_OK) return c;
+    if (tokens == 0) return CKDA_OK;
+    if (!q_out || (Hk > 0 && !k_out)) return CKDA_ERR_INVALID_ARG;
+    if (!aligned16(q_out) || !aligned16(k_out)) return CKDA_ERR_MISALIGNED;
+    a.out[0] = q_out;
+    a.out[1] = k_out;
+    int blocks;
+    return dt == CKDA_BF16 ? prep_launch<bf16, false>(a, dt, &blocks, as_stream(stream))
+                           : prep_launch<float, false>(a, dt, &blocks, as_stream(stream));
+}
+
+size_t ckda_qk_prep_bwd_workspace_bytes(int d) {
+    return d < 1 || d > CKDA_PREP_MAX_D ? 0 : (size_t)kPrepMaxBlocks * 2 * d * sizeof(float);
+}
+
+ckda_status_t ckda_qk_prep_bwd(const void* q, const void* k, const void* grad_q_out, const void* grad_k_out, void* grad_q,
+                               void* grad_k, float* grad_q_weight, float* grad_k_weight, const float* q_weight,
+                               const float* k_weight, const void* positions, int positions64, const double* inv_freq,
+                               int tokens, int period, int Hq, int Hk, int d, int rotary, long long q_stride,
+                               long long k_stride, ckda_dtype_t dt, int norm, int interleaved, float eps, float q_scale,
+                               float rope_scale, void* workspace, size_t workspace_bytes, void* stream) {
+    PrepArgs a;
+    ckda_status_t c = prep_args(a, q, k, q_weight, k_weight, positions, positions64, inv_freq, tokens, period, Hq, Hk, d,
+                                rotary, q_stride, k_stride, dt, norm, interleaved, eps, q_scale, rope_scale);
+    if (c != CKDA_OK) return c;
+    const bool weights = grad_q_weight || grad_k_weight;
+    if (tokens > 0 && (!grad_q_out || !grad_q || (Hk > 0 && (!grad_k_out || !grad_k)))) return CKDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {grad_q_out, grad_k_out, grad_q, grad_k, grad_q_weight, grad_k_weight, workspace};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return CKDA_ERR_MISALIGNED;
+    if (weights && tokens > 0 && (!workspace || workspace_bytes < ckda_qk_prep_bwd_workspace_bytes(d))) return CKDA_ERR_WORKSPACE;
+    cudaStream_t st = as_stream(stream);
+    if (tokens == 0) {
+        for (float* w : {grad_q_weight, grad_k_weight})
+            if (w && cudaMemsetAsync(w, 0, d * sizeof(float), st) != cudaSuccess) return CKDA_ERR_CUDA;
+        return CKDA_OK;
+    }
+    a.dy[0] = grad_q_out;
+    a.dy[1] = grad_k_out;
+    a.out[0] = grad_q;
+    a.out[1] = grad_k;
+    a.partial = weights ? static_cast<float*>(workspace) : nullptr;
+    int blocks = 0;
+    c = dt == CKDA_BF16 ? prep_launch<bf16, true>(a, dt, &blocks, st) : prep_launch<float, true>(a, dt, &blocks, st);
+    if (c != CKDA_OK || !weights) return c;
+    prep_weight_kernel<<<(unsigned)((2 * d + 31) / 32), 256, 0, st>>>(a.partial, blocks, d, grad_q_weight, grad_k_weight);
+    return launch_status();
+}
+
+ckda_status_t ckda_state_copy(float* S, const int* src, const int* dst, int pairs, int layers, int slots,
+                              long long state_floats, void* stream) {
+    if (pairs < 0 || layers < 0 || slots < 0 || state_floats < 0) return CKDA_ERR_INVALID_ARG;
+    if (pairs == 0 || layers == 0 || state_floats == 0) return CKDA_OK;
+    if (!src || !dst || !S || slots == 0) return CKDA_ERR_INVALID_ARG;
+    if (!aligned16(S) || !aligned4(src) || !aligned4(dst)) return CKDA_ERR_MISALIGNED;
+    if (pairs > kCopyMaxPairs || state_floats % 4 != 0 || layers > 65535) return CKDA_ERR_UNSUPPORTED;
+    const long long pieces = state_floats / 4;
+    // Slice: about 32 KB of states a CTA (several CTAs per SM overlap their reads and writes),
+    // narrower while that leaves SMs without work, 128 bytes at least.
+    int width = std::max(8, std::min(256, 2048 / pairs));
+    while (width > 8 && ((pieces + width - 1) / width) * layers < 2LL * sm_count()) width /= 2;
+    if (pieces < width) width = (int)pieces;
+    const long long slices = (pieces + width - 1) / width;
+    if (slices > 0x7fffffffLL) return CKDA_ERR_UNSUPPORTED;
+    const int table = copy_table(pairs);
+    const size_t smem = (size_t)pairs * width * 16 + (size_t)(2 * table + 2 * pairs) * sizeof(int);
+    if (smem > 48 * 1024 && allow_smem(state_copy_kernel, smem) != cudaSuccess) return CKDA_ERR_CUDA;
+    state_copy_kernel<<<dim3((unsigned)slices, (unsigned)layers), kCopyThreads, smem, as_stream(stream)>>>(
+        reinterpret_cast<uint4*>(S), src, dst, pairs, slots, pieces, width, table);
+    return launch_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,428 @@
+"""Binding of the scalar-gate operators (argument marshalling only; every step runs in CUDA).
+
+    gated_chunk_fwd(q, k, v, g, beta, S0=None)    -> (o, S_T)
+    gated_bwd(q, k, v, g, beta, grad_o, S0=None)  -> gradients
+    gated_decode_step(q, k, v, g, beta, S)        -> o   (states of a pool, in place)
+    qk_norm_rope(q, k) / qk_norm_rope_bwd(...)    -> queries and keys ready for the rule
+    state_copy(S, src, dst)                       -> S   (forks, moves and clears states)
+
+The rule, per sequence and value head, with one decay e^{g_t} per token:
+
+    S_t = e^{g_t} (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,   o_t = S_t^T q_t
+
+q and k have Hk heads, v, g, beta and the states Hv, a multiple of Hk. Dense tensors are
+[B, T, heads, d]; with cu_seqlens (int32 [N+1], device) they are packed, [total, heads, d].
+q, k and v may be slices of wider rows (heads and channels contiguous, one distance from token
+to token). The full conventions are in include/ckda.h.
+"""
+from __future__ import annotations
+
+from typing import Optional, Tuple
+
+import torch
+
+from ._lib import _check, _device, _dt, _ptr, _raise, _stream, load
+
+NORMS = {"none": 0, "l2": 1, "rms": 2}          # ckda_prep_norm_t
+LAYOUTS = {"half": 0, "interleaved": 1}
+MAX_COPY_PAIRS = 1024
+
+
+def _rows(t: torch.Tensor, name: str, lead: int, dtype, device) -> int:
+    """Checks a tensor of rows [..., heads, d] with `lead` leading token dimensions whose heads
+    and channels are contiguous; returns the distance from token to token in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {device}")
+    if t.dim() != lead + 2:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {lead + 2} dimensions")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    heads, d = t.shape[-2:]
+    inner = heads * d
+    st = t.stride()
+    if t.numel() == 0:
+        return max(inner, 1)
+    if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d):
+        raise ValueError(f"{name} must have contiguous heads and channels, has strides {st}")
+    row = None                                    # the distance between tokens, over every leading dimension
+    step = 1
+    for i in range(lead - 1, -1, -1):
+        if t.shape[i] > 1:
+            if row is None:
+                row = st[i] // step if st[i] % step == 0 else -1
+            if st[i] != row * step:
+                raise ValueError(f"{name} must have one distance from token to token, has strides {st}")
+        step *= t.shape[i]
+    row = max(inner, 1) if row is None else row
+    if row < inner:
+        raise ValueError(f"{name} has overlapping tokens, strides {st}")
+    return row
+
+
+def _int32(t: torch.Tensor, name: str, n: Optional[int], device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    _check(t, name, tuple(t.shape) if n is None else (n,), torch.int32, device)
+    if t.dim() != 1:
+        raise ValueError(f"{name} must have one dimension, has shape {tuple(t.shape)}")
+
+
+def _apart(out: Optional[torch.Tensor], name: str, others) -> None:
+    """An output that shares memory with an input (or another output) it must not share it with."""
+    if out is None or out.numel() == 0:
+        return
+    a0 = out.data_ptr()
+    a1 = a0 + out.numel() * out.element_size()
+    for other, t in others.items():
+        if t is None or t.numel() == 0:
+            continue
+        b0 = t.data_ptr()
+        b1 = b0 + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+        if a0 < b1 and b0 < a1:
+            raise ValueError(f"{name} overlaps {other}")
+
+
+class _Problem:
+    """The checked inputs of a gated delta rule call."""
+
+    def __init__(self, q, k, v, g, beta, S0, cu_seqlens):
+        dev = self.dev = _device(q)
+        packed = cu_seqlens is not None
+        lead = 1 if packed else 2
+        self.qs = _rows(q, "q", lead, None, dev)
+        dt = q.dtype
+        self.dt = _dt(q)
+        self.ks = _rows(k, "k", lead, dt, dev)
+        self.vs = _rows(v, "v", lead, dt, dev)
+        tokens = tuple(q.shape[:lead])
+        self.Hk, self.dk = q.shape[-2:]
+        self.Hv, self.dv = v.shape[-2:]
+        if tuple(k.shape) != tuple(q.shape):
+            raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(q.shape)}")
+        if tuple(v.shape[:lead]) != tokens:
+            raise ValueError(f"v has shape {tuple(v.shape)}, expected {tokens + (self.Hv, self.dv)}")
+        if self.Hk < 1 or self.Hv % max(self.Hk, 1) != 0 or self.Hv < 1:
+            raise ValueError(f"v has {self.Hv} heads, not a multiple of the {self.Hk} of q and k")
+        _check(g, "g", tokens + (self.Hv,), torch.float32, dev)
+        _check(beta, "beta", tokens + (self.Hv,), torch.float32, dev)
+        if packed:
+            _int32(cu_seqlens, "cu_seqlens", None, dev)
+            if cu_seqlens.numel() < 1:
+                raise ValueError("cu_seqlens must hold N + 1 offsets")
+            self.N, self.T, self.total = cu_seqlens.numel() - 1, 0, tokens[0]
+        else:
+            self.N, self.T = tokens
+            self.total = self.N * self.T
+        self.o_shape = tokens + (self.Hv, self.dv)
+        self.state_shape = (self.N, self.Hv, self.dk, self.dv)
+        if S0 is not None:
+            _check(S0, "S0", self.state_shape, torch.float32, dev)
+        self.inputs = {"q": q, "k": k, "v": v, "g": g, "beta": beta, "cu_seqlens": cu_seqlens}
+        self.sizes = (self.N, self.T, self.total, self.Hk, self.Hv, self.dk, self.dv, self.qs, self.ks, self.vs, self.dt)
+        self.ws_sizes = (self.N, self.total, self.Hk, self.Hv, self.dk, self.dv, self.dt)
+
+    def workspace(self, need: int, workspace):
+        if need and workspace is None:
+            workspace = torch.empty(need, device=self.dev, dtype=torch.uint8)
+        if workspace is not None:
+            _check(workspace, "workspace", tuple(workspace.shape), None, self.dev)
+        return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def gated_fwd_workspace_bytes(N, total, Hk, Hv, dk, dv, dtype=torch.bfloat16) -> int:
+    return int(load().ckda_gated_fwd_workspace_bytes(N, total, Hk, Hv, dk, dv, _dt(torch.empty(0, dtype=dtype))))
+
+
+def gated_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, o=None, S_T=None, want_state=True, workspace=None,
+                    stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """ckda_gated_fwd. Returns (o, S_T): o in v's type and shape (rows behind the last packed
+    sequence are not written), S_T [N, Hv, dk, dv] fp32, which may be S0 itself. Allocates o, S_T
+    and the workspace with torch when not given."""
+    p = _Problem(q, k, v, g, beta, S0, cu_seqlens)
+    if o is None:
+        o = torch.empty(p.o_shape, device=p.dev, dtype=v.dtype)
+    _check(o, "o", p.o_shape, v.dtype, p.dev)
+    if S_T is None and want_state:
+        S_T = torch.empty(p.state_shape, device=p.dev, dtype=torch.float32)
+    if S_T is not None:
+        _check(S_T, "S_T", p.state_shape, torch.float32, p.dev)
+        _apart(S_T, "S_T", {**p.inputs, "o": o})
+        if S0 is not None and S_T.data_ptr() != S0.data_ptr():
+            _apart(S_T, "S_T", {"S0": S0})
+    _apart(o, "o", {**p.inputs, "S0": S0})
+    lib = load()
+    with torch.cuda.device(p.dev):
+        workspace, wbytes = p.workspace(int(lib.ckda_gated_fwd_workspace_bytes(*p.ws_sizes)), workspace)
+        st = lib.ckda_gated_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(o), _ptr(S_T),
+                                _ptr(cu_seqlens), *p.sizes, _ptr(workspace), wbytes, _stream(stream, p.dev))
+    _raise(st, "ckda_gated_fwd")
+    return o, S_T
+
+
+def gated_bwd_workspace_bytes(N, total, Hk, Hv, dk, dv, dtype=torch.bfloat16) -> int:
+    return int(load().ckda_gated_bwd_workspace_bytes(N, total, Hk, Hv, dk, dv, _dt(torch.empty(0, dtype=dtype))))
+
+
+def gated_bwd(q, k, v, g, beta, grad_o, S0=None, grad_S_T=None, *, cu_seqlens=None, want_dS0=True, grads=None,
+              workspace=None, stream=None):
+    """ckda_gated_bwd: gradients of L = <grad_o, o> + <grad_S_T, S_T> for gated_chunk_fwd. Returns a
+    dict with dq, dk, dv (in q's type), dg, dbeta, dS0 (fp32; dS0 None unless want_dS0). Output
+    tensors may be passed in `grads` (same keys); dS0 may be grad_S_T itself."""
+    p = _Problem(q, k, v, g, beta, S0, cu_seqlens)
+    _check(grad_o, "grad_o", p.o_shape, v.dtype, p.dev)
+    if grad_S_T is not None:
+        _check(grad_S_T, "grad_S_T", p.state_shape, torch.float32, p.dev)
+    got = dict(grads or {})
+    f32 = torch.float32
+    shapes = {"dq": (tuple(q.shape), q.dtype), "dk": (tuple(q.shape), q.dtype), "dv": (p.o_shape, q.dtype),
+              "dg": (tuple(g.shape), f32), "dbeta": (tuple(g.shape), f32), "dS0": (p.state_shape, f32)}
+    for name, (shape, dtype) in shapes.items():
+        if name == "dS0" and not want_dS0:
+            got[name] = None
+            continue
+        if got.get(name) is None:
+            got[name] = torch.empty(shape, device=p.dev, dtype=dtype)
+        _check(got[name], name, shape, dtype, p.dev)
+    for i, name in enumerate(shapes):
+        others = {**p.inputs, "grad_o": grad_o, "S0": S0, "grad_S_T": grad_S_T}
+        others.update({n: got[n] for n in list(shapes)[:i]})
+        if name == "dS0" and got[name] is not None and grad_S_T is not None and got[name].data_ptr() == grad_S_T.data_ptr():
+            others.pop("grad_S_T")
+        _apart(got[name], name, others)
+    lib = load()
+    with torch.cuda.device(p.dev):
+        workspace, wbytes = p.workspace(int(lib.ckda_gated_bwd_workspace_bytes(*p.ws_sizes)), workspace)
+        st = lib.ckda_gated_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(grad_o), _ptr(grad_S_T),
+                                _ptr(got["dq"]), _ptr(got["dk"]), _ptr(got["dv"]), _ptr(got["dg"]), _ptr(got["dbeta"]),
+                                _ptr(got["dS0"]), _ptr(cu_seqlens), *p.sizes, _ptr(workspace), wbytes,
+                                _stream(stream, p.dev))
+    _raise(st, "ckda_gated_bwd")
+    return got
+
+
+def gated_decode_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None) -> torch.Tensor:
+    """ckda_gated_decode_step: one token of N sequences, q, k [N, Hk, dk], v [N, Hv, dv], g, beta
+    [N, Hv]. Updates states of the pool S [P, Hv, dk, dv] in place: row n's is S[slots[n]] (int32;
+    None: S[n]); rows with a negative slot are padding and keep their o. Returns o [N, Hv, dv]."""
+    dev = _device(q)
+    qs = _rows(q, "q", 1, None, dev)
+    dt = q.dtype
+    ks, vs = _rows(k, "k", 1, dt, dev), _rows(v, "v", 1, dt, dev)
+    N, Hk, dk = q.shape
+    Hv, dv = v.shape[-2:]
+    if tuple(k.shape) != tuple(q.shape):
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(q.shape)}")
+    if v.shape[0] != N:
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected {(N, Hv, dv)}")
+    if Hk < 1 or Hv < 1 or Hv % Hk != 0:
+        raise ValueError(f"v has {Hv} heads, not a multiple of the {Hk} of q and k")
+    _check(g, "g", (N, Hv), torch.float32, dev)
+    _check(beta, "beta", (N, Hv), torch.float32, dev)
+    if not isinstance(S, torch.Tensor) or S.dim() != 4:
+        raise ValueError("S must be a [pool, Hv, dk, dv] tensor")
+    _check(S, "S", (S.shape[0], Hv, dk, dv), torch.float32, dev)
+    if slots is None:
+        if S.shape[0] < N:
+            raise ValueError(f"S holds {S.shape[0]} states, the call has {N} rows")
+    else:
+        _int32(slots, "slots", N, dev)
+    if o is None:
+        o = torch.empty(N, Hv, dv, device=dev, dtype=dt)
+    _check(o, "o", (N, Hv, dv), dt, dev)
+    inputs = {"q": q, "k": k, "v": v, "g": g, "beta": beta, "slots": slots}
+    _apart(o, "o", {**inputs, "S": S})
+    _apart(S, "S", inputs)
+    with torch.cuda.device(dev):
+        st = load().ckda_gated_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), _ptr(o), _ptr(slots),
+                                           N, S.shape[0], Hk, Hv, dk, dv, qs, ks, vs, _dt(q), _stream(stream, dev))
+    _raise(st, "ckda_gated_decode_step")
+    return o
+
+
+class _Prep:
+    """The checked arguments that qk_norm_rope and its backward share."""
+
+    def __init__(self, q, k, positions, inv_freq, norm, layout, q_weight, k_weight, eps, q_scale, rope_scale):
+        dev = self.dev = _device(q)
+        if q.dim() < 3:
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected [..., heads, d]")
+        lead = q.dim() - 2
+        self.qs = _rows(q, "q", lead, None, dev)
+        self.dt = _dt(q)
+        self.tokens_shape = tuple(q.shape[:-2])
+        self.Hq, self.d = q.shape[-2:]
+        self.Hk, self.ks = 0, 0
+        if k is not None:
+            self.ks = _rows(k, "k", lead, q.dtype, dev)
+            if tuple(k.shape[:-2]) != self.tokens_shape or k.shape[-1] != self.d:
+                raise ValueError(f"k has shape {tuple(k.shape)}, expected {self.tokens_shape + (k.shape[-2], self.d)}")
+            self.Hk = k.shape[-2]
+        tokens = 1
+        for n in self.tokens_shape:
+            tokens *= n
+        if tokens > 0x7fffffff:
+            raise ValueError("more than 2**31 - 1 tokens")
+        if norm not in NORMS:
+            raise ValueError(f"norm must be one of {sorted(NORMS)}, got {norm!r}")
+        if layout not in LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                _check(w, name, (self.d,), torch.float32, dev)
+        rotary, pos64 = 0, 0
+        if inv_freq is not None:
+            if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
+                raise ValueError("inv_freq must be a tensor of one dimension")
+            _check(inv_freq, "inv_freq", tuple(inv_freq.shape), torch.float64, dev)
+            rotary = 2 * inv_freq.numel()
+            if rotary > self.d:
+                raise ValueError(f"inv_freq turns {rotary} channels, a head has {self.d}")
+        if positions is not None:
+            if inv_freq is None:
+                raise ValueError("positions without inv_freq")
+            if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+                raise TypeError("positions must be an int32 or int64 tensor")
+            _check(positions, "positions", self.tokens_shape, positions.dtype, dev)
+            pos64 = int(positions.dtype == torch.int64)
+        self.inputs = {"q": q, "k": k, "q_weight": q_weight, "k_weight": k_weight, "positions": positions,
+                       "inv_freq": inv_freq}
+        self.ptrs = (_ptr(q_weight), _ptr(k_weight), _ptr(positions), pos64, _ptr(inv_freq))
+        self.sizes = (tokens, max(1, self.tokens_shape[-1]), self.Hq, self.Hk, self.d, rotary, self.qs, self.ks, self.dt,
+                      NORMS[norm], LAYOUTS[layout], float(eps), float(q_scale), float(rope_scale))
+
+    def out(self, t, name, heads, like):
+        shape = self.tokens_shape + (heads, self.d)
+        if t is None:
+            t = torch.empty(shape, device=self.dev, dtype=like.dtype)
+        _check(t, name, shape, like.dtype, self.dev)
+        return t
+
+
+def qk_norm_rope(q, k=None, *, positions=None, inv_freq=None, norm="l2", layout="half", q_weight=None, k_weight=None,
+                 eps=1e-6, q_scale=1.0, rope_scale=1.0, q_out=None, k_out=None, stream=None):
+    """ckda_qk_prep: the norm of every head of q [..., Hq, d] and k [..., Hk, d], weights, and the
+    rotation of the first 2 * len(inv_freq) channels by the tokens' positions, in one pass.
+    norm: "l2", "rms" (with eps) or "none"; layout: pairs (p, p + R/2) ("half") or (2p, 2p + 1)
+    ("interleaved"). inv_freq is fp64 (see rope_frequencies); positions int32 or int64 of the
+    tokens' shape, None: the index along the last token dimension. Returns (q_out, k_out), which may
+    be q and k themselves where those are contiguous (k_out None without k)."""
+    p = _Prep(q, k, positions, inv_freq, norm, layout, q_weight, k_weight, eps, q_scale, rope_scale)
+    q_out = p.out(q_out, "q_out", p.Hq, q)
+    k_out = p.out(k_out, "k_out", p.Hk, k) if k is not None else None
+    for name, t, own in (("q_out", q_out, "q"), ("k_out", k_out, "k")):
+        if t is None:
+            continue
+        src = p.inputs[own]
+        same = t.data_ptr() == src.data_ptr() and src.is_contiguous()
+        _apart(t, name, {n: x for n, x in p.inputs.items() if not (same and n == own)})
+    _apart(k_out, "k_out", {"q_out": q_out})
+    with torch.cuda.device(p.dev):
+        st = load().ckda_qk_prep(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), *p.ptrs, *p.sizes, _stream(stream, p.dev))
+    _raise(st, "ckda_qk_prep")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q, k, grad_q, grad_k=None, *, positions=None, inv_freq=None, norm="l2", layout="half", q_weight=None,
+                     k_weight=None, eps=1e-6, q_scale=1.0, rope_scale=1.0, grads=None, workspace=None, stream=None):
+    """ckda_qk_prep_bwd: gradients of qk_norm_rope from those of its outputs. Returns a dict with dq,
+    dk (contiguous, in q's type) and dq_weight, dk_weight (fp32 [d]; None without that weight).
+    Output tensors may be passed in `grads` (same keys)."""
+    p = _Prep(q, k, positions, inv_freq, norm, layout, q_weight, k_weight, eps, q_scale, rope_scale)
+    _check(grad_q, "grad_q", p.tokens_shape + (p.Hq, p.d), q.dtype, p.dev)
+    if (k is None) != (grad_k is None):
+        raise ValueError("k and grad_k come together")
+    if k is not None:
+        _check(grad_k, "grad_k", p.tokens_shape + (p.Hk, p.d), q.dtype, p.dev)
+    got = dict(grads or {})
+    got["dq"] = p.out(got.get("dq"), "dq", p.Hq, q)
+    got["dk"] = p.out(got.get("dk"), "dk", p.Hk, k) if k is not None else None
+    for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
+        if w is None:
+            got[name] = None
+            continue
+        if got.get(name) is None:
+            got[name] = torch.empty(p.d, device=p.dev, dtype=torch.float32)
+        _check(got[name], name, (p.d,), torch.float32, p.dev)
+    names = ["dq", "dk", "dq_weight", "dk_weight"]
+    for i, name in enumerate(names):
+        _apart(got[name], name, {**p.inputs, "grad_q": grad_q, "grad_k": grad_k, **{n: got[n] for n in names[:i]}})
+    lib = load()
+    with torch.cuda.device(p.dev):
+        need = int(lib.ckda_qk_prep_bwd_workspace_bytes(p.d)) if got["dq_weight"] is not None or got["dk_weight"] is not None else 0
+        if need and workspace is None:
+            workspace = torch.empty(need, device=p.dev, dtype=torch.uint8)
+        if workspace is not None:
+            _check(workspace, "workspace", tuple(workspace.shape), None, p.dev)
+        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = lib.ckda_qk_prep_bwd(_ptr(q), _ptr(k), _ptr(grad_q), _ptr(grad_k), _ptr(got["dq"]), _ptr(got["dk"]),
+                                  _ptr(got["dq_weight"]), _ptr(got["dk_weight"]), *p.ptrs, *p.sizes, _ptr(workspace),
+                                  wbytes, _stream(stream, p.dev))
+    _raise(st, "ckda_qk_prep_bwd")
+    return got
+
+
+def rope_frequencies(rotary: int, base: float = 10000.0, *, factor: float = 1.0, scaling: str = "none",
+                     trained: int = 4096, slow: float = 1.0, fast: float = 32.0, device=None) -> Tuple[torch.Tensor, float]:
+    """(inv_freq, rope_scale) for qk_norm_rope: fp64 [rotary / 2] frequencies base^(-2p / rotary),
+    scaled for contexts `factor` times the `trained` length:
+      "none":    as they are;
+      "linear":  all divided by factor (positions interpolated);
+      "base":    base * factor^(rotary / (rotary - 2)), which leaves the fastest pair alone and
+                 divides the slowest by factor;
+      "by_parts": pairs that turn more than `fast` times in the trained length are left alone,
+                 those that turn less than `slow` times are divided by factor, between them a ramp
+                 in the pair index; rope_scale is then 0.1 ln(factor) + 1."""
+    import math
+    if rotary < 2 or rotary % 2 != 0:
+        raise ValueError(f"rotary must be even and at least 2, got {rotary}")
+    if not (base > 1.0 and factor >= 1.0 and trained >= 1 and 0 < slow < fast):
+        raise ValueError("need base > 1, factor >= 1, trained >= 1 and 0 < slow < fast")
+    p = torch.arange(0, rotary, 2, dtype=torch.float64) / rotary
+    scale = 1.0
+    if scaling == "none":
+        f = base ** -p
+    elif scaling == "linear":
+        f = base ** -p / factor
+    elif scaling == "base":
+        if rotary < 4:
+            raise ValueError("scaling by the base needs two pairs at least")
+        f = (base * factor ** (rotary / (rotary - 2))) ** -p
+    elif scaling == "by_parts":
+        def index(turns):                         # the (real) pair index that turns this often in `trained` tokens
+            return rotary * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rotary // 2 - 1)
+        ramp = ((torch.arange(rotary // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        f = base ** -p * (1 - ramp + ramp / factor)
+        scale = 0.1 * math.log(factor) + 1.0
+    else:
+        raise ValueError(f"scaling must be one of none, linear, base, by_parts, got {scaling!r}")
+    return f.to(device) if device is not None else f, scale
+
+
+def state_copy(S, src, dst, *, pool_dim=0, stream=None) -> torch.Tensor:
+    """ckda_state_copy, in place on a pool of states S [P, Hv, dk, dv] (pool_dim 0), or on every
+    layer's, S [L, P, Hv, dk, dv] (pool_dim 1): slot dst[i] takes the state of slot src[i] as it was
+    before the call, or zeros where src[i] is negative; a negative dst[i] names nothing; of pairs
+    with the same dst the last counts. src, dst: int32, at most 1024. Returns S."""
+    dev = _device(S, "S")
+    if pool_dim not in (0, 1) or S.dim() < pool_dim + 2:
+        raise ValueError(f"S has shape {tuple(S.shape)}, with the pool in dimension {pool_dim}")
+    _check(S, "S", tuple(S.shape), torch.float32, dev)
+    _int32(src, "src", None, dev)
+    _int32(dst, "dst", src.numel(), dev)
+    _apart(S, "S", {"src": src, "dst": dst})
+    layers = S.shape[0] if pool_dim else 1
+    slots = S.shape[pool_dim]
+    row = 1
+    for n in S.shape[pool_dim + 1:]:
+        row *= n
+    if slots == 0:
+        raise ValueError("S holds no states")
+    with torch.cuda.device(dev):
+        st = load().ckda_state_copy(_ptr(S), _ptr(src), _ptr(dst), src.numel(), layers, slots, row, _stream(stream, dev))
+    _raise(st, "ckda_state_copy")
+    return S

@@ -22,7 +22,7 @@
  *   device memory and keeps no per-call state; the only global state is one device
  *   error word per GPU (see ckda_get_device_error), kernel attributes cached per GPU,
  *   and the fixed scratch array of ckda_chunk_fwd_noalloc (part of the module's
- *   device image).
+ *   device image). The scalar-gate operators further down keep one error word more.
  * - Layout is contiguous row-major, head-interleaved:
  *       q, k, alpha : [B, T, H, d_k]     v, o : [B, T, H, d_v]     beta : [B, T, H]
  *       S0, S_T, S  : [B, H, d_k, d_v]   (d_v fastest)
@@ -64,7 +64,9 @@ typedef enum {
     CKDA_ERR_MISALIGNED = 3,    /* a base pointer is not 16-byte aligned             */
     CKDA_ERR_CUDA = 4,          /* a CUDA runtime call or launch failed              */
     CKDA_ERR_TIMEOUT = 5,       /* a device-side bounded wait ran out                */
-    CKDA_ERR_WORKSPACE = 6      /* workspace missing or smaller than required        */
+    CKDA_ERR_WORKSPACE = 6,     /* workspace missing or smaller than required        */
+    CKDA_ERR_INDEX = 7          /* an index read on the device was out of range or   */
+                                /* named twice (ckda_get_device_error only)          */
 } ckda_status_t;
 
 typedef enum {
@@ -347,11 +349,136 @@ CKDA_API ckda_status_t ckda_decode_step_ex(const void* q, const void* k, const v
                                float* S, float* o,
                                int N, int H, int dk, int dv, ckda_dtype_t dt, int mode, void* stream);
 
+/* ======================================================================================
+ * Scalar-gate operators: the gated delta rule with one decay per head, the preparation of
+ * its queries and keys, and copies of its states. They stand beside the calls above and
+ * differ from them in these conventions:
+ * - The gate is one number per token and head, g = ln(alpha) <= 0, fp32 (g = -inf, or any
+ *   g below -128, clears the state: e^-128 is 0 in fp32).
+ * - Value heads may share key heads: q and k have Hk heads, v, g, beta, o and the states Hv,
+ *   a multiple of Hk; value head h reads key head h / (Hv / Hk).
+ * - Tokens are one row each, [token][head][channel]. Dense calls (cu_seqlens NULL) hold N
+ *   sequences of T tokens, total = N * T. Packed calls hold sequence n in rows
+ *   cu_seqlens[n] .. cu_seqlens[n+1] - 1 (int32 [N+1], device memory; T is ignored), empty
+ *   sequences allowed; rows outside every sequence are neither read nor written.
+ * - q, k and v may be slices of wider rows: *_stride is the distance from token to token in
+ *   elements (at least heads * channels); heads and channels are contiguous. Every other
+ *   tensor is contiguous.
+ * - o, and every gradient, has the type of its tensor: bf16 with bf16 q, k, v; g, beta, the
+ *   states and their gradients are fp32.
+ * - g, beta, their gradients, positions, inv_freq and the indexes in device memory
+ *   (cu_seqlens, slots, src, dst) need their own type's alignment only. An index that is out of range or out of order is cut to the tensors or its work is
+ *   skipped, never followed, and ckda_get_device_error then returns CKDA_ERR_INDEX.
+ * - Results do not depend on the run: every sum has one order.
+ */
+
 /*
- * Synchronises `stream`, then reads and clears this GPU's device error word.
+ * Gated delta rule, all tokens of every sequence (prefill; training forward):
+ *     S_t = e^{g_t} (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T,   o_t = S_t^T q_t
+ *   q, k  [total][Hk][dk] dt   v [total][Hv][dv] dt   g, beta [total][Hv] fp32
+ *   S0    [N][Hv][dk][dv] fp32 or NULL (zero)         o [total][Hv][dv] dt, out
+ *   S_T   [N][Hv][dk][dv] fp32 out or NULL; may be S0 (an empty sequence copies S0)
+ *   workspace: ckda_gated_fwd_workspace_bytes(...) bytes (may be 0), owned by the caller; calls
+ *              that may run at once (streams, captured graphs) need one each.
+ * 1 <= dk, dv <= 128. o must not overlap an input.
+ */
+CKDA_API size_t ckda_gated_fwd_workspace_bytes(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt);
+CKDA_API ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                                      const float* S0, void* o, float* S_T, const int* cu_seqlens, int N, int T,
+                                      int total, int Hk, int Hv, int dk, int dv, long long q_stride,
+                                      long long k_stride, long long v_stride, ckda_dtype_t dt, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of ckda_gated_fwd for L = sum_t <grad_o_t, o_t> + <grad_S_T, S_T>.
+ *   grad_o [total][Hv][dv] dt     grad_S_T [N][Hv][dk][dv] fp32 or NULL (zero)
+ *   grad_q, grad_k [total][Hk][dk] dt out (summed over the value heads that share a key head)
+ *   grad_v [total][Hv][dv] dt out     grad_g, grad_beta [total][Hv] fp32 out
+ *   grad_S0 [N][Hv][dk][dv] fp32 out or NULL; may be grad_S_T
+ *   workspace: ckda_gated_bwd_workspace_bytes(...) bytes, as above.
+ * The forward is recomputed from its inputs; nothing of it need be kept.
+ */
+CKDA_API size_t ckda_gated_bwd_workspace_bytes(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt);
+CKDA_API ckda_status_t ckda_gated_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                                      const float* S0, const void* grad_o, const float* grad_S_T, void* grad_q,
+                                      void* grad_k, void* grad_v, float* grad_g, float* grad_beta, float* grad_S0,
+                                      const int* cu_seqlens, int N, int T, int total, int Hk, int Hv, int dk, int dv,
+                                      long long q_stride, long long k_stride, long long v_stride, ckda_dtype_t dt,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token of N independent sequences whose states lie in a pool, updated in place.
+ *   q, k [N][Hk][dk], v [N][Hv][dv] dt    g, beta [N][Hv] fp32    o [N][Hv][dv] dt out
+ *   S     [pool][Hv][dk][dv] fp32
+ *   slots [N] int32: row n's state, or NULL (row n has state n; pool >= N). A negative slot is
+ *         a padding row: its o is left as it was. Rows must name different slots: of rows that
+ *         name the same one the first is computed, the others are skipped and reported.
+ */
+CKDA_API ckda_status_t ckda_gated_decode_step(const void* q, const void* k, const void* v, const float* g,
+                                              const float* beta, float* S, void* o, const int* slots, int N, int pool,
+                                              int Hk, int Hv, int dk, int dv, long long q_stride, long long k_stride,
+                                              long long v_stride, ckda_dtype_t dt, void* stream);
+
+#define CKDA_PREP_MAX_D 256
+
+/* The norm of ckda_qk_prep. */
+typedef enum {
+    CKDA_PREP_NONE = 0,
+    CKDA_PREP_L2 = 1,           /* x / max(||x||_2, 1e-12), as CKDA_OPT_NORMALIZE_QK */
+    CKDA_PREP_RMS = 2           /* x / sqrt(mean(x^2) + eps)                         */
+} ckda_prep_norm_t;
+
+/*
+ * The layer step before the recurrence: norm of every head of q and k, per-channel weights,
+ * rotation by the token's position, in one pass.
+ *     y = s * Rot(w (.) norm(x)),   s = q_scale for q, 1 for k
+ * Rot turns pair p of the first `rotary` channels by positions[token] * inv_freq[p], times
+ * rope_scale in length; the other channels pass. Pairs are (p, p + rotary/2), or (2p, 2p + 1)
+ * with interleaved = 1. Angles are formed in 64 bits.
+ *   q, q_out [tokens][Hq][d], k, k_out [tokens][Hk][d] dt (Hk may be 0); outputs contiguous,
+ *            and each may be its own input where that is contiguous
+ *   q_weight, k_weight [d] fp32 or NULL (ones)
+ *   positions [tokens] int32 (int64 with positions64 = 1), or NULL: row index modulo `period`
+ *   inv_freq [rotary / 2] fp64 (may be NULL when rotary is 0)
+ * 1 <= d <= CKDA_PREP_MAX_D; rotary even, 0 <= rotary <= d.
+ */
+CKDA_API ckda_status_t ckda_qk_prep(const void* q, const void* k, void* q_out, void* k_out, const float* q_weight,
+                                    const float* k_weight, const void* positions, int positions64,
+                                    const double* inv_freq, int tokens, int period, int Hq, int Hk, int d, int rotary,
+                                    long long q_stride, long long k_stride, ckda_dtype_t dt, int norm, int interleaved,
+                                    float eps, float q_scale, float rope_scale, void* stream);
+
+/*
+ * Gradients of ckda_qk_prep from those of its outputs (contiguous).
+ *   grad_q, grad_k: contiguous, dt, out     grad_q_weight, grad_k_weight [d] fp32 out, or NULL
+ *   workspace: ckda_qk_prep_bwd_workspace_bytes(d) bytes when a weight's gradient is asked for.
+ */
+CKDA_API size_t ckda_qk_prep_bwd_workspace_bytes(int d);
+CKDA_API ckda_status_t ckda_qk_prep_bwd(const void* q, const void* k, const void* grad_q_out, const void* grad_k_out,
+                                        void* grad_q, void* grad_k, float* grad_q_weight, float* grad_k_weight,
+                                        const float* q_weight, const float* k_weight, const void* positions,
+                                        int positions64, const double* inv_freq, int tokens, int period, int Hq, int Hk,
+                                        int d, int rotary, long long q_stride, long long k_stride, ckda_dtype_t dt,
+                                        int norm, int interleaved, float eps, float q_scale, float rope_scale,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Copies of whole states within a pool, in every layer: slot dst[i] takes the state of slot
+ * src[i] as it was before the call (all reads come before all writes, so pairs may chain, swap
+ * or fork); a negative src[i] clears dst[i]; a negative dst[i] names nothing. Of pairs with the
+ * same dst the last one counts. A pair with an index beyond the pool is skipped and reported.
+ *   S [layers][slots][state_floats] fp32; src, dst [pairs] int32, pairs <= 1024
+ * state_floats must be a multiple of 4 (CKDA_ERR_UNSUPPORTED).
+ */
+CKDA_API ckda_status_t ckda_state_copy(float* S, const int* src, const int* dst, int pairs, int layers, int slots,
+                                       long long state_floats, void* stream);
+
+/*
+ * Synchronises `stream`, then reads and clears this GPU's device error words.
  * Returns CKDA_OK, CKDA_ERR_TIMEOUT (a bounded device wait ran out; the kernel
- * returned early and its outputs are invalid) or CKDA_ERR_CUDA (a sticky CUDA error;
- * the context is unusable).
+ * returned early and its outputs are invalid), CKDA_ERR_INDEX (a scalar-gate operator met an
+ * index that it did not follow; the other rows' results are valid) or CKDA_ERR_CUDA (a sticky
+ * CUDA error; the context is unusable).
  */
 CKDA_API ckda_status_t ckda_get_device_error(void* stream);
 

@@ -1,0 +1,464 @@
+"""The scalar-gate operators on the GPU against their fp64 definitions (oracle/gated.py)."""
+import pytest
+import torch
+
+from gated_util import make, near
+from oracle import gated as ref
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def ck():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from delta_rule_attention_ckda_b200 import build
+    build.build()
+    import delta_rule_attention_ckda_b200 as m
+    m.load()
+    assert m.get_device_error() == 0
+    return m
+
+
+def dev(*ts):
+    return [None if t is None else t.cuda() for t in ts]
+
+
+def fine(ck):
+    torch.cuda.synchronize()
+    assert ck.get_device_error() == 0
+
+
+# ------------------------------------------------------------------- the rule, in chunks
+
+DENSE = [  # B, T, Hk, Hv, dk, dv, dtype, S0
+    (1, 1, 1, 1, 128, 128, BF, True), (2, 63, 1, 2, 128, 128, BF, True), (1, 64, 2, 2, 64, 64, BF, False),
+    (1, 65, 1, 1, 128, 64, BF, True), (2, 200, 2, 4, 64, 128, BF, True), (1, 333, 3, 3, 128, 128, BF, False),
+    (1, 130, 1, 2, 96, 80, BF, True), (1, 70, 1, 1, 8, 16, BF, True), (2, 66, 1, 1, 24, 40, BF, True),
+    (1, 67, 1, 3, 17, 31, BF, True), (1, 50, 2, 4, 128, 128, F32, True), (2, 35, 1, 2, 33, 20, F32, False),
+    (1, 20, 1, 1, 1, 1, F32, True),
+]
+
+
+@pytest.mark.parametrize("case", DENSE, ids=str)
+def test_forward_dense(ck, case):
+    B, T, Hk, Hv, dk, dv, dt, s0 = case
+    q, k, v, g, b, S0, _, _ = make((B, T), Hk, Hv, dk, dv, dt, T, B, s0=s0)
+    o, ST = ck.gated_chunk_fwd(*dev(q, k, v, g, b, S0))
+    fine(ck)
+    assert o.dtype == dt and ST.dtype == F32
+    o_ref, S_ref = ref.gated_fwd(q, k, v, g, b, S0)
+    near("o", o, o_ref)
+    near("S_T", ST, S_ref)
+
+
+PACKED = [  # lengths, rows behind the last sequence, Hk, Hv, dk, dv, dtype
+    ([5], 0, 1, 1, 64, 64, BF), ([1, 64, 0, 65, 130], 7, 2, 4, 128, 128, BF), ([0, 0, 3], 1, 1, 2, 64, 128, BF),
+    ([63, 1, 1, 128, 2], 0, 1, 1, 128, 64, BF), ([9, 0, 17], 3, 1, 2, 20, 36, F32), ([200], 56, 1, 1, 40, 24, BF),
+]
+
+
+def packed(lens, tail):
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    return cu, sum(lens) + tail
+
+
+@pytest.mark.parametrize("case", PACKED, ids=str)
+def test_forward_packed(ck, case):
+    lens, tail, Hk, Hv, dk, dv, dt = case
+    cu, total = packed(lens, tail)
+    q, k, v, g, b, S0, _, _ = make((total,), Hk, Hv, dk, dv, dt, total, len(lens))
+    o = torch.full(v.shape, 7.0, dtype=dt).cuda()
+    dq, dk_, dv_, dg, db, dS = dev(q, k, v, g, b, S0)
+    _, ST = ck.gated_chunk_fwd(dq, dk_, dv_, dg, db, dS, cu_seqlens=cu.cuda(), o=o, S_T=dS)   # state in place
+    fine(ck)
+    o_ref, S_ref = ref.gated_fwd(q, k, v, g, b, S0, cu)
+    near("o", o[:sum(lens)], o_ref[:sum(lens)])
+    near("S_T", ST, S_ref)
+    assert (o[sum(lens):] == 7.0).all()
+
+
+@pytest.mark.parametrize("dt,d", [(BF, 128), (BF, 64), (F32, 32)])
+def test_forward_strided(ck, dt, d):
+    """q, k and v as slices of one projection's rows."""
+    B, T, Hk, Hv = 2, 100, 2, 4
+    q, k, v, g, b, S0, _, _ = make((B, T), Hk, Hv, d, d, dt, 3, B)
+    rows = torch.cat([t.flatten(2) for t in (q, v, k)], -1).cuda()
+    qs, vs, ks = rows.split([Hk * d, Hv * d, Hk * d], -1)
+    o, ST = ck.gated_chunk_fwd(qs.unflatten(-1, (Hk, d)), ks.unflatten(-1, (Hk, d)), vs.unflatten(-1, (Hv, d)), *dev(g, b, S0))
+    same, S2 = ck.gated_chunk_fwd(*dev(q, k, v, g, b, S0))
+    fine(ck)
+    assert torch.equal(o, same) and torch.equal(ST, S2)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_extreme_gates(ck, dt):
+    """Gates that clear the state (-inf, far below the floor), that leave it (0), steps of 0 and 2,
+    and repeated keys, whose updates cancel."""
+    T, d = 150, 64
+    q, k, v, g, b, S0, do, dST = make((1, T), 1, 2, d, d, dt, 5, 1)
+    g[0, 10], g[0, 64], g[0, 100] = float("-inf"), -1e30, -200.0
+    g[0, 20:40] = 0.0
+    b[0, 30:70:3], b[0, 31:70:3] = 0.0, 2.0
+    k[0, 110:140] = k[0, 110]
+    o, ST = ck.gated_chunk_fwd(*dev(q, k, v, g, b, S0))
+    fine(ck)
+    o_ref, S_ref = ref.gated_fwd(q, k, v, g, b, S0)
+    near("o", o, o_ref)
+    near("S_T", ST, S_ref)
+    got = ck.gated_bwd(*dev(q, k, v, g, b, do, S0, dST))
+    fine(ck)
+    want = ref.gated_bwd(q, k, v, g.clamp_min(-1e4), b, do, S0, dST)
+    for n in want:
+        near(n, got[n], want[n])
+
+
+@pytest.mark.parametrize("case", DENSE, ids=str)
+def test_backward_dense(ck, case):
+    B, T, Hk, Hv, dk, dv, dt, s0 = case
+    q, k, v, g, b, S0, do, dST = make((B, T), Hk, Hv, dk, dv, dt, T + 1, B, s0=s0)
+    dST = dST if s0 else None
+    got = ck.gated_bwd(*dev(q, k, v, g, b, do, S0, dST))
+    fine(ck)
+    want = ref.gated_bwd(q, k, v, g, b, do, S0, dST)
+    for n in want:
+        near(n, got[n], want[n])
+
+
+@pytest.mark.parametrize("case", PACKED, ids=str)
+def test_backward_packed(ck, case):
+    lens, tail, Hk, Hv, dk, dv, dt = case
+    cu, total = packed(lens, tail)
+    q, k, v, g, b, S0, do, dST = make((total,), Hk, Hv, dk, dv, dt, total, len(lens))
+    x = dev(q, k, v, g, b, do, S0, dST)
+    grads = {"dq": torch.full_like(x[0], 7.0), "dk": torch.full_like(x[1], 7.0), "dv": torch.full_like(x[2], 7.0),
+             "dg": torch.full_like(x[3], 7.0), "dbeta": torch.full_like(x[4], 7.0), "dS0": x[7]}   # in place of grad_S_T
+    got = ck.gated_bwd(*x, cu_seqlens=cu.cuda(), grads=grads)
+    fine(ck)
+    want = ref.gated_bwd(q, k, v, g, b, do, S0, dST, cu)
+    n = sum(lens)
+    for name in want:
+        if name == "dS0":
+            near(name, got[name], want[name])
+        else:
+            near(name, got[name][:n], want[name][:n])
+            assert (got[name][n:] == 7.0).all(), name
+
+
+def test_backward_by_differences(ck):
+    """The fp32 gradients against central differences of the forward (fp32, steps of 2^-6: the
+    rule is at most cubic in one input's entries here, differences are off by the third
+    derivative times h^2 / 6 and by 2^-24 |L| / h)."""
+    T, d = 9, 8
+    q, k, v, g, b, S0, do, dST = make((1, T), 1, 2, d, d, F32, 4, 1)
+    x = dict(zip("qkvgbS", dev(q, k, v, g, b, S0)))
+    do, dST = dev(do, dST)
+
+    def loss(**new):
+        y = {**x, **new}
+        o, ST = ck.gated_chunk_fwd(y["q"], y["k"], y["v"], y["g"], y["b"], y["S"])
+        return float((o.double() * do.double()).sum() + (ST.double() * dST.double()).sum())
+
+    got = ck.gated_bwd(x["q"], x["k"], x["v"], x["g"], x["b"], do, x["S"], dST)
+    h = 2.0 ** -6
+    gen = torch.Generator().manual_seed(1)
+    for name, grad in (("q", "dq"), ("k", "dk"), ("v", "dv"), ("g", "dg"), ("b", "dbeta"), ("S", "dS0")):
+        way = torch.randn(x[name].shape, generator=gen).cuda()
+        way /= way.norm()
+        slope = (loss(**{name: x[name] + h * way}) - loss(**{name: x[name] - h * way})) / (2 * h)
+        want = float((got[grad].double() * way.double()).sum())
+        assert abs(slope - want) <= 1e-3 * float(got[grad].double().norm()) + 1e-3, (name, slope, want)
+
+
+def test_long_packed_offsets(ck):
+    """A chunk boundary on every kind of place: lengths 1 .. 140 packed, each against its own dense call."""
+    lens = list(range(1, 141, 7)) + [64, 128]
+    cu, total = packed(lens, 0)
+    q, k, v, g, b, S0, do, dST = dev(*make((total,), 1, 2, 64, 128, BF, 8, len(lens)))
+    o, ST = ck.gated_chunk_fwd(q, k, v, g, b, S0, cu_seqlens=cu.cuda())
+    got = ck.gated_bwd(q, k, v, g, b, do, S0, dST, cu_seqlens=cu.cuda())
+    for n, (a, e) in enumerate(ref.bounds(cu)):
+        one = [t[a:e][None].contiguous() for t in (q, k, v, g, b)]
+        o1, S1 = ck.gated_chunk_fwd(*one, S0[n:n + 1].contiguous())
+        g1 = ck.gated_bwd(*one, do[a:e][None].contiguous(), S0[n:n + 1].contiguous(), dST[n:n + 1].contiguous())
+        assert torch.equal(o1[0], o[a:e]) and torch.equal(S1[0], ST[n])
+        for name in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert torch.equal(g1[name][0], got[name][a:e]), (n, name)
+        assert torch.equal(g1["dS0"][0], got["dS0"][n])
+    fine(ck)
+
+
+def test_bad_offsets_are_reported(ck):
+    """Offsets beyond the tensors, negative or out of order are cut and reported, never followed."""
+    q, k, v, g, b, S0, do, dST = dev(*make((100,), 1, 1, 64, 64, BF, 2, 2))
+    for cu in ([0, 60, 300], [-5, 50, 100], [0, 70, 30]):
+        cu = torch.tensor(cu, dtype=torch.int32).cuda()
+        ck.gated_chunk_fwd(q, k, v, g, b, S0, cu_seqlens=cu)
+        assert ck.get_device_error() == 7
+        ck.gated_bwd(q, k, v, g, b, do, S0, dST, cu_seqlens=cu)
+        assert ck.get_device_error() == 7
+    fine(ck)
+
+
+# ------------------------------------------------------------------- single tokens
+
+@pytest.mark.parametrize("case", [(1, 1, 1, 1, 128, 128, BF), (3, 7, 2, 4, 128, 128, BF), (40, 40, 4, 8, 64, 64, BF),
+                                  (5, 9, 1, 2, 128, 96, BF), (6, 6, 2, 2, 64, 128, F32), (4, 6, 1, 1, 20, 12, F32),
+                                  (200, 210, 2, 4, 128, 128, BF), (4, 5, 1, 2, 48, 64, BF)], ids=str)
+def test_decode(ck, case):
+    N, P, Hk, Hv, dk, dv, dt = case
+    q, k, v, g, b, _, _, _ = make((N,), Hk, Hv, dk, dv, dt, N, N)
+    gen = torch.Generator().manual_seed(N)
+    S = torch.randn(P, Hv, dk, dv, generator=gen)
+    slots = torch.randperm(P, generator=gen)[:N].to(torch.int32)
+    if N > 2:
+        slots[1] = -1
+    dS = S.cuda()
+    o = torch.full((N, Hv, dv), 7.0, dtype=dt).cuda()
+    ck.gated_decode_step(*dev(q, k, v, g, b), dS, slots=slots.cuda(), o=o)
+    fine(ck)
+    rows = [n for n in range(N) if slots[n] >= 0]
+    used = slots[rows].long()
+    o_ref, S_ref = ref.gated_fwd(*(t[rows][:, None] for t in (q, k, v, g, b)), S[used])
+    near("o", o[rows], o_ref[:, 0])
+    near("S", dS[used.cuda()], S_ref)
+    rest = torch.ones(P, dtype=torch.bool)
+    rest[used] = False
+    assert torch.equal(dS.cpu()[rest], S[rest])
+    if N > 2:
+        assert (o[1] == 7.0).all()
+
+
+@pytest.mark.parametrize("d", [128, 20])
+def test_decode_bad_slots(ck, d):
+    """A slot beyond the pool and a slot named twice: skipped, reported, the other rows computed."""
+    q, k, v, g, b, S0, _, _ = make((5,), 1, 1, d, d, F32, 9, 4)
+    S = S0.cuda()
+    o = torch.full((5, 1, d), 7.0).cuda()
+    ck.gated_decode_step(*dev(q, k, v, g, b), S, slots=torch.tensor([2, 4, 2, 0, 1 << 30], dtype=torch.int32).cuda(), o=o)
+    assert ck.get_device_error() == 7
+    fine(ck)
+    o_ref, S_ref = ref.gated_fwd(*(t[[0, 3]][:, None] for t in (q, k, v, g, b)), S0[[2, 0]])
+    near("o", o[[0, 3]], o_ref[:, 0])
+    near("S", S[[2, 0]], S_ref)
+    assert torch.equal(S.cpu()[[1, 3]], S0[[1, 3]]) and (o[[1, 2, 4]] == 7.0).all()
+
+
+# ------------------------------------------------------------------- queries and keys
+
+PREP = [  # tokens, Hq, Hk, d, rotary, norm, layout, weights, dtype
+    (1, 1, 1, 128, 128, "l2", "half", False, BF), (7, 16, 4, 128, 64, "rms", "interleaved", True, BF),
+    (65, 3, 5, 64, 32, "l2", "half", True, BF), (33, 2, 1, 256, 256, "rms", "half", True, BF),
+    (20, 4, 2, 96, 24, "rms", "half", True, BF), (21, 4, 2, 96, 24, "none", "interleaved", False, BF),
+    (5, 2, 2, 37, 10, "l2", "half", True, F32), (9, 1, 1, 1, 0, "rms", "half", True, F32),
+    (40, 2, 2, 64, 0, "l2", "half", False, F32), (300, 8, 2, 128, 128, "none", "half", True, BF),
+    (1000, 4, 4, 64, 16, "rms", "interleaved", True, F32), (17, 2, 0, 128, 32, "l2", "interleaved", False, BF),
+]
+
+
+def prep_inputs(case):
+    t, Hq, Hk, d, r, norm, layout, weights, dt = case
+    gen = torch.Generator().manual_seed(t)
+    rand = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    q, k = (rand(t, Hq, d) * 2).to(dt), (rand(t, Hk, d) * 2).to(dt) if Hk else None
+    q[0, 0] = 0                                            # a row whose norm is at its floor
+    pos = torch.randint(0, 1 << 20, (t,), generator=gen)
+    w = (1 + 0.2 * rand(d), 1 + 0.2 * rand(d) if Hk else None) if weights else (None, None)
+    f = 10000.0 ** (-torch.arange(0, r, 2, dtype=torch.float64) / max(r, 1)) if r else None
+    dy = rand(t, Hq, d).to(dt), rand(t, Hk, d).to(dt) if Hk else None
+    return q, k, pos, f, w, dy
+
+
+def prep_near(name, got, want):
+    """One rounding to the output's type after fp32 arithmetic (angles reduced in fp64, so a turned
+    value is off by a few 2^-24 of its pair): half a step and 16 * 2^-24 of the row's largest."""
+    g, w = got.double().cpu(), want.detach().double()
+    tol = torch.finfo(got.dtype).eps / 2 * w.abs() + 16 * 2.0 ** -24 * w.abs().amax(-1, keepdim=True)
+    assert ((g - w).abs() <= tol).all(), f"{name}: {float(((g - w).abs() - tol).max()):.3e}"
+
+
+@pytest.mark.parametrize("case", PREP, ids=str)
+def test_prep(ck, case):
+    t, Hq, Hk, d, r, norm, layout, weights, dt = case
+    q, k, pos, f, w, dy = prep_inputs(case)
+    how = dict(norm=norm, layout=layout)
+    outs = ck.qk_norm_rope(*dev(q, k), positions=pos.cuda() if r else None, inv_freq=dev(f)[0], q_weight=dev(w[0])[0],
+                           k_weight=dev(w[1])[0], q_scale=0.5, rope_scale=1.25, **how)
+    again = ck.qk_norm_rope(*dev(q, k), positions=pos.to(torch.int32).cuda() if r else None, inv_freq=dev(f)[0],
+                            q_weight=dev(w[0])[0], k_weight=dev(w[1])[0], q_scale=0.5, rope_scale=1.25, **how)
+    fine(ck)
+    for n, x, got, two, wt, s in (("q", q, outs[0], again[0], w[0], 0.5), ("k", k, outs[1], again[1], w[1], 1.0)):
+        if x is None:
+            assert got is None
+            continue
+        want = ref.prep(x.double(), pos, f, weight=None if wt is None else wt.double(), scale=s, rope_scale=1.25, **how)
+        prep_near(n, got, want)
+        assert torch.equal(got, two)
+
+
+@pytest.mark.parametrize("case", PREP, ids=str)
+def test_prep_backward(ck, case):
+    t, Hq, Hk, d, r, norm, layout, weights, dt = case
+    q, k, pos, f, w, dy = prep_inputs(case)
+    q[0, 0] = q[0, -1] + 1                                # a zero row under the L2 norm has a gradient of 1e12 times dy
+    how = dict(norm=norm, layout=layout)
+    got = ck.qk_norm_rope_bwd(*dev(q, k, *dy), positions=pos.cuda() if r else None, inv_freq=dev(f)[0],
+                              q_weight=dev(w[0])[0], k_weight=dev(w[1])[0], q_scale=0.5, rope_scale=1.25, **how)
+    fine(ck)
+    for n, x, wt, g, s in (("q", q, w[0], dy[0], 0.5), ("k", k, w[1], dy[1], 1.0)):
+        if x is None:
+            continue
+        x64 = x.double().requires_grad_()
+        w64 = None if wt is None else wt.double().requires_grad_()
+        y = ref.prep(x64, pos, f, weight=w64, scale=s, rope_scale=1.25, **how)
+        dx, *dw = torch.autograd.grad(y, [x64] + ([] if wt is None else [w64]), g.double())
+        a = got["d" + n].double().cpu()
+        # dx = r (dxh - xh <dxh, xh> c): one rounding of the result, and each of the two terms, of
+        # the size of r |dxh|, is off by a few
+        # 2^-24 of itself, which stays where the terms cancel (with d = 1 they cancel wholly):
+        # 2^-18 of the row's largest r |dxh| covers both
+        xs = x.double()
+        r = {"l2": 1 / xs.norm(dim=-1, keepdim=True), "rms": (xs.square().mean(-1, keepdim=True) + 1e-6).rsqrt(),
+             "none": torch.ones(1, dtype=torch.float64)}[norm]
+        xn = (xs * r).requires_grad_()
+        yn = ref.prep(xn, pos, f, norm="none", layout=layout, weight=None if wt is None else wt.double(), scale=s, rope_scale=1.25)
+        big = (r * torch.autograd.grad(yn, xn, g.double())[0]).abs().amax(-1, keepdim=True)
+        tol = torch.finfo(x.dtype).eps / 2 * dx.abs() + 2.0 ** -18 * big
+        assert ((a - dx).abs() <= tol).all(), (n, float(((a - dx).abs() - tol).max()))
+        if dw:
+            near("d" + n + "_weight", got["d" + n + "_weight"], dw[0])
+        else:
+            assert got["d" + n + "_weight"] is None
+
+
+def test_prep_strided_in_place_and_default_positions(ck):
+    B, T, Hq, Hk, d = 2, 50, 4, 2, 64
+    gen = torch.Generator().manual_seed(0)
+    rows = torch.randn(B, T, (Hq + 2 * Hk) * d, generator=gen).to(BF).cuda()
+    q, k = rows[..., :Hq * d].unflatten(-1, (Hq, d)), rows[..., Hq * d:(Hq + Hk) * d].unflatten(-1, (Hk, d))
+    f, scale = ck.rope_frequencies(32, factor=8.0, scaling="by_parts", device="cuda")
+    pos = torch.arange(T, device="cuda").expand(B, T).contiguous()
+    a = ck.qk_norm_rope(q, k, positions=pos, inv_freq=f, rope_scale=scale)
+    b = ck.qk_norm_rope(q, k, inv_freq=f, rope_scale=scale)              # None: the index in the sequence
+    c = [q.contiguous(), k.contiguous()]
+    ck.qk_norm_rope(*c, positions=pos, inv_freq=f, rope_scale=scale, q_out=c[0], k_out=c[1])
+    odd = torch.randn(3, 2, 37, generator=gen).cuda()
+    o1, _ = ck.qk_norm_rope(odd, norm="rms")
+    ck.qk_norm_rope(odd, norm="rms", q_out=odd)
+    fine(ck)
+    for x, y, z in zip(a, b, c):
+        assert torch.equal(x, y) and torch.equal(x, z)
+    assert torch.equal(o1, odd)
+
+
+# ------------------------------------------------------------------- copies of states
+
+@pytest.mark.parametrize("case", [(1, 5, (2, 8, 16)), (3, 40, (1, 64, 64)), (2, 9, (1, 4, 1)), (1, 1, (1, 20, 12))], ids=str)
+@pytest.mark.parametrize("pairs", [1, 7, 300])
+def test_state_copy(ck, case, pairs):
+    """Random pairs: forks, chains, cycles, cleared slots, pairs that name nothing, destinations
+    named more than once (the last pair counts)."""
+    L, P, shape = case
+    gen = torch.Generator().manual_seed(pairs)
+    S = torch.randn(L, P, *shape, generator=gen)
+    src = torch.randint(-1, P, (pairs,), generator=gen, dtype=torch.int32)
+    dst = torch.randint(-1, P, (pairs,), generator=gen, dtype=torch.int32)
+    got = ck.state_copy(S.cuda(), src.cuda(), dst.cuda(), pool_dim=1)
+    fine(ck)
+    assert torch.equal(got.cpu(), ref.copy(S, src, dst))
+
+
+def test_state_copy_swap_and_bad_pairs(ck):
+    S = torch.randn(6, 2, 128, 128)
+    src, dst = torch.tensor([0, 1, 9, 3], dtype=torch.int32), torch.tensor([1, 0, 2, 1 << 30], dtype=torch.int32)
+    got = ck.state_copy(S.cuda(), src.cuda(), dst.cuda())
+    assert ck.get_device_error() == 7
+    assert torch.equal(got.cpu(), S[[1, 0, 2, 3, 4, 5]])
+    fine(ck)
+
+
+# ------------------------------------------------------------------- together
+
+def test_layer_run_together(ck):
+    """As a server uses them: prepare, prefill into states, fork one sequence, decode on the pool;
+    the whole against the rule token by token on the prepared (rounded) queries and keys."""
+    lens, H, d = [70, 5], 2, 64
+    cu, total = packed(lens, 0)
+    gen = torch.Generator().manual_seed(3)
+    raw_q, raw_k, v = (torch.randn(total + 4, H, d, generator=gen).to(BF) for _ in range(3))
+    g, b = -torch.rand(total + 4, H, generator=gen), torch.rand(total + 4, H, generator=gen) * 2
+    pos = torch.cat([torch.arange(n) for n in lens] + [torch.tensor([70, 5, 70, 70])]).int()
+    f, _ = ck.rope_frequencies(32, device="cuda")
+    q, k = ck.qk_norm_rope(*dev(raw_q, raw_k), positions=pos.cuda(), inv_freq=f, q_scale=d ** -0.5)
+    dv, dg, db = dev(v, g, b)
+    pool = torch.randn(6, H, d, d).cuda()
+    states = torch.zeros(2, H, d, d).cuda()
+    o, _ = ck.gated_chunk_fwd(q[:total], k[:total], dv[:total], dg[:total], db[:total], states, cu_seqlens=cu.cuda(), S_T=states)
+    pool[3], pool[1] = states[0], states[1]
+    ck.state_copy(pool, torch.tensor([3, 3], dtype=torch.int32).cuda(), torch.tensor([0, 5], dtype=torch.int32).cuda())
+    slots = torch.tensor([3, 1, 0, 5], dtype=torch.int32).cuda()
+    od = ck.gated_decode_step(q[total:], k[total:], dv[total:], dg[total:], db[total:], pool, slots=slots)
+    fine(ck)
+    x = [t.cpu() for t in (q, k)] + [v, g, b]
+    o_ref, S_ref = ref.gated_fwd(*(t[:total] for t in x), None, cu)
+    near("o", o, o_ref)
+    od_ref, _ = ref.gated_fwd(*(t[total:][:, None] for t in x), S_ref[[0, 1, 0, 0]])
+    near("decode", od, od_ref[:, 0])
+
+
+def test_graph_streams_and_two_calls(ck):
+    """Captured and replayed, on a stream of its own, and two calls at once with a workspace each."""
+    q, k, v, g, b, S0, do, dST = dev(*make((2, 200), 2, 2, 128, 128, BF, 6, 2))
+    o0, S_0 = ck.gated_chunk_fwd(q, k, v, g, b, S0)
+    g0 = ck.gated_bwd(q, k, v, g, b, do, S0, dST)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o1, S_1 = ck.gated_chunk_fwd(q, k, v, g, b, S0)
+        g1 = ck.gated_bwd(q, k, v, g, b, do, S0, dST)
+    for t in (o1, S_1, *g1.values()):
+        t.zero_()
+    for _ in range(2):
+        graph.replay()
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    both = []
+    for s in side:
+        with torch.cuda.stream(s):
+            both.append((ck.gated_chunk_fwd(q, k, v, g, b, S0), ck.gated_bwd(q, k, v, g, b, do, S0, dST)))
+    fine(ck)
+    for (o, S), gr in [((o1, S_1), g1)] + both:
+        assert torch.equal(o, o0) and torch.equal(S, S_0)
+        for n in g0:
+            assert torch.equal(gr[n], g0[n]), n
+
+
+def test_same_result_every_run(ck):
+    cu, total = packed([700, 3, 260], 0)
+    q, k, v, g, b, S0, do, dST = dev(*make((total,), 1, 4, 128, 128, BF, 6, 3))
+    runs = [(ck.gated_chunk_fwd(q, k, v, g, b, S0, cu_seqlens=cu.cuda()),
+             ck.gated_bwd(q, k, v, g, b, do, S0, dST, cu_seqlens=cu.cuda())) for _ in range(3)]
+    fine(ck)
+    for (o, S), gr in runs[1:]:
+        assert torch.equal(o, runs[0][0][0]) and torch.equal(S, runs[0][0][1])
+        assert all(torch.equal(gr[n], runs[0][1][n]) for n in gr)
+
+
+def test_empty(ck):
+    z = lambda *s, dt=F32: torch.empty(*s, dtype=dt, device="cuda")  # noqa: E731
+    S0 = torch.randn(2, 2, 16, 16).cuda()
+    o, ST = ck.gated_chunk_fwd(z(2, 0, 1, 16), z(2, 0, 1, 16), z(2, 0, 2, 16), z(2, 0, 2), z(2, 0, 2), S0)
+    assert torch.equal(ST, S0) and o.shape == (2, 0, 2, 16)
+    got = ck.gated_bwd(z(2, 0, 1, 16), z(2, 0, 1, 16), z(2, 0, 2, 16), z(2, 0, 2), z(2, 0, 2), z(2, 0, 2, 16), S0, S0 + 1)
+    assert torch.equal(got["dS0"], S0 + 1)
+    cu = torch.zeros(1, dtype=torch.int32).cuda()
+    ck.gated_chunk_fwd(z(0, 1, 16), z(0, 1, 16), z(0, 1, 16), z(0, 1), z(0, 1), cu_seqlens=cu)
+    ck.gated_decode_step(z(0, 1, 16), z(0, 1, 16), z(0, 1, 16), z(0, 1), z(0, 1), z(3, 1, 16, 16))
+    ck.qk_norm_rope(z(0, 1, 16), z(0, 1, 16))
+    w = torch.ones(16).cuda()
+    got = ck.qk_norm_rope_bwd(z(0, 1, 16), z(0, 1, 16), z(0, 1, 16), z(0, 1, 16), q_weight=w)
+    assert (got["dq_weight"] == 0).all()
+    e = torch.empty(0, dtype=torch.int32).cuda()
+    assert ck.state_copy(S0, e, e) is S0
+    fine(ck)
