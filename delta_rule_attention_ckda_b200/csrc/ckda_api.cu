@@ -457,7 +457,7 @@ ckda_status_t ckda_get_device_error(void* stream) {
         return CKDA_ERR_CUDA;
     unsigned int gated = 0;
     if (ckda_gated_take_error(&gated) != cudaSuccess) return CKDA_ERR_CUDA;
-    if (word & ckda::kErrTimeout) return CKDA_ERR_TIMEOUT;
+    if ((word | gated) & ckda::kErrTimeout) return CKDA_ERR_TIMEOUT;
     return gated != 0 ? CKDA_ERR_INDEX : CKDA_OK;
 }
 

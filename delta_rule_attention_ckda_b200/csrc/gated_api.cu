@@ -14,6 +14,10 @@
 #include "kernels/gated_common.cuh"
 #include "kernels/gated_simt.cuh"
 #include "kernels/gated_decode.cuh"
+#include "kernels/gated_intra.cuh"
+#include "kernels/gated_chain.cuh"
+#include "kernels/gated_grads.cuh"
+#include "kernels/tc_host.cuh"
 #include "kernels/qk_prep.cuh"
 #include "kernels/state_copy.cuh"
 
@@ -122,6 +126,147 @@ ckda_status_t simt_bwd(const Shape& s, const void* q, const void* k, const void*
     return launch_status();
 }
 
+// ---------------------------------------------------------------- the chunked kernels
+
+// They take bf16 with heads of a multiple of 8 channels (16-byte rows); channels are padded to
+// 64 or 128 in shared memory.
+bool chunked(const Shape& s) { return s.dt == CKDA_BF16 && s.dk % 8 == 0 && s.dv % 8 == 0; }
+bool chunked(const Shape& s, long long qs, long long ks, long long vs) {
+    return chunked(s) && qs % 8 == 0 && ks % 8 == 0 && vs % 8 == 0;
+}
+
+struct ChunkLayout {
+    size_t zhi, zlo, phi, plo, vec, shi, slo, dshi, u, w, parts, total;
+};
+ChunkLayout chunk_layout(const Shape& s, bool back) {
+    ChunkLayout l{};
+    const size_t n = Seqs::slots(s.N, s.total) * s.Hv, strips = (s.dv + 31) / 32;
+    size_t at = 0;
+    auto take = [&](size_t each) {
+        const size_t here = at;
+        at = up256(at + n * each);
+        return here;
+    };
+    l.zhi = take(8192);
+    l.zlo = take(8192);
+    l.phi = take(8192);
+    l.plo = take(8192);
+    l.vec = take(VEC * 4);
+    if (back) {
+        l.shi = take((size_t)s.dk * s.dv * 2);
+        l.slo = take((size_t)s.dk * s.dv * 2);
+        l.dshi = take((size_t)s.dk * s.dv * 2);
+        l.u = take((size_t)64 * s.dv * 2);
+        l.w = take((size_t)s.dv * 64 * 4);
+        l.parts = take(strips * PARTS * 4);
+    }
+    l.total = at;
+    return l;
+}
+ChunkWs chunk_ws(const ChunkLayout& l, void* base) {
+    char* b = static_cast<char*>(base);
+    auto H = [&](size_t at) { return reinterpret_cast<bf16*>(b + at); };
+    auto F = [&](size_t at) { return reinterpret_cast<float*>(b + at); };
+    return ChunkWs{H(l.zhi), H(l.zlo), H(l.phi), H(l.plo), F(l.vec), H(l.shi), H(l.slo), H(l.dshi), H(l.u), F(l.w), F(l.parts)};
+}
+
+struct Call {
+    Shape s;
+    Seqs seqs;
+    const bf16 *q, *k, *v, *grad_o;
+    const float *g, *beta, *S0, *dST;
+    bf16 *o, *gq, *gk, *gv;
+    float *ST, *gg, *gb, *gS0;
+    long long qs, ks, vs;
+    ChunkWs ws;
+    cudaStream_t st;
+};
+
+template <int DK>
+cudaError_t run_intra(const Call& c) {
+    constexpr size_t smem = intra_smem(DK);
+    cudaError_t e = allow_smem(intra_kernel<DK>, smem);
+    if (e != cudaSuccess) return e;
+    intra_kernel<DK><<<dim3((unsigned)Seqs::slots(c.s.N, c.s.total), (unsigned)c.s.Hk), 128, smem, c.st>>>(
+        c.q, c.k, c.g, c.beta, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.qs, c.ks);
+    return cudaPeekAtLastError();
+}
+
+// Tensor map over [tokens][heads][channels] rows a token stride apart, boxes of 64 channels of one
+// head of 64 tokens, 128-byte swizzle; channels beyond the head read as zeros.
+bool rows_map(CUtensorMap* map, const bf16* base, long long tokens, int heads, int d, long long stride) {
+    auto fn = ckda::tc::encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64u, 1u, 64u}, each[3] = {1u, 1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16*>(base), dims, strides, box, each,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+    CUtensorMap q, k, v, o;
+};
+
+// The chain kernels move registers between warps: the split adds up only against the register
+// count they were compiled to.
+template <typename K>
+cudaError_t chain_ready(K kernel, size_t smem) {
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kernel));
+    if (e != cudaSuccess) return e;
+    if (a.numRegs != kRegLaunch) return cudaErrorInvalidConfiguration;
+    return allow_smem(kernel, smem);
+}
+
+template <int DK, bool kBack>
+cudaError_t run_chain_fwd(const Call& c, const Maps& m, const ChainIn& in) {
+    constexpr size_t smem = ChainStage<DK, kBack>::SMEM;
+    cudaError_t e = chain_ready(chain_fwd_kernel<DK, kBack>, smem);
+    if (e != cudaSuccess) return e;
+    chain_fwd_kernel<DK, kBack><<<(unsigned)(c.s.N * c.s.Hv), kChainThreads, smem, c.st>>>(
+        m.q, m.k, m.v, m.o, in, c.S0, c.o, c.ST, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
+    return cudaPeekAtLastError();
+}
+template <int DK>
+cudaError_t run_chain_bwd(const Call& c, const Maps& m, const ChainIn& in) {
+    constexpr size_t smem = ChainStage<DK, true>::SMEM;
+    cudaError_t e = chain_ready(chain_bwd_kernel<DK>, smem);
+    if (e != cudaSuccess) return e;
+    chain_bwd_kernel<DK><<<(unsigned)(c.s.N * c.s.Hv), kChainThreads, smem, c.st>>>(
+        m.q, m.k, m.v, m.o, in, c.dST, c.gv, c.gS0, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
+    return cudaPeekAtLastError();
+}
+template <int DV>
+cudaError_t run_grads(const Call& c) {
+    constexpr size_t smem = GradSmem<DV>::BYTES;
+    cudaError_t e = allow_smem(grad_kernel<DV>, smem);
+    if (e != cudaSuccess) return e;
+    grad_kernel<DV><<<dim3((unsigned)Seqs::slots(c.s.N, c.s.total), (unsigned)c.s.Hk, (unsigned)((c.s.dk + 63) / 64)), 128, smem, c.st>>>(
+        c.q, c.k, c.grad_o, c.gv, c.gq, c.gk, c.gg, c.gb, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv, c.qs, c.ks);
+    return cudaPeekAtLastError();
+}
+
+template <int DK, bool kBack>
+cudaError_t run_chunked(const Call& c) {
+    ChainIn in{c.q, c.k, c.v, c.grad_o, c.qs, c.ks, c.vs, c.s.dk >= 64 && c.s.dv >= 64};
+    Maps m{};
+    if (in.maps) {
+        const bool ok = rows_map(&m.q, c.q, c.s.total, c.s.Hk, c.s.dk, c.qs) && rows_map(&m.k, c.k, c.s.total, c.s.Hk, c.s.dk, c.ks) &&
+                        rows_map(&m.v, c.v, c.s.total, c.s.Hv, c.s.dv, c.vs) &&
+                        (!kBack || rows_map(&m.o, c.grad_o, c.s.total, c.s.Hv, c.s.dv, (long long)c.s.Hv * c.s.dv));
+        if (!ok) return cudaErrorInvalidValue;
+    }
+    cudaError_t e = run_intra<DK>(c);
+    if (e == cudaSuccess) e = run_chain_fwd<DK, kBack>(c, m, in);
+    if constexpr (kBack) {
+        if (e == cudaSuccess) e = run_chain_bwd<DK>(c, m, in);
+        if (e == cudaSuccess) e = c.s.dv <= 64 ? run_grads<64>(c) : run_grads<128>(c);
+    }
+    return e;
+}
+
 }  // namespace
 
 extern "C" {
@@ -129,15 +274,20 @@ extern "C" {
 // Reads and clears the error word of this file's kernels (for ckda_get_device_error, after it
 // synchronised the stream). Not part of the ABI.
 cudaError_t ckda_gated_take_error(unsigned int* word) {
-    unsigned int zero = 0;
+    const unsigned int zero = 0;
+    unsigned int wait = 0;                     // bit 0: a bounded wait of this file's kernels ran out
     cudaError_t e = cudaMemcpyFromSymbol(word, g_gated_error_word, sizeof(*word));
     if (e == cudaSuccess && *word != 0) e = cudaMemcpyToSymbol(g_gated_error_word, &zero, sizeof(zero));
+    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&wait, ckda::g_error_word, sizeof(wait));
+    if (e == cudaSuccess && wait != 0) e = cudaMemcpyToSymbol(ckda::g_error_word, &zero, sizeof(zero));
+    *word |= wait;
     return e;
 }
 
 size_t ckda_gated_fwd_workspace_bytes(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt) {
-    (void)N; (void)total; (void)Hk; (void)Hv; (void)dk; (void)dv; (void)dt;
-    return 0;
+    const Shape s{N, 0, total, Hk, Hv, dk, dv, dt};
+    if (check_shape(s, true) != CKDA_OK || N == 0 || total == 0 || !chunked(s)) return 0;
+    return chunk_layout(s, false).total;
 }
 
 ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -159,6 +309,19 @@ ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const 
     if (N == 0) return CKDA_OK;
     if (total == 0) return clear_or_copy(S0, S_T, (size_t)N * Hv * dk * dv, st);
     const Seqs seqs{cu_seqlens, N, T, total};
+    if (chunked(s, q_stride, k_stride, v_stride)) {
+        Call a{};
+        a.s = s;
+        a.seqs = seqs;
+        a.q = static_cast<const bf16*>(q); a.k = static_cast<const bf16*>(k); a.v = static_cast<const bf16*>(v);
+        a.g = g; a.beta = beta; a.S0 = S0;
+        a.o = static_cast<bf16*>(o); a.ST = S_T;
+        a.qs = q_stride; a.ks = k_stride; a.vs = v_stride;
+        a.ws = chunk_ws(chunk_layout(s, false), workspace);
+        a.st = st;
+        const cudaError_t e = dk <= 64 ? run_chunked<64, false>(a) : run_chunked<128, false>(a);
+        return e == cudaSuccess ? launch_status() : (cudaGetLastError(), CKDA_ERR_CUDA);
+    }
     if (dt == CKDA_BF16) return simt_fwd<bf16>(s, q, k, v, g, beta, S0, o, S_T, seqs, nullptr, N, q_stride, k_stride, v_stride, st);
     return simt_fwd<float>(s, q, k, v, g, beta, S0, o, S_T, seqs, nullptr, N, q_stride, k_stride, v_stride, st);
 }
@@ -166,7 +329,8 @@ ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const 
 size_t ckda_gated_bwd_workspace_bytes(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt) {
     const Shape s{N, 0, total, Hk, Hv, dk, dv, dt};
     if (check_shape(s, true) != CKDA_OK || N == 0 || total == 0) return 0;
-    return simt_bwd_layout(s).total;
+    // rows whose stride the chunked kernels cannot read go to the CUDA cores: room for either
+    return chunked(s) ? std::max(chunk_layout(s, true).total, simt_bwd_layout(s).total) : simt_bwd_layout(s).total;
 }
 
 ckda_status_t ckda_gated_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -193,6 +357,21 @@ ckda_status_t ckda_gated_bwd(const void* q, const void* k, const void* v, const 
     if (total == 0) return clear_or_copy(grad_S_T, grad_S0, (size_t)N * Hv * dk * dv, st);
     const Seqs seqs{cu_seqlens, N, T, total};
     char* ws = static_cast<char*>(workspace);
+    if (chunked(s, q_stride, k_stride, v_stride)) {
+        Call a{};
+        a.s = s;
+        a.seqs = seqs;
+        a.q = static_cast<const bf16*>(q); a.k = static_cast<const bf16*>(k); a.v = static_cast<const bf16*>(v);
+        a.grad_o = static_cast<const bf16*>(grad_o);
+        a.g = g; a.beta = beta; a.S0 = S0; a.dST = grad_S_T;
+        a.gq = static_cast<bf16*>(grad_q); a.gk = static_cast<bf16*>(grad_k); a.gv = static_cast<bf16*>(grad_v);
+        a.gg = grad_g; a.gb = grad_beta; a.gS0 = grad_S0;
+        a.qs = q_stride; a.ks = k_stride; a.vs = v_stride;
+        a.ws = chunk_ws(chunk_layout(s, true), ws);
+        a.st = st;
+        const cudaError_t e = dk <= 64 ? run_chunked<64, true>(a) : run_chunked<128, true>(a);
+        return e == cudaSuccess ? launch_status() : (cudaGetLastError(), CKDA_ERR_CUDA);
+    }
     if (dt == CKDA_BF16)
         return simt_bwd<bf16>(s, q, k, v, g, beta, S0, grad_o, grad_S_T, grad_q, grad_k, grad_v, grad_g, grad_beta, grad_S0,
                               seqs, q_stride, k_stride, v_stride, ws, st);

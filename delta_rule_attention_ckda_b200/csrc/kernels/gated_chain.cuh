@@ -1,0 +1,889 @@
+// Chunked gated delta rule, part 2: the state from chunk to chunk (see gated_intra.cuh for Z, P).
+// Per chunk, S the state entering it:
+//   X = V - e^G (.) K S,   W = X + Z (beta X),   U = beta W
+//   O = e^G (.) Q S + P U,  S' = e^{G_C} S + K^T (e^{G_C - G} (.) U)
+//
+// Three products follow one another in every chunk, so the time is a chain of latencies: an
+// operand written, a product, its result read. One CTA per (sequence, value head) walks the
+// chunks; everything is held transposed, d_v on the 128 TMEM lanes, so that an epilogue thread
+// has one column of the state and each product's result, split into bf16 terms, is written
+// back to TMEM as the left operand of the next without crossing threads. Eight epilogue warps
+// (two per lane quarter, half of the channels or tokens each) keep S in fp32 registers; four
+// warps form the output; one thread issues the products; three warps load the next chunk's
+// tiles, by tensor copies, or row by row where a chunk ends inside (zeros behind a packed
+// sequence's end, where a tile copy would bring the next sequence's rows).
+//
+// What hides what: the output's products (P U), its epilogue and its store run under the next
+// chunk's state split; loads run a chunk ahead. A product of N = 64 takes as long as one of
+// N = 128, so pairs share one: [K; Q] S, and both terms of Z side by side.
+//
+// Rounding: raw K, Q, V are exact; every other operand (S, beta X, Z, U, P) is two bf16 terms
+// (2.7e-6 of a value at RMS), o is rounded once at its store. Sums are fp32; S' is formed in
+// registers. Backward (kBack): S and U in three terms, because dg sums differences of <dO, o> and
+// <dV, v> (a model of this arithmetic in fp64: dg off by 1.9e-6 in place of 2.1e-5 where the
+// states are large, by 1.3e-6 in place of 1.4e-5 elsewhere).
+#pragma once
+#include "gated_mma.cuh"
+#include "tc_primitives.cuh"
+
+namespace ckda {
+namespace gated {
+
+// Warps by role; every role is whole warpgroups, so that registers can be moved between them.
+constexpr int kEpiWarps = 8, kOutWarps = 4, kMmaWarp = 12, kLoadWarps = 3;
+constexpr int kChainThreads = 512;
+// Registers a thread: 128 at launch; the epilogue warps hold half a state column each, the out
+// warps a row of the output.
+constexpr int kRegLaunch = 128, kRegEpi = 168, kRegOut = 112, kRegOther = 64;
+static_assert(256 * kRegEpi + 128 * kRegOut + 128 * kRegOther <= kChainThreads * kRegLaunch,
+              "a register split larger than the launch's waits forever");
+
+// Tensor memory columns
+constexpr uint32_t TM_ACC = 0;      // [K S | Q S]; backward: K dS | y
+constexpr uint32_t TM_S = 128;      // the state's operand (per half of the channels: hi, lo), then its update
+constexpr uint32_t TM_UZ = 256;     // the products with both terms of Z; then the operands U' and U (e^G dV)
+constexpr uint32_t TM_X = 384;      // beta X (per half of the tokens: hi, lo); then U' third term
+constexpr uint32_t TM_PU = 448;     // P U; backward: P^T dO
+constexpr uint32_t TM_COLS = 512;
+
+// A stage of shared memory (bytes from a 1024-aligned base), rows of 128 bytes, 128-byte swizzle
+template <int DK, bool kDO>
+struct ChainStage {
+    static constexpr uint32_t KQ = 0;                              // per 64 channels: [64 rows of K | 64 of Q]
+    static constexpr uint32_t V = KQ + (DK / 64) * 16384;          // 2 x [64][64]
+    static constexpr uint32_t DO = V + 16384;                      // 2 x [64][64]
+    static constexpr uint32_t Z = DO + (kDO ? 16384 : 0);          // [hi | lo]
+    static constexpr uint32_t P = Z + 16384;
+    static constexpr uint32_t VECS = P + 16384;
+    static constexpr uint32_t BYTES = VECS + 1024;
+    static constexpr uint32_t OUT = 2 * BYTES;                     // [64][128] rows on their way out
+    static constexpr size_t SMEM = OUT + 16384 + 1024;
+    static constexpr uint32_t kTileBytes = (DK / 64) * 16384 + 16384 + (kDO ? 16384 : 0);
+};
+static_assert(ChainStage<128, true>::SMEM <= 232448, "more shared memory than an SM has");
+
+struct ChainBars {
+    uint64_t full[2], empty[2], s, m1, x, m2, d, u, uo, m3, o, out, qs;
+    uint32_t tmem;
+    int dead;                       // a bounded wait ran out: nothing waits any more, the loops run off
+};
+
+__device__ __forceinline__ void chain_wait(ChainBars& b, uint64_t* bar, uint32_t phase) {
+    if (tc::mbar_try_wait(bar, phase)) return;
+    if (*reinterpret_cast<volatile int*>(&b.dead)) return;
+    if (!tc::mbar_wait(bar, phase)) *reinterpret_cast<volatile int*>(&b.dead) = 1;
+}
+// A value the compiler takes as new, so that what it computes from it (a chunk's operand
+// descriptors) is computed there and not kept in registers across the loop.
+__device__ __forceinline__ uint32_t fresh(uint32_t x) {
+    asm volatile("" : "+r"(x));
+    return x;
+}
+template <int R> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+__device__ __forceinline__ uint32_t swz(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
+// Element (token, channel) of a tile of 64-channel blocks, read by the thread that owns the channel.
+__device__ __forceinline__ float tile_value(const unsigned char* tile, int token, int ch) {
+    const uint16_t x = *reinterpret_cast<const uint16_t*>(tile + (ch / 64) * 8192 + swz(token, (ch % 64) / 8) + (ch % 8) * 2);
+    return __uint_as_float((uint32_t)x << 16);
+}
+
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int head, int token) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(c0), "r"(head), "r"(token)
+                 : "memory");
+}
+
+// What a chain kernel reads by rows: tensor maps over [tokens][heads][channels] (boxes of 64
+// tokens of one head's 64 channels), and plain pointers for the rows at a sequence's end.
+struct ChainIn {
+    const __nv_bfloat16 *q, *k, *v, *dO;
+    long long qs, ks, vs;
+    int maps;                       // whether the maps are usable (heads of at least 64 channels)
+};
+
+// The loading warps' share (thread x) of a chunk into stage `st`, completing on `full`: k, q, v, dO
+// by tensor copies where the chunk is whole, else by rows with zeros behind the sequence's end;
+// the lower blocks of Z and P (those above the block diagonal stay the zeros the kernel starts
+// with); the vectors.
+template <int DK, bool kDO>
+__device__ __forceinline__ void chain_load(uint32_t st, uint64_t* full, int x, const ChainIn& in, const CUtensorMap* mq, const CUtensorMap* mk,
+                                           const CUtensorMap* mv, const CUtensorMap* mo, const ChunkWs& ws, size_t wh, int tok, int nt,
+                                           int h, int hk, int Hv, int dk, int dv) {
+    using L = ChainStage<DK, kDO>;
+    constexpr int NT = 32 * kLoadWarps, PK = DK / 8;
+    const bool tiles = in.maps && nt == C;
+    if (x == 0) {
+        tc::mbar_arrive_expect_tx(full, tiles ? L::kTileBytes : 0);
+        if (tiles) {
+#pragma unroll
+            for (int b = 0; b < DK / 64; ++b) {
+                tma_rows(st + L::KQ + b * 16384, mk, full, 64 * b, hk, tok);
+                tma_rows(st + L::KQ + b * 16384 + 8192, mq, full, 64 * b, hk, tok);
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                tma_rows(st + L::V + b * 8192, mv, full, 64 * b, h, tok);
+                if constexpr (kDO) tma_rows(st + L::DO + b * 8192, mo, full, 64 * b, h, tok);
+            }
+        }
+    }
+    const size_t w0 = wh * 4096;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = x; e < 32 * (i + 1); e += NT) {
+            const int r = 16 * i + e / (2 * (i + 1)), p = e % (2 * (i + 1));
+            const size_t from = w0 + r * 64 + p * 8;
+            const uint32_t to = st + swz(r, p);
+            cp16(to + L::Z, ws.zhi + from, true);
+            cp16(to + L::Z + 8192, ws.zlo + from, true);
+            cp16(to + L::P, ws.phi + from, true);
+            cp16(to + L::P + 8192, ws.plo + from, true);
+        }
+    if (x < 48) cp16(st + L::VECS + x * 16, ws.vec + wh * VEC + x * 4, true);
+    if (!tiles) {
+        const __nv_bfloat16 *q = in.q + tok * in.qs + (size_t)hk * dk, *k = in.k + tok * in.ks + (size_t)hk * dk,
+                            *v = in.v + tok * in.vs + (size_t)h * dv, *dO = kDO ? in.dO + ((size_t)tok * Hv + h) * dv : nullptr;
+#pragma unroll 2
+        for (int e = x; e < 64 * PK; e += NT) {
+            const int r = e / PK, p = e % PK;
+            const bool is = r < nt && p * 8 < dk;
+            const uint32_t to = st + L::KQ + (p / 8) * 16384 + swz(r, p & 7);
+            cp16(to, is ? k + r * in.ks + p * 8 : k, is);
+            cp16(to + 8192, is ? q + r * in.qs + p * 8 : q, is);
+        }
+#pragma unroll 2
+        for (int e = x; e < 64 * 16; e += NT) {
+            const int r = e / 16, p = e % 16;
+            const bool is = r < nt && p * 8 < dv;
+            const uint32_t to = (p / 8) * 8192 + swz(r, p & 7);
+            cp16(st + L::V + to, is ? v + r * in.vs + p * 8 : v, is);
+            if constexpr (kDO) cp16(st + L::DO + to, is ? dO + (size_t)r * Hv * dv + p * 8 : dO, is);
+        }
+    }
+    cp_commit();
+    cp_wait<0>();
+    tc::fence_proxy_async_smem();
+    tc::mbar_arrive(full);
+}
+
+// 32 consecutive floats of shared memory that every thread reads alike.
+__device__ __forceinline__ void read32(float (&x)[32], const float* p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 y = *reinterpret_cast<const float4*>(p + 4 * i);
+        x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
+    }
+}
+
+// The out warps' [64][128] tile of bf16 rows in shared memory to global rows, 16 bytes a lane.
+__device__ __forceinline__ void rows_out(const unsigned char* tile, int x, __nv_bfloat16* dst, long long stride, int rows, int cols) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = x + 128 * i, r = e / 16, p = e % 16;
+        if (r < rows && p * 8 < cols) *reinterpret_cast<uint4*>(dst + r * stride + p * 8) = *reinterpret_cast<const uint4*>(tile + r * 256 + p * 16);
+    }
+}
+__device__ __forceinline__ void out_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// 32 fp32 values as bf16 terms to TMEM operand columns: hi at `to`, then 16 columns a term.
+template <int TERMS>
+__device__ __forceinline__ void put_terms(const float* x, const uint32_t (&to)[TERMS]) {
+#pragma unroll
+    for (int k = 0; k < 16; k += 8) {
+        uint32_t h[8], m[8], l[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = 2 * (k + i);
+            if constexpr (TERMS == 3) split3(x[j], x[j + 1], h[i], m[i], l[i]);
+            else split2(x[j], x[j + 1], h[i], m[i]);
+        }
+        tc::tmem_st32<8>(to[0] + k, h);
+        tc::tmem_st32<8>(to[1] + k, m);
+        if constexpr (TERMS == 3) tc::tmem_st32<8>(to[TERMS - 1] + k, l);
+    }
+}
+
+// Channels i .. i + 31 of a thread's half column of the state as the next product's operand; a third
+// term lies in the columns of beta X, which is written after that product.
+template <int TERMS, int H>
+__device__ __forceinline__ void put_state_terms(const float* s, uint32_t tl, int wg, int i) {
+    uint32_t to[TERMS];
+    to[0] = tl + TM_S + wg * H + i / 2;
+    to[1] = to[0] + H / 2;
+    if constexpr (TERMS == 3) to[TERMS - 1] = tl + TM_X + wg * (H / 2) + i / 2;
+    put_terms<TERMS>(s, to);
+}
+
+// s <- whole s + the H update columns at `from`, all loads in flight.
+template <int H>
+__device__ __forceinline__ void add_update(float (&s)[H], float whole, uint32_t from) {
+    float d[H / 32][32];
+#pragma unroll
+    for (int i = 0; i < H / 32; ++i) tc::tmem_ld32<32>(from + 32 * i, d[i]);
+    tc::tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < H; i += 2) {
+        fma2(d[i / 32][i % 32], d[i / 32][i % 32 + 1], s[i], s[i + 1], whole, whole);
+        s[i] = d[i / 32][i % 32];
+        s[i + 1] = d[i / 32][i % 32 + 1];
+    }
+}
+
+// Sum over the lanes of each of 32 values: lane i returns the sum of v[i].
+__device__ __forceinline__ float lane_sums(float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+        for (int i = 0; i < off; ++i) {
+            const bool up = lane & off;
+            const float keep = up ? v[i + off] : v[i], send = up ? v[i] : v[i + off];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, off);
+        }
+    return v[0];
+}
+
+// HD channels of a state column in 4 bytes a value: the fp32 bits, rounded half up to their
+// upper 16 (a bf16 value, `hi`) and the signed rest: bits = (hi << 16) + lo. `step`: elements
+// between groups of 8 channels (see ChunkWs).
+template <int HD>
+__device__ __forceinline__ void put_state(const float* s, __nv_bfloat16* hi, __nv_bfloat16* lo, size_t step, int left) {
+#pragma unroll
+    for (int i = 0; i < HD; i += 8) {
+        if (i >= left) break;
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t a = __float_as_uint(s[i + 2 * j]), b = __float_as_uint(s[i + 2 * j + 1]);
+            h[j] = __byte_perm(a + 0x8000u, b + 0x8000u, 0x7632);
+            l[j] = __byte_perm(a, b, 0x5410);
+        }
+        *reinterpret_cast<uint4*>(hi + i / 8 * step) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(lo + i / 8 * step) = make_uint4(l[0], l[1], l[2], l[3]);
+    }
+}
+__device__ __forceinline__ float state_lo(uint32_t h, uint32_t l) {
+    return __uint_as_float((h << 16) + (uint32_t)(int)(short)(l & 0xffffu));
+}
+__device__ __forceinline__ float state_hi(uint32_t h, uint32_t l) {
+    return __uint_as_float((h & 0xffff0000u) + (uint32_t)((int)l >> 16));
+}
+
+// What both chains set up and take down.
+__device__ __forceinline__ void chain_begin(ChainBars& b, unsigned char* stages, uint32_t bytes) {
+    if (threadIdx.x / 32 == kMmaWarp) tc::tmem_alloc(&b.tmem, TM_COLS);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&b.full[i], 32 * kLoadWarps + 1);
+            tc::mbar_init(&b.empty[i], 1 + kEpiWarps + kOutWarps);
+        }
+        for (uint64_t* e : {&b.s, &b.x, &b.u, &b.uo}) tc::mbar_init(e, 32 * kEpiWarps);
+        for (uint64_t* e : {&b.d, &b.out, &b.qs}) tc::mbar_init(e, 32 * kOutWarps);
+        for (uint64_t* e : {&b.m1, &b.m2, &b.m3, &b.o}) tc::mbar_init(e, 1);
+        b.dead = 0;
+        tc::fence_mbar_init();
+    }
+    for (uint32_t i = threadIdx.x; i < bytes / 16; i += kChainThreads) reinterpret_cast<uint4*>(stages)[i] = make_uint4(0, 0, 0, 0);
+    tc::fence_proxy_async_smem();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+}
+__device__ __forceinline__ void chain_end(ChainBars& b) {
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    if (threadIdx.x / 32 == kMmaWarp) {
+        tc::tmem_dealloc(b.tmem, TM_COLS);
+        tc::tmem_relinquish();
+    }
+}
+
+template <int DK, bool kBack>
+__global__ void __launch_bounds__(kChainThreads, 1)
+chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                 const __grid_constant__ CUtensorMap mo, const ChainIn in, const float* S0, __nv_bfloat16* __restrict__ o, float* ST,
+                 ChunkWs ws, Seqs seqs, int Hk, int Hv, int dk, int dv) {
+    using L = ChainStage<DK, kBack>;
+    constexpr int H = DK / 2;                  // channels of an epilogue thread
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ ChainBars bars;
+    const int n = blockIdx.x / Hv, h = blockIdx.x % Hv, hk = h / (Hv / Hk);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int start, len;
+    bool ok;
+    seqs.get(n, start, len, ok);
+    if (!ok && h == 0 && threadIdx.x == 0) report_index_error();
+    const int chunks = (len + C - 1) / C, slot0 = seqs.first_slot(n, start), strips = (dv + 31) / 32;
+    const size_t mat = (size_t)dk * dv, sbase = ((size_t)n * Hv + h) * mat;
+    chain_begin(bars, sm, 2 * L::BYTES);
+    const uint32_t tm = bars.tmem, base = s32(sm);
+
+    if (warp >= kMmaWarp) {
+        regs_down<kRegOther>();
+        if (warp > kMmaWarp) {                 // ------------------------------------------ loads
+            const int x = threadIdx.x - 32 * (kMmaWarp + 1);
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                if (c >= 2) chain_wait(bars, &bars.empty[c & 1], ((c >> 1) - 1) & 1);
+                chain_load<DK, kBack>(base + (c & 1) * L::BYTES, &bars.full[c & 1], x, in, &mq, &mk, &mv, &mo, ws,
+                                      (size_t)(slot0 + c) * Hv + h, start + c * C, min(C, len - c * C), h, hk, Hv, dk, dv);
+            }
+        } else if (lane == 0) {                // ------------------------------------------ products
+            constexpr uint32_t i128 = tc::idesc_bf16(128, 128, 0, 0), i64 = tc::idesc_bf16(128, 64, 0, 0),
+                               iS = tc::idesc_bf16(128, DK, 0, 1);
+            // The output's product of a chunk is issued behind the next chunk's first one: it runs under the
+            // epilogue that follows that one.
+            auto output = [&](int c) {
+                const uint32_t st = fresh(base + (c & 1) * L::BYTES);
+                if (c > 0) chain_wait(bars, &bars.out, (c - 1) & 1);   // P U of the chunk before is read
+                chain_wait(bars, &bars.uo, c & 1);
+                tc::tc_fence_after();
+#pragma unroll
+                for (int term = 0; term < 3; ++term)               // P U: hi lo, lo hi, hi hi
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        tc::mma_ts(tm + TM_PU, tm + TM_UZ + 64 + (j / 2) * 32 + (term == 1 ? 16 : 0) + (j % 2) * 8,
+                                   tc::sdesc(st + L::P + (term == 0 ? 8192 : 0) + j * 32, 16, 1024), i64, (term | j) != 0);
+                tc::mma_commit(&bars.o);
+                tc::mma_commit(&bars.empty[c & 1]);
+            };
+            if (chunks > 0) chain_wait(bars, &bars.full[0], 0);
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) {
+                const uint32_t st = fresh(base + (c & 1) * L::BYTES), ph = c & 1;
+                chain_wait(bars, &bars.s, ph);
+                tc::tc_fence_after();
+#pragma unroll
+                for (int term = 0; term < (kBack ? 3 : 2); ++term) // [K S | Q S]
+#pragma unroll
+                    for (int j = 0; j < DK / 16; ++j) {
+                        const int half = j / (H / 16), jj = j % (H / 16);
+                        const uint32_t a = term < 2 ? TM_S + half * H + term * (H / 2) : TM_X + half * (H / 2);
+                        tc::mma_ts(tm + TM_ACC, tm + a + jj * 8, tc::sdesc(st + L::KQ + (j / 4) * 16384 + (j % 4) * 32, 16, 1024),
+                                   i128, (term | j) != 0);
+                    }
+                tc::mma_commit(&bars.m1);
+                if (c > 0) output(c - 1);
+                chain_wait(bars, &bars.x, ph);
+                tc::tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 4; ++j)                        // beta X [Z_hi | Z_lo]
+                    tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 32, 16, 1024), i128, j != 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + 16 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 32, 16, 1024), i64, 1);
+                tc::mma_commit(&bars.m2);
+                chain_wait(bars, &bars.qs, ph);                    // Q S is read: its columns may be written again
+                chain_wait(bars, &bars.u, ph);
+                tc::tc_fence_after();
+#pragma unroll
+                for (int term = 0; term < (kBack ? 3 : 2); ++term) // the state's update
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t a = term < 2 ? TM_UZ + (j / 2) * 32 + term * 16 + (j % 2) * 8 : TM_X + (j / 2) * 32 + (j % 2) * 8;
+                        tc::mma_ts(tm + TM_S, tm + a, tc::sdesc(st + L::KQ + j * 2048, 16384, 1024), iS, (term | j) != 0);
+                    }
+                tc::mma_commit(&bars.m3);
+                if (c + 1 < chunks) chain_wait(bars, &bars.full[(c + 1) & 1], ((c + 1) >> 1) & 1);
+            }
+            if (chunks > 0) {
+                output(chunks - 1);
+                chain_wait(bars, &bars.o, (chunks - 1) & 1);       // nothing in flight past this point
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kEpiWarps) {            // ------------------------------------------ output
+        regs_down<kRegOut>();
+        const int quarter = warp & 3, row = 32 * quarter + lane, x = threadIdx.x - 32 * kEpiWarps;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
+        unsigned char* tile = sm + L::OUT;
+#pragma unroll 1
+        for (int c = 0; c < chunks; ++c) {
+            const unsigned char* st = sm + (c & 1) * L::BYTES;
+            const float* eg = reinterpret_cast<const float*>(st + L::VECS) + VEC_EG;
+            const int tok = start + c * C, nt = min(C, len - c * C);
+            float r[64];
+            chain_wait(bars, &bars.full[c & 1], (c >> 1) & 1);
+            chain_wait(bars, &bars.m1, c & 1);
+            tc::tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 64; i += 32) {
+                float a[32];
+                tc::tmem_ld32<32>(tl + TM_ACC + 64 + i, a);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[i + j] = a[j];
+            }
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bars.qs);
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+                const float4 e = *reinterpret_cast<const float4*>(eg + i);
+                r[i] *= e.x; r[i + 1] *= e.y; r[i + 2] *= e.z; r[i + 3] *= e.w;
+            }
+            chain_wait(bars, &bars.o, c & 1);
+            tc::tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 64; i += 16) {
+                float a[16];
+                tc::tmem_ld32<16>(tl + TM_PU + i, a);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) r[i + j] += a[j];
+            }
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bars.out);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                if constexpr (kBack) {
+                    float t[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) t[i] = r[32 * half + i] * tile_value(st + L::DO, 32 * half + i, row);
+                    const float sum = lane_sums(t);
+                    if (quarter < strips)
+                        ws.parts[(((size_t)(slot0 + c) * Hv + h) * strips + quarter) * PARTS + PART_DOO + 32 * half + lane] = sum;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        *reinterpret_cast<__nv_bfloat16*>(tile + (32 * half + i) * 256 + 2 * row) = __float2bfloat16_rn(r[32 * half + i]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars.empty[c & 1]);
+            if constexpr (!kBack) {
+                out_sync();
+                rows_out(tile, x, o + ((size_t)tok * Hv + h) * dv, (long long)Hv * dv, nt, dv);
+                out_sync();
+            }
+        }
+    } else {                                   // ------------------------------------------ epilogues of the chain
+        regs_up<kRegEpi>();
+        const int quarter = warp & 3, wg = warp >> 2, row = 32 * quarter + lane;
+        const bool live = row < dv;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
+        float s[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const int d = wg * H + i;
+            s[i] = (S0 != nullptr && live && d < dk) ? S0[sbase + (size_t)d * dv + row] : 0.f;
+        }
+#pragma unroll 1
+        for (int c = 0; c <= chunks; ++c) {
+            if (c > 0) {                       // S <- e^{G_C} S + update
+                const float whole = reinterpret_cast<const float*>(sm + ((c - 1) & 1) * L::BYTES + L::VECS)[VEC_EG + 63];
+                chain_wait(bars, &bars.m3, (c - 1) & 1);
+                tc::tc_fence_after();
+                add_update<H>(s, whole, tl + TM_S + wg * H);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars.empty[(c - 1) & 1]);
+            }
+            if (c < chunks) {
+#pragma unroll
+                for (int i = 0; i < H; i += 32) put_state_terms<kBack ? 3 : 2, H>(s + i, tl, wg, i);
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                tc::mbar_arrive(&bars.s);
+            }
+            if constexpr (kBack) {             // the entering (at the end: the final) state for the backward kernels
+                if (live) {
+                    const size_t to = ((size_t)(slot0 + c) * Hv + h) * mat + ((size_t)(wg * H / 8) * dv + row) * 8;
+                    put_state<H>(s, ws.shi + to, ws.slo + to, (size_t)dv * 8, dk - wg * H);
+                }
+            }
+            if (c == chunks) break;
+            // X = V - e^G K S, and beta X as an operand
+            const unsigned char* st = sm + (c & 1) * L::BYTES;
+            const float* vec = reinterpret_cast<const float*>(st + L::VECS) + 32 * wg;
+            float x[32], y[32];
+            chain_wait(bars, &bars.full[c & 1], (c >> 1) & 1);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = tile_value(st + L::V, 32 * wg + i, row);
+            chain_wait(bars, &bars.m1, c & 1);
+            tc::tc_fence_after();
+            tc::tmem_ld32<32>(tl + TM_ACC + 32 * wg, x);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 eg = *reinterpret_cast<const float4*>(vec + VEC_EG + i), bt = *reinterpret_cast<const float4*>(vec + VEC_BETA + i);
+                fma2(y[i], y[i + 1], x[i], x[i + 1], -eg.x, -eg.y);
+                fma2(y[i + 2], y[i + 3], x[i + 2], x[i + 3], -eg.z, -eg.w);
+                x[i] = y[i]; x[i + 1] = y[i + 1]; x[i + 2] = y[i + 2]; x[i + 3] = y[i + 3];
+                mul2(y[i], y[i + 1], bt.x, bt.y);
+                mul2(y[i + 2], y[i + 3], bt.z, bt.w);
+            }
+            {
+                const uint32_t to[2] = {tl + TM_X + 32 * wg, tl + TM_X + 32 * wg + 16};
+                put_terms<2>(y, to);
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bars.x);
+            // W, U; the operands U' = e^{G_C - G} U and U
+            chain_wait(bars, &bars.m2, c & 1);
+            tc::tc_fence_after();
+            {
+                tc::tmem_ld32<32>(tl + TM_UZ + 32 * wg, y);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) add2(x[i], x[i + 1], y[i], y[i + 1]);
+                tc::tmem_ld32<32>(tl + TM_UZ + 64 + 32 * wg, y);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) add2(x[i], x[i + 1], y[i], y[i + 1]);
+            }
+            const size_t wh = (size_t)(slot0 + c) * Hv + h;
+            if constexpr (kBack) {
+                if (live) {
+                    float4* wp = reinterpret_cast<float4*>(ws.w + wh * 64 * dv) + (size_t)(8 * wg) * dv + row;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) wp[i * dv] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 bt = *reinterpret_cast<const float4*>(vec + VEC_BETA + i), dc = *reinterpret_cast<const float4*>(vec + VEC_DEC + i);
+                mul2(x[i], x[i + 1], bt.x, bt.y);
+                mul2(x[i + 2], x[i + 3], bt.z, bt.w);
+                y[i] = x[i]; y[i + 1] = x[i + 1]; y[i + 2] = x[i + 2]; y[i + 3] = x[i + 3];
+                mul2(y[i], y[i + 1], dc.x, dc.y);
+                mul2(y[i + 2], y[i + 3], dc.z, dc.w);
+            }
+            if constexpr (kBack) {
+                const uint32_t to[3] = {tl + TM_UZ + 32 * wg, tl + TM_UZ + 32 * wg + 16, tl + TM_X + 32 * wg};
+                put_terms<3>(y, to);
+            } else {
+                const uint32_t to[2] = {tl + TM_UZ + 32 * wg, tl + TM_UZ + 32 * wg + 16};
+                put_terms<2>(y, to);
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bars.u);
+            {
+                const uint32_t to[2] = {tl + TM_UZ + 64 + 32 * wg, tl + TM_UZ + 64 + 32 * wg + 16};
+                put_terms<2>(x, to);
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bars.uo);
+            if constexpr (kBack) {
+                if (live) {
+                    __nv_bfloat16* up = ws.u + wh * 64 * dv + (size_t)(32 * wg) * dv + row;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) up[i * dv] = __float2bfloat16_rn(x[i]);
+                }
+            }
+        }
+        if constexpr (!kBack) {
+            if (ST != nullptr && live) {
+#pragma unroll
+                for (int i = 0; i < H; ++i) {
+                    const int d = wg * H + i;
+                    if (d < dk) ST[sbase + (size_t)d * dv + row] = s[i];
+                }
+            }
+        }
+    }
+    chain_end(bars);
+}
+
+// The adjoint chain, chunks last to first, dS the cotangent of the state leaving a chunk:
+//   dU = P^T dO + e^{G_C - G} (.) K dS,   y = dU + Z^T (beta dU),   dV = beta y
+//   dS <- e^{G_C} dS + Q^T (e^G (.) dO) - K^T (e^G (.) dV)
+// and the sums that the gradients of beta and g need: w.y and dV.v per token, <S', dS> per
+// chunk. The layout and roles of the forward chain; the out warps prepare the operand e^G dO and
+// take y from TMEM for dV and the sums. The products that do not wait for dS (P^T dO, Q^T dO)
+// run under the epilogues; the operands of the update carry three terms.
+template <int DK>
+__global__ void __launch_bounds__(kChainThreads, 1)
+chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                 const __grid_constant__ CUtensorMap mo, const ChainIn in, const float* dST, __nv_bfloat16* __restrict__ grad_v,
+                 float* grad_S0, ChunkWs ws, Seqs seqs, int Hk, int Hv, int dk, int dv) {
+    using L = ChainStage<DK, true>;
+    constexpr int H = DK / 2;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ ChainBars bars;
+    const int n = blockIdx.x / Hv, h = blockIdx.x % Hv, hk = h / (Hv / Hk);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int start, len;
+    bool ok;
+    seqs.get(n, start, len, ok);
+    const int chunks = (len + C - 1) / C, slot0 = seqs.first_slot(n, start), strips = (dv + 31) / 32;
+    const size_t mat = (size_t)dk * dv, sbase = ((size_t)n * Hv + h) * mat;
+    chain_begin(bars, sm, 2 * L::BYTES);
+    const uint32_t tm = bars.tmem, base = s32(sm);
+
+    if (warp >= kMmaWarp) {
+        regs_down<kRegOther>();
+        if (warp > kMmaWarp) {                 // ------------------------------------------ loads
+            const int x = threadIdx.x - 32 * (kMmaWarp + 1);
+#pragma unroll 1
+            for (int it = 0; it < chunks; ++it) {
+                const int c = chunks - 1 - it;
+                if (it >= 2) chain_wait(bars, &bars.empty[it & 1], ((it >> 1) - 1) & 1);
+                chain_load<DK, true>(base + (it & 1) * L::BYTES, &bars.full[it & 1], x, in, &mq, &mk, &mv, &mo, ws,
+                                     (size_t)(slot0 + c) * Hv + h, start + c * C, min(C, len - c * C), h, hk, Hv, dk, dv);
+            }
+        } else if (lane == 0) {                // ------------------------------------------ products
+            constexpr uint32_t iE = tc::idesc_bf16(128, 64, 1, 1), iK = tc::idesc_bf16(128, 64, 0, 0),
+                               iZ = tc::idesc_bf16(128, 128, 0, 1), iZ64 = tc::idesc_bf16(128, 64, 0, 1),
+                               iS = tc::idesc_bf16(128, DK, 0, 1);
+#pragma unroll 1
+            for (int it = 0; it < chunks; ++it) {
+                const uint32_t st = fresh(base + (it & 1) * L::BYTES), ph = it & 1;
+                chain_wait(bars, &bars.full[it & 1], (it >> 1) & 1);
+                if (it > 0) chain_wait(bars, &bars.m3, (it - 1) & 1);
+                tc::tc_fence_after();
+#pragma unroll
+                for (int term = 1; term >= 0; --term)              // P^T dO, both terms of P
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        tc::mma_ss(tm + TM_PU, tc::sdesc(st + L::DO + j * 2048, 8192, 1024),
+                                   tc::sdesc(st + L::P + term * 8192 + j * 2048, 8192, 1024), iE, term == 0 || j != 0);
+                chain_wait(bars, &bars.s, ph);
+                tc::tc_fence_after();
+#pragma unroll
+                for (int term = 0; term < 3; ++term)               // K dS
+#pragma unroll
+                    for (int j = 0; j < DK / 16; ++j) {
+                        const int half = j / (H / 16), jj = j % (H / 16);
+                        const uint32_t a = term < 2 ? TM_S + half * H + term * (H / 2) : TM_X + half * (H / 2);
+                        tc::mma_ts(tm + TM_ACC, tm + a + jj * 8, tc::sdesc(st + L::KQ + (j / 4) * 16384 + (j % 4) * 32, 16, 1024),
+                                   iK, (term | j) != 0);
+                    }
+                tc::mma_commit(&bars.m1);
+                if (it > 0) chain_wait(bars, &bars.out, (it - 1) & 1);   // y of the chunk before is read
+                chain_wait(bars, &bars.x, ph);
+                tc::tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 4; ++j)                        // beta dU [Z_hi | Z_lo], transposed
+                    tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 2048, 8192, 1024), iZ, j != 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + 16 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 2048, 8192, 1024), iZ64, 1);
+                tc::mma_commit(&bars.m2);
+                chain_wait(bars, &bars.d, ph);
+                tc::tc_fence_after();
+#pragma unroll
+                for (int term = 0; term < 3; ++term)               // Q^T (e^G dO)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t a = (term < 2 ? TM_ACC + term * 16 : TM_PU) + (j / 2) * 32 + (j % 2) * 8;
+                        tc::mma_ts(tm + TM_S, tm + a, tc::sdesc(st + L::KQ + 8192 + j * 2048, 16384, 1024), iS, (term | j) != 0);
+                    }
+                chain_wait(bars, &bars.u, ph);
+                tc::tc_fence_after();
+#pragma unroll
+                for (int term = 0; term < 3; ++term)               // - K^T (e^G dV)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t a = TM_UZ + (term < 2 ? term * 16 : 64) + (j / 2) * 32 + (j % 2) * 8;
+                        tc::mma_ts(tm + TM_S, tm + a, tc::sdesc(st + L::KQ + j * 2048, 16384, 1024), iS, 1);
+                    }
+                tc::mma_commit(&bars.m3);
+                tc::mma_commit(&bars.empty[it & 1]);
+            }
+            if (chunks > 0) chain_wait(bars, &bars.m3, (chunks - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp >= kEpiWarps) {            // ------------------------------------------ e^G dO; dV and sums over y
+        regs_down<kRegOut>();
+        const int quarter = warp & 3, row = 32 * quarter + lane, x = threadIdx.x - 32 * kEpiWarps;
+        const bool live = row < dv;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
+        unsigned char* tile = sm + L::OUT;
+#pragma unroll 1
+        for (int it = 0; it < chunks; ++it) {
+            const int c = chunks - 1 - it, tok = start + c * C, nt = min(C, len - c * C);
+            const unsigned char* st = sm + (it & 1) * L::BYTES;
+            const float* vec = reinterpret_cast<const float*>(st + L::VECS);
+            const size_t wh = (size_t)(slot0 + c) * Hv + h;
+            float* part = ws.parts + (wh * strips + quarter) * PARTS;
+            chain_wait(bars, &bars.full[it & 1], (it >> 1) & 1);
+            chain_wait(bars, &bars.x, it & 1);                     // K dS and P^T dO are read: their columns are free
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                float e[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) e[i] = vec[VEC_EG + 32 * half + i] * tile_value(st + L::DO, 32 * half + i, row);
+                const uint32_t to[3] = {tl + TM_ACC + 32 * half, tl + TM_ACC + 32 * half + 16, tl + TM_PU + 32 * half};
+                put_terms<3>(e, to);
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bars.d);
+            chain_wait(bars, &bars.u, it & 1);
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                float y[32];
+                tc::tmem_ld32<32>(tl + TM_ACC + 64 + 32 * half, y);
+                tc::tmem_ld_wait();
+                if (half == 1) {
+                    tc::tc_fence_before();
+                    tc::mbar_arrive(&bars.out);
+                }
+                {
+                    float w[32];
+                    const float4* wp = reinterpret_cast<const float4*>(ws.w + wh * 64 * dv) + (size_t)(8 * half) * dv + (live ? row : 0);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 a = live ? wp[i * dv] : make_float4(0.f, 0.f, 0.f, 0.f);
+                        w[4 * i] = a.x * y[4 * i]; w[4 * i + 1] = a.y * y[4 * i + 1];
+                        w[4 * i + 2] = a.z * y[4 * i + 2]; w[4 * i + 3] = a.w * y[4 * i + 3];
+                    }
+                    const float db = lane_sums(w);
+                    if (quarter < strips) part[PART_DB + 32 * half + lane] = db;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    y[i] *= vec[VEC_BETA + 32 * half + i];
+                    *reinterpret_cast<__nv_bfloat16*>(tile + (32 * half + i) * 256 + 2 * row) = __float2bfloat16_rn(y[i]);
+                    y[i] *= tile_value(st + L::V, 32 * half + i, row);
+                }
+                const float dvv = lane_sums(y);
+                if (quarter < strips) part[PART_DVV + 32 * half + lane] = dvv;
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars.empty[it & 1]);
+            out_sync();
+            rows_out(tile, x, grad_v + ((size_t)tok * Hv + h) * dv, (long long)Hv * dv, nt, dv);
+            out_sync();
+        }
+    } else {                                   // ------------------------------------------ epilogues of the chain
+        regs_up<kRegEpi>();
+        const int quarter = warp & 3, wg = warp >> 2, row = 32 * quarter + lane;
+        const bool live = row < dv;
+        const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
+        float s[H];
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const int d = wg * H + i;
+            s[i] = (dST != nullptr && live && d < dk) ? dST[sbase + (size_t)d * dv + row] : 0.f;
+        }
+#pragma unroll 1
+        for (int it = 0; it <= chunks; ++it) {
+            const int c = chunks - 1 - it;
+            if (it > 0) {                      // dS <- e^{G_C} dS + update
+                const float whole = reinterpret_cast<const float*>(sm + ((it - 1) & 1) * L::BYTES + L::VECS)[VEC_EG + 63];
+                chain_wait(bars, &bars.m3, (it - 1) & 1);
+                tc::tc_fence_after();
+                add_update<H>(s, whole, tl + TM_S + wg * H);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars.empty[(it - 1) & 1]);
+            }
+            if (it < chunks) {
+#pragma unroll
+                for (int i = 0; i < H; i += 32) put_state_terms<3, H>(s + i, tl, wg, i);
+                tc::tmem_st_wait();
+                tc::tc_fence_before();
+                tc::mbar_arrive(&bars.s);
+            }
+            // <S', dS> with the state behind the chunk (after the first chunk: with the one before it), and
+            // dS itself for the gradients of k
+            if (quarter < strips && chunks > 0) {
+                float dot = 0.f;
+                if (live) {
+                    const size_t col = ((size_t)(wg * H / 8) * dv + row) * 8, at0 = ((size_t)(slot0 + c) * Hv + h) * mat + col;
+                    const size_t next = at0 + Hv * mat;
+#pragma unroll
+                    for (int i = 0; i < H; i += 8) {
+                        if (wg * H + i >= dk) break;
+                        const size_t at = (size_t)(i / 8) * dv * 8;
+                        const uint4 a = *reinterpret_cast<const uint4*>(ws.shi + next + at), b = *reinterpret_cast<const uint4*>(ws.slo + next + at);
+                        const uint32_t hi[4] = {a.x, a.y, a.z, a.w}, lo[4] = {b.x, b.y, b.z, b.w};
+                        uint32_t out[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            dot = fmaf(state_lo(hi[j], lo[j]), s[i + 2 * j], dot);
+                            dot = fmaf(state_hi(hi[j], lo[j]), s[i + 2 * j + 1], dot);
+                            out[j] = pack2(s[i + 2 * j], s[i + 2 * j + 1]);
+                        }
+                        if (it < chunks) *reinterpret_cast<uint4*>(ws.dshi + at0 + at) = make_uint4(out[0], out[1], out[2], out[3]);
+                    }
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+                if (lane == 0)
+                    ws.parts[((((size_t)slot0 + max(c, 0)) * Hv + h) * strips + quarter) * PARTS + (it < chunks ? PART_SDS : PART_SDS0) + wg] = dot;
+            }
+            if (it == chunks) break;
+            // dU, and beta dU as an operand
+            const unsigned char* st = sm + (it & 1) * L::BYTES;
+            const float* vec = reinterpret_cast<const float*>(st + L::VECS) + 32 * wg;
+            float x[32], y[32];
+            chain_wait(bars, &bars.full[it & 1], (it >> 1) & 1);
+            chain_wait(bars, &bars.m1, it & 1);
+            tc::tc_fence_after();
+            tc::tmem_ld32<32>(tl + TM_ACC + 32 * wg, x);
+            tc::tmem_ld32<32>(tl + TM_PU + 32 * wg, y);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 dc = *reinterpret_cast<const float4*>(vec + VEC_DEC + i), bt = *reinterpret_cast<const float4*>(vec + VEC_BETA + i);
+                x[i] = fmaf(dc.x, x[i], y[i]);
+                x[i + 1] = fmaf(dc.y, x[i + 1], y[i + 1]);
+                x[i + 2] = fmaf(dc.z, x[i + 2], y[i + 2]);
+                x[i + 3] = fmaf(dc.w, x[i + 3], y[i + 3]);
+                y[i] = bt.x * x[i]; y[i + 1] = bt.y * x[i + 1]; y[i + 2] = bt.z * x[i + 2]; y[i + 3] = bt.w * x[i + 3];
+            }
+            {
+                const uint32_t to[2] = {tl + TM_X + 32 * wg, tl + TM_X + 32 * wg + 16};
+                put_terms<2>(y, to);
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bars.x);
+            // y (to TMEM for the out warps), and - e^G dV as an operand
+            chain_wait(bars, &bars.m2, it & 1);
+            tc::tc_fence_after();
+            tc::tmem_ld32<32>(tl + TM_UZ + 32 * wg, y);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] += y[i];
+            tc::tmem_ld32<32>(tl + TM_UZ + 64 + 32 * wg, y);
+            tc::tmem_ld_wait();
+            {
+                uint32_t r[16];
+#pragma unroll
+                for (int i = 0; i < 32; i += 16) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        x[i + j] += y[i + j];
+                        r[j] = __float_as_uint(x[i + j]);
+                    }
+                    tc::tmem_st32<16>(tl + TM_ACC + 64 + 32 * wg + i, r);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+                const float4 bt = *reinterpret_cast<const float4*>(vec + VEC_BETA + i), eg = *reinterpret_cast<const float4*>(vec + VEC_EG + i);
+                x[i] *= -eg.x * bt.x; x[i + 1] *= -eg.y * bt.y; x[i + 2] *= -eg.z * bt.z; x[i + 3] *= -eg.w * bt.w;
+            }
+            {
+                const uint32_t to[3] = {tl + TM_UZ + 32 * wg, tl + TM_UZ + 32 * wg + 16, tl + TM_UZ + 64 + 32 * wg};
+                put_terms<3>(x, to);
+            }
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bars.u);
+        }
+        if (grad_S0 != nullptr && live) {
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+                const int d = wg * H + i;
+                if (d < dk) grad_S0[sbase + (size_t)d * dv + row] = s[i];
+            }
+        }
+    }
+    chain_end(bars);
+}
+
+}  // namespace gated
+}  // namespace ckda

@@ -49,25 +49,18 @@ struct Seqs {
         len = end - start;
         ok = start == a && end == b;
     }
-    // Every sequence's chunks have places of their own among slots() workspace slots:
-    // ceil(len / C) chunks of a sequence that starts at token s fit between s / C + n and
-    // (s + len) / C + n + 1.
-    __host__ __device__ static size_t slots(int N, int total) { return (size_t)total / C + (size_t)N + 1; }
-    __device__ __forceinline__ int first_slot(int n, int start) const { return start / C + n; }
+    // Every sequence has places of its own among slots() workspace slots, one for each chunk and
+    // one for the state behind the last: ceil(len / C) + 1 places of a sequence that starts at
+    // token s end before (s + len) / C + 2 (n + 1), where the next one's begin.
+    __host__ __device__ static size_t slots(int N, int total) { return (size_t)total / C + 2 * (size_t)N; }
+    __device__ __forceinline__ int first_slot(int n, int start) const { return start / C + 2 * n; }
     // The sequence whose places hold slot s: the last n with first_slot(n) <= s.
     __device__ __forceinline__ int find(int s) const {
-        if (cu == nullptr) {
-            int lo = 0, hi = N - 1;
-            while (lo < hi) {
-                const int m = (lo + hi + 1) / 2;
-                if ((int)(((long long)m * T) / C) + m <= s) lo = m; else hi = m - 1;
-            }
-            return lo;
-        }
         int lo = 0, hi = N - 1;
         while (lo < hi) {
             const int m = (lo + hi + 1) / 2;
-            if (min(max(__ldg(cu + m), 0), total) / C + m <= s) lo = m; else hi = m - 1;
+            const int start = cu == nullptr ? m * T : min(max(__ldg(cu + m), 0), total);
+            if (first_slot(m, start) <= s) lo = m; else hi = m - 1;
         }
         return lo;
     }

@@ -76,6 +76,55 @@ def gated_bwd(q, k, v, g, beta, grad_o, S0=None, grad_S_T=None, cu=None):
     return {n: (torch.zeros(t.shape, dtype=F64) if r is None else r.reshape(t.shape)) for n, r, t in zip(names, got, like)}
 
 
+def grad_squares(q, k, v, g, beta, grad_o, S0=None, grad_S_T=None, cu=None, chunk=64):
+    """For every element of dq and dk: the sum over its products a b of their squares, counted once
+    for each factor that the chunked kernels round to bf16 (states, updates, the weighted pair
+    products and the pair products' own factors). Shapes of q, k; fp64. Their square root times a
+    rounding's standard deviation is that of the element's error before its last rounding."""
+    lead = 2 if cu is None else 1
+    spans = bounds(cu, *(q.shape[:2] if cu is None else ()))
+    qf, kf, vf, gf, bf, of = (_flat(t, lead) for t in (q, k, v, g, beta, grad_o))
+    Hk, dk = qf.shape[1:]
+    Hv, dv = vf.shape[1:]
+    rep = Hv // Hk
+    out_q, out_k = torch.zeros_like(qf), torch.zeros_like(kf)
+    for n, (a, e) in enumerate(spans):
+        for h in range(Hv):
+            kk, qq, vv, gg, bb, oo = kf[a:e, h // rep], qf[a:e, h // rep], vf[a:e, h], gf[a:e, h], bf[a:e, h], of[a:e, h]
+            S = torch.zeros(dk, dv, dtype=F64) if S0 is None else _f64(S0)[n, h]
+            T = e - a
+            starts, U, Rs = {}, torch.zeros(T, dv, dtype=F64), []
+            for t in range(T):
+                if t % chunk == 0:
+                    starts[t] = S
+                R = S * torch.exp(gg[t])
+                U[t] = bb[t] * (vv[t] - R.T @ kk[t])
+                S = R + torch.outer(kk[t], U[t])
+            dS = torch.zeros(dk, dv, dtype=F64) if grad_S_T is None else _f64(grad_S_T)[n, h]
+            ends, dV = {}, torch.zeros(T, dv, dtype=F64)
+            for t in reversed(range(T)):
+                if t == T - 1 or (t + 1) % chunk == 0:
+                    ends[t // chunk * chunk] = dS
+                dS = dS + torch.outer(qq[t], oo[t])
+                dV[t] = bb[t] * (dS.T @ kk[t])
+                dS = (dS - torch.outer(kk[t], dV[t])) * torch.exp(gg[t])
+            for t0, S_in in starts.items():
+                z = slice(t0, min(t0 + chunk, T))
+                G = gg[z].clamp_min(-128.0).cumsum(0)
+                D = torch.exp((G[:, None] - G[None]).clamp_max(0)).tril()
+                eg, dec = torch.exp(G)[:, None], torch.exp(G[-1] - G)[:, None]
+                u, do, dx, qz, kz = U[z], oo[z], dV[z], qq[z], kk[z]
+                Dw, Da = D * (do @ u.T), D.tril(-1) * (dx @ u.T)
+                w2 = Dw ** 2 + D ** 2 * (do ** 2 @ u.T ** 2)              # Dw itself, and u in it
+                a2 = Da ** 2 + 2 * D.tril(-1) ** 2 * (dx ** 2 @ u.T ** 2)  # Da, u and dV in it
+                dS2, S2 = ends[t0].T ** 2, S_in.T ** 2
+                tok = slice(a + t0, a + t0 + u.shape[0])
+                out_q[tok, h // rep] += eg ** 2 * (do ** 2 @ S2) + w2 @ kz ** 2
+                out_k[tok, h // rep] += (2 * eg ** 2 * (dx ** 2 @ S2) + 2 * dec ** 2 * (u ** 2 @ dS2)
+                                         + w2.T @ qz ** 2 + a2 @ kz ** 2 + a2.T @ kz ** 2)
+    return out_q.reshape(q.shape), out_k.reshape(k.shape)
+
+
 def prep(x, positions=None, inv_freq=None, norm="l2", layout="half", weight=None, eps=1e-6, scale=1.0, rope_scale=1.0):
     """x [tokens, heads, d] fp64 (may require grad), positions [tokens], inv_freq [R / 2]."""
     d = x.shape[-1]
