@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "kernels/gated_common.cuh"
@@ -33,18 +34,51 @@ inline ckda_status_t launch_status() { return cudaGetLastError() == cudaSuccess 
 inline size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 int sm_count() {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices] = {};
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();                    // no device: plan for a B200
-        return 148;
+    if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices) {
+        n = known[dev].load(std::memory_order_relaxed);
+        if (n == 0 && cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) known[dev].store(n);
     }
-    return n;
+    if (n > 0) return n;
+    cudaGetLastError();                        // no device: plan for a B200
+    return 148;
 }
 
-// Opt in to more than 48 KB of dynamic shared memory, once per kernel and device.
+// Opt in to more than 48 KB of dynamic shared memory, once per kernel and device (a kernel asks for
+// the same size every time, or for the most it can use). regs != 0: the registers a thread that
+// the kernel has to have been compiled to.
 template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-    return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+cudaError_t kernel_ready(K kernel, size_t bytes, int regs = 0) {
+    constexpr int kDevices = 64;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    struct Entry { const void* f; std::atomic<bool> done[kDevices]; };
+    static Entry entries[64] = {};
+    static std::mutex mu;
+    const void* f = reinterpret_cast<const void*>(kernel);
+    Entry* at = nullptr;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        for (Entry& x : entries)
+            if (x.f == f || x.f == nullptr) {
+                x.f = f;
+                at = &x;
+                break;
+            }
+    }
+    if (at && dev >= 0 && dev < kDevices && at->done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    if (regs != 0) {
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, f);
+        if (e != cudaSuccess) return e;
+        if (a.numRegs != regs) return cudaErrorInvalidConfiguration;
+    }
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && at && dev >= 0 && dev < kDevices) at->done[dev].store(true, std::memory_order_release);
+    return e;
 }
 
 struct Shape {
@@ -114,7 +148,7 @@ ckda_status_t simt_bwd(const Shape& s, const void* q, const void* k, const void*
                        cudaStream_t st) {
     const SimtBwdLayout l = simt_bwd_layout(s);
     auto F = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
-    if (allow_smem(simt_bwd_kernel<TIn>, kSimtBwdSmem) != cudaSuccess) return CKDA_ERR_CUDA;
+    if (kernel_ready(simt_bwd_kernel<TIn>, kSimtBwdSmem) != cudaSuccess) return CKDA_ERR_CUDA;
     simt_bwd_kernel<TIn><<<(unsigned)(s.N * s.Hv), NTB, kSimtBwdSmem, st>>>(
         static_cast<const TIn*>(q), static_cast<const TIn*>(k), static_cast<const TIn*>(v), g, beta, S0,
         static_cast<const TIn*>(grad_o), dST, F(l.ckpt), F(l.scratch), F(l.pq), F(l.pk), static_cast<TIn*>(gv), gg, gb,
@@ -185,7 +219,7 @@ struct Call {
 template <int DK>
 cudaError_t run_intra(const Call& c) {
     constexpr size_t smem = intra_smem(DK);
-    cudaError_t e = allow_smem(intra_kernel<DK>, smem);
+    cudaError_t e = kernel_ready(intra_kernel<DK>, smem);
     if (e != cudaSuccess) return e;
     intra_kernel<DK><<<dim3((unsigned)Seqs::slots(c.s.N, c.s.total), (unsigned)c.s.Hk), 128, smem, c.st>>>(
         c.q, c.k, c.g, c.beta, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.qs, c.ks);
@@ -209,21 +243,11 @@ struct Maps {
     CUtensorMap q, k, v, o;
 };
 
-// The chain kernels move registers between warps: the split adds up only against the register
-// count they were compiled to.
-template <typename K>
-cudaError_t chain_ready(K kernel, size_t smem) {
-    cudaFuncAttributes a;
-    cudaError_t e = cudaFuncGetAttributes(&a, reinterpret_cast<const void*>(kernel));
-    if (e != cudaSuccess) return e;
-    if (a.numRegs != kRegLaunch) return cudaErrorInvalidConfiguration;
-    return allow_smem(kernel, smem);
-}
-
 template <int DK, bool kBack>
 cudaError_t run_chain_fwd(const Call& c, const Maps& m, const ChainIn& in) {
     constexpr size_t smem = ChainStage<DK, kBack>::SMEM;
-    cudaError_t e = chain_ready(chain_fwd_kernel<DK, kBack>, smem);
+    // the register split between warps adds up only against the count it was compiled to
+    cudaError_t e = kernel_ready(chain_fwd_kernel<DK, kBack>, smem, kRegLaunch);
     if (e != cudaSuccess) return e;
     chain_fwd_kernel<DK, kBack><<<(unsigned)(c.s.N * c.s.Hv), kChainThreads, smem, c.st>>>(
         m.q, m.k, m.v, m.o, in, c.S0, c.o, c.ST, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
@@ -232,7 +256,7 @@ cudaError_t run_chain_fwd(const Call& c, const Maps& m, const ChainIn& in) {
 template <int DK>
 cudaError_t run_chain_bwd(const Call& c, const Maps& m, const ChainIn& in) {
     constexpr size_t smem = ChainStage<DK, true>::SMEM;
-    cudaError_t e = chain_ready(chain_bwd_kernel<DK>, smem);
+    cudaError_t e = kernel_ready(chain_bwd_kernel<DK>, smem, kRegLaunch);
     if (e != cudaSuccess) return e;
     chain_bwd_kernel<DK><<<(unsigned)(c.s.N * c.s.Hv), kChainThreads, smem, c.st>>>(
         m.q, m.k, m.v, m.o, in, c.dST, c.gv, c.gS0, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
@@ -241,7 +265,7 @@ cudaError_t run_chain_bwd(const Call& c, const Maps& m, const ChainIn& in) {
 template <int DV>
 cudaError_t run_grads(const Call& c) {
     constexpr size_t smem = GradSmem<DV>::BYTES;
-    cudaError_t e = allow_smem(grad_kernel<DV>, smem);
+    cudaError_t e = kernel_ready(grad_kernel<DV>, smem);
     if (e != cudaSuccess) return e;
     grad_kernel<DV><<<dim3((unsigned)Seqs::slots(c.s.N, c.s.total), (unsigned)c.s.Hk, (unsigned)((c.s.dk + 63) / 64)), 128, smem, c.st>>>(
         c.q, c.k, c.grad_o, c.gv, c.gq, c.gk, c.gg, c.gb, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv, c.qs, c.ks);
@@ -432,10 +456,10 @@ ckda_status_t ckda_gated_decode_step(const void* q, const void* k, const void* v
 
 namespace {
 
-constexpr int kPrepMaxBlocks = 148 * 4;
-
-// Blocks of the backward pass: fixed by the sizes alone, so the weights' sums have one order.
-int prep_blocks(int tokens, int tpb) { return std::max(1, std::min((tokens + tpb - 1) / tpb, kPrepMaxBlocks)); }
+// Blocks of the backward pass, which each leave a partial sum of the weights' gradients: fixed by
+// the sizes alone, so those sums have one order.
+constexpr int kPrepMaxBlocks = 148 * 2;
+int prep_blocks(long long units) { return (int)std::max(1LL, std::min(units, (long long)kPrepMaxBlocks)); }
 
 ckda_status_t prep_args(PrepArgs& a, const void* q, const void* k, const float* qw, const float* kw, const void* pos,
                         int pos64, const double* inv_freq, int tokens, int period, int Hq, int Hk, int d, int rotary,
@@ -461,6 +485,7 @@ ckda_status_t prep_args(PrepArgs& a, const void* q, const void* k, const float* 
     a.pos64 = pos64;
     a.period = std::max(period, 1);
     a.tokens = tokens; a.d = d; a.rotary = rotary; a.norm = norm; a.interleaved = interleaved;
+    a.inv_d = 1.f / (float)d;
     a.eps = eps; a.q_scale = q_scale; a.rope_scale = rope_scale;
     const void* ptrs[] = {q, k, qw, kw};
     for (const void* p : ptrs)
@@ -474,33 +499,28 @@ ckda_status_t prep_args(PrepArgs& a, const void* q, const void* k, const float* 
 bool prep_vector(const PrepArgs& a, ckda_dtype_t dt) {
     const int per16 = dt == CKDA_BF16 ? 8 : 4;
     if (a.d % 8 != 0 || a.stride[0] % per16 != 0 || (a.heads[1] > 0 && a.stride[1] % per16 != 0)) return false;
-    return a.interleaved || a.rotary % 16 == 0;
-}
-
-// Tokens a block takes at a time: enough rows for the block's lanes, not more than spread the
-// tokens over the SMs.
-int prep_tpb(const PrepArgs& a, int groups, int ur) {
-    const int H = a.heads[0] + a.heads[1], sms = sm_count();
-    int tpb = std::max(1, groups * ur / H);
-    while (tpb > 1 && (long long)sms * 2 * tpb > a.tokens) tpb /= 2;
-    return std::min(tpb, 16);
+    return a.rotary % (a.interleaved ? 8 : 16) == 0;
 }
 
 template <typename TIn, bool kBack>
 ckda_status_t prep_launch(const PrepArgs& a, ckda_dtype_t dt, int* blocks_out, cudaStream_t st) {
     constexpr int UR = kBack ? 2 : 4;
     if (prep_vector(a, dt)) {
-        const int G = a.d <= 64 ? 8 : (a.d <= 128 ? 16 : 32);
-        const int groups = 256 / G, tpb = prep_tpb(a, groups, UR);
-        const int blocks = kBack ? prep_blocks(a.tokens, tpb) : (a.tokens + tpb - 1) / tpb;
-        size_t smem = ((size_t)tpb * a.rotary + 2 * a.d) * sizeof(float);
-        if (kBack) smem = std::max(smem, (size_t)groups * a.d * sizeof(float));
+        const int G = a.d <= 64 ? 8 : (a.d <= 128 ? 16 : 32), gp = 32 / G;
+        // Warps to a token: one, more while tokens are too few to give every SM two blocks and the
+        // heads still give each warp a row.
+        int wpt = 1;
+        while (wpt < 8 && (long long)a.tokens * wpt < 16LL * sm_count() && wpt * gp < a.heads[0] + a.heads[1]) wpt *= 2;
+        const long long units = ((long long)a.tokens * wpt + 7) / 8;
+        const int blocks = kBack ? prep_blocks(units) : (int)units;
+        size_t smem = (size_t)8 * a.rotary * sizeof(float);
+        if (kBack) smem = std::max(smem, (size_t)8 * gp * a.d * sizeof(float));
         *blocks_out = blocks;
-        if (G == 8) prep_vec_kernel<TIn, 8, UR, kBack><<<blocks, 256, smem, st>>>(a, tpb);
-        else if (G == 16) prep_vec_kernel<TIn, 16, UR, kBack><<<blocks, 256, smem, st>>>(a, tpb);
-        else prep_vec_kernel<TIn, 32, UR, kBack><<<blocks, 256, smem, st>>>(a, tpb);
+        if (G == 8) prep_vec_kernel<TIn, 8, UR, kBack><<<blocks, 256, smem, st>>>(a, wpt);
+        else if (G == 16) prep_vec_kernel<TIn, 16, UR, kBack><<<blocks, 256, smem, st>>>(a, wpt);
+        else prep_vec_kernel<TIn, 32, UR, kBack><<<blocks, 256, smem, st>>>(a, wpt);
     } else {
-        *blocks_out = prep_blocks(a.tokens, 1);
+        *blocks_out = kBack ? prep_blocks(a.tokens) : std::min(a.tokens, 148 * 8);
         prep_row_kernel<TIn, kBack><<<*blocks_out, 256, 0, st>>>(a);
     }
     return launch_status();
@@ -563,7 +583,7 @@ ckda_status_t ckda_qk_prep_bwd(const void* q, const void* k, const void* grad_q_
     int blocks = 0;
     c = dt == CKDA_BF16 ? prep_launch<bf16, true>(a, dt, &blocks, st) : prep_launch<float, true>(a, dt, &blocks, st);
     if (c != CKDA_OK || !weights) return c;
-    prep_weight_kernel<<<(unsigned)((2 * d + 31) / 32), 256, 0, st>>>(a.partial, blocks, d, grad_q_weight, grad_k_weight);
+    prep_weight_kernel<<<(unsigned)((2 * d + 31) / 32), 1024, 0, st>>>(a.partial, blocks, d, grad_q_weight, grad_k_weight);
     return launch_status();
 }
 
@@ -584,7 +604,7 @@ ckda_status_t ckda_state_copy(float* S, const int* src, const int* dst, int pair
     if (slices > 0x7fffffffLL) return CKDA_ERR_UNSUPPORTED;
     const int table = copy_table(pairs);
     const size_t smem = (size_t)pairs * width * 16 + (size_t)(2 * table + 2 * pairs) * sizeof(int);
-    if (smem > 48 * 1024 && allow_smem(state_copy_kernel, smem) != cudaSuccess) return CKDA_ERR_CUDA;
+    if (smem > 48 * 1024 && kernel_ready(state_copy_kernel, kCopyMaxSmem) != cudaSuccess) return CKDA_ERR_CUDA;
     state_copy_kernel<<<dim3((unsigned)slices, (unsigned)layers), kCopyThreads, smem, as_stream(stream)>>>(
         reinterpret_cast<uint4*>(S), src, dst, pairs, slots, pieces, width, table);
     return launch_status();

@@ -356,6 +356,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t st = fresh(base + (c & 1) * L::BYTES), ph = c & 1;
+                if (c > 0) chain_wait(bars, &bars.qs, (c - 1) & 1);    // Q S of the chunk before is read
                 chain_wait(bars, &bars.s, ph);
                 tc::tc_fence_after();
 #pragma unroll
@@ -378,7 +379,6 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 for (int j = 0; j < 4; ++j)
                     tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + 16 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 32, 16, 1024), i64, 1);
                 tc::mma_commit(&bars.m2);
-                chain_wait(bars, &bars.qs, ph);                    // Q S is read: its columns may be written again
                 chain_wait(bars, &bars.u, ph);
                 tc::tc_fence_after();
 #pragma unroll

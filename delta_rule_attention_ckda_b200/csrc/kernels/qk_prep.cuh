@@ -11,12 +11,16 @@
 //
 // HBM-bound: each row is read once and written once, everything between in fp32 registers, one
 // rounding at the store. The angle is formed and reduced to one turn in 64 bits (a position of
-// a million turns an fp32 angle by 0.06 rad), once per token and pair, shared by all heads
-// through shared memory. Vector path: G lanes per row, 16 bytes each, UR rows per thread in
-// flight; a rotated pair's other half comes from a lane R/16 away. Rows of other sizes or
-// alignments take the scalar path, one warp per row through a row buffer.
+// a million turns an fp32 angle by 0.06 rad), once per token and pair.
+//
+// Vector path: a warp takes a token (several warps where tokens are few), G lanes a head row, 16
+// bytes each, UR rows in flight. What a lane does to a channel is the same for every head of
+// the token, out = r (x A + x' B) with x' the pair's other channel (from a lane R/16 away, or the
+// neighbour in the same register), so weight, cosine, sine and scale are folded into A and B once
+// per token. Warps share nothing and meet at no barrier. Rows of other sizes or alignments take
+// the scalar path, one warp per row through a row buffer.
 #pragma once
-#include "gated_common.cuh"
+#include "gated_mma.cuh"
 
 namespace ckda {
 namespace gated {
@@ -33,7 +37,7 @@ struct PrepArgs {
     const void* pos;               // int32 or int64 positions, or NULL: token % period
     const double* inv_freq;        // [rotary / 2]
     int pos64, period, tokens, d, rotary, norm, interleaved;
-    float eps, q_scale, rope_scale;
+    float eps, inv_d, q_scale, rope_scale;
     float* partial;                // backward: [blocks][2][d] sums of dw, or NULL
 };
 
@@ -48,184 +52,222 @@ __device__ __forceinline__ float2 turn(const PrepArgs& a, int token, int p) {
     return make_float2(c * a.rope_scale, s * a.rope_scale);
 }
 
+// r, and the coefficient c of the gradient's projection (0 where the norm is at its floor).
 __device__ __forceinline__ float norm_factor(const PrepArgs& a, float ss, float& coef) {
     if (a.norm == kNormL2) {
-        const float n = sqrtf(ss);
-        coef = n > 1e-12f ? 1.f : 0.f;
-        return 1.f / fmaxf(n, 1e-12f);
+        const bool above = ss > 1e-24f;
+        coef = above ? 1.f : 0.f;
+        return above ? rsqrtf(ss) : 1e12f;
     }
     if (a.norm == kNormRms) {
-        coef = 1.f / (float)a.d;
-        return 1.f / sqrtf(ss / (float)a.d + a.eps);
+        coef = a.inv_d;
+        return rsqrtf(fmaf(ss, a.inv_d, a.eps));
     }
     coef = 0.f;
     return 1.f;
 }
 
-template <typename T> struct Vec8 { float4 lo, hi; };           // 8 elements as loaded
-template <> struct Vec8<__nv_bfloat16> { uint4 raw; };
-
-__device__ __forceinline__ Vec8<float> ld8(const float* p) {
-    return {*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4)};
-}
-__device__ __forceinline__ Vec8<__nv_bfloat16> ld8(const __nv_bfloat16* p) {
-    return {*reinterpret_cast<const uint4*>(p)};
-}
-__device__ __forceinline__ void unpack8(const Vec8<float>& v, float (&x)[8]) {
-    x[0] = v.lo.x; x[1] = v.lo.y; x[2] = v.lo.z; x[3] = v.lo.w;
-    x[4] = v.hi.x; x[5] = v.hi.y; x[6] = v.hi.z; x[7] = v.hi.w;
-}
-__device__ __forceinline__ void unpack8(const Vec8<__nv_bfloat16>& v, float (&x)[8]) {
-    const uint32_t u[4] = {v.raw.x, v.raw.y, v.raw.z, v.raw.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+// 8 channels of a row as loaded.
+template <typename T> struct Raw8;
+template <> struct Raw8<__nv_bfloat16> {
+    uint32_t r[4];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
     }
-}
-__device__ __forceinline__ void st8(float* p, const float (&x)[8]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
-}
-__device__ __forceinline__ void st8(__nv_bfloat16* p, const float (&x)[8]) {
-    uint32_t u[4];
+    __device__ __forceinline__ void zero() { r[0] = r[1] = r[2] = r[3] = 0u; }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        u[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-}
-
-// Turn the 8 channels at e0 (all lanes of the warp take part). sign = -1 turns back.
-template <int G>
-__device__ __forceinline__ void rotate8(float (&x)[8], const PrepArgs& a, const float2* cs, int e0, float sign) {
-    const int R = a.rotary;
-    if (a.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (e0 + 2 * i < R) {
-                const float2 t = cs[e0 / 2 + i];
-                const float s = sign * t.y, u = x[2 * i], v = x[2 * i + 1];
-                x[2 * i] = u * t.x - v * s;
-                x[2 * i + 1] = v * t.x + u * s;
-            }
-        return;
-    }
-    const int half = R / 2, lane = threadIdx.x & 31, away = half / 8;
-    const bool first = e0 < half, in = e0 < R;
-    const int other = in ? (first ? lane + away : lane - away) : lane;
-    const int p0 = in ? (first ? e0 : e0 - half) : 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float y = __shfl_sync(0xffffffffu, x[i], other);
-        if (in) {
-            const float2 t = cs[p0 + i];
-            const float s = sign * t.y;
-            x[i] = first ? x[i] * t.x - y * s : x[i] * t.x + y * s;
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = lo_of(r[i]);
+            x[2 * i + 1] = hi_of(r[i]);
         }
     }
+    __device__ __forceinline__ Raw8 swapped() const {
+        Raw8 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o.r[i] = __byte_perm(r[i], r[i], 0x1032);
+        return o;
+    }
+    __device__ __forceinline__ Raw8 from_lane(int lane, bool use) const {
+        Raw8 o;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o.r[i] = __shfl_sync(0xffffffffu, r[i], lane);
+            if (!use) o.r[i] = 0u;
+        }
+        return o;
+    }
+    __device__ static __forceinline__ void store(__nv_bfloat16* p, const float (&x)[8]) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+    }
+};
+template <> struct Raw8<float> {
+    float r[8];
+    __device__ __forceinline__ void load(const float* p) {
+        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+        r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w; r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = 0.f;
+    }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = r[i];
+    }
+    __device__ __forceinline__ Raw8 swapped() const {
+        Raw8 o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.r[i] = r[i ^ 1];
+        return o;
+    }
+    __device__ __forceinline__ Raw8 from_lane(int lane, bool use) const {
+        Raw8 o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            o.r[i] = __shfl_sync(0xffffffffu, r[i], lane);
+            if (!use) o.r[i] = 0.f;
+        }
+        return o;
+    }
+    __device__ static __forceinline__ void store(float* p, const float (&x)[8]) {
+        *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    }
+};
+
+template <int G>
+__device__ __forceinline__ float group_sum(float x) {
+#pragma unroll
+    for (int off = G / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
 }
 
-// Vector path: d a multiple of 8, rows 16-byte aligned, half layout with R a multiple of 16.
-// A block takes `tpb` tokens at a time (all their heads), grid-stride over the tokens.
+// Vector path: d a multiple of 8, rows 16-byte aligned, R a multiple of 16 (half) or 8 (interleaved).
+// `wpt` warps share a token's heads.
 template <typename TIn, int G, int UR, bool kBack>
 __global__ void __launch_bounds__(256)
-prep_vec_kernel(const PrepArgs a, int tpb) {
+prep_vec_kernel(const PrepArgs a, int wpt) {
     extern __shared__ __align__(16) float smf[];
-    constexpr int GROUPS = 256 / G;
-    const int half = a.rotary / 2, H = a.heads[0] + a.heads[1];
-    float2* cs = reinterpret_cast<float2*>(smf);                // [tpb][half]
-    float* sw = smf + 2 * tpb * half;                           // [2][d] weights, then the dw reduction
-    const int lane = threadIdx.x % G, grp = threadIdx.x / G, e0 = 8 * lane;
-    const bool live = e0 < a.d;
-    for (int i = threadIdx.x; i < 2 * a.d; i += 256) {
-        const float* w = a.w[i / a.d];
-        sw[i] = w ? w[i % a.d] : 1.f;
-    }
+    constexpr int GP = 32 / G;                                  // rows a warp takes at once
+    const int half = a.rotary / 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, e0 = 8 * l;
+    float2* cs = reinterpret_cast<float2*>(smf) + warp * half;
+    const bool live = e0 < a.d, in = e0 < a.rotary, first = a.interleaved || e0 < half;
+    const int other = in && !a.interleaved ? (first ? lane + half / 8 : lane - half / 8) : lane;
+    const int eo = in && !a.interleaved ? (first ? e0 + half : e0 - half) : e0;      // the partners' channels
+    const int p0 = a.interleaved ? e0 / 2 : (first ? e0 : e0 - half);
     float acc[2][8];
     if constexpr (kBack) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = 0.f;
     }
-    for (int t0 = blockIdx.x * tpb; t0 < a.tokens; t0 += gridDim.x * tpb) {
-        const int rows = min(tpb, a.tokens - t0) * H;
-        for (int r0 = 0; r0 < rows; r0 += GROUPS * UR) {
-            Vec8<TIn> vx[UR], vd[kBack ? UR : 1];
+    const int per = 8 / wpt;                                    // tokens a block takes at once
+    for (int t = blockIdx.x * per + warp / wpt; t < a.tokens; t += gridDim.x * per) {
+        if (half) {
+            __syncwarp();
+            for (int p = lane; p < half; p += 32) cs[p] = turn(a, t, p);
+            __syncwarp();
+        }
 #pragma unroll
-            for (int j = 0; j < UR; ++j) {                      // all loads of the pass in flight
-                const int r = r0 + j * GROUPS + grp;
-                if (r < rows && live) {
-                    const int tok = t0 + r / H, h = r % H, which = h >= a.heads[0], hh = which ? h - a.heads[0] : h;
-                    vx[j] = ld8(static_cast<const TIn*>(a.x[which]) + tok * a.stride[which] + (long long)hh * a.d + e0);
-                    if constexpr (kBack)
-                        vd[j] = ld8(static_cast<const TIn*>(a.dy[which]) + ((long long)tok * a.heads[which] + hh) * a.d + e0);
+        for (int which = 0; which < 2; ++which) {
+            if (a.heads[which] == 0) continue;
+            const float scale = which ? 1.f : a.q_scale;
+            const float* w = a.w[which];
+            const TIn* xp = static_cast<const TIn*>(a.x[which]) + t * a.stride[which] + e0;
+            const long long row0 = (long long)t * a.heads[which] * a.d + e0;
+            const TIn* dp = kBack ? static_cast<const TIn*>(a.dy[which]) + row0 : nullptr;
+            TIn* op = static_cast<TIn*>(a.out[which]) + row0;
+            // forward: A, B with the weights of the channel and of its partner; backward: of dy, without
+            float A[8], B[8], wt[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float we = w && live ? __ldg(w + e0 + i) : 1.f;
+                const float wo = kBack ? 1.f : (w && live ? __ldg(w + (a.interleaved ? (e0 + i) ^ 1 : eo + i) % a.d) : 1.f);
+                const float own = kBack ? scale : we * scale;
+                A[i] = own;
+                B[i] = 0.f;
+                if constexpr (kBack) wt[i] = we;
+                if (in) {
+                    const float2 c = cs[a.interleaved ? p0 + i / 2 : p0 + i];
+                    const bool plus = a.interleaved ? (i & 1) : !first;              // the sine's sign, turned back in reverse
+                    A[i] = own * c.x;
+                    B[i] = wo * scale * (plus != kBack ? c.y : -c.y);
                 }
             }
-            if (r0 == 0) {
-                __syncthreads();                                // the tokens before are done with cs
-                for (int i = threadIdx.x; i < min(tpb, a.tokens - t0) * half; i += 256)
-                    cs[i] = turn(a, t0 + i / half, i % half);
-                __syncthreads();
-            }
+            for (int hb = (warp % wpt) * GP; hb < a.heads[which]; hb += wpt * GP * UR) {
+                Raw8<TIn> rx[UR], rd[kBack ? UR : 1];
 #pragma unroll
-            for (int j = 0; j < UR; ++j) {
-                const int r = r0 + j * GROUPS + grp;
-                if (r0 + j * GROUPS >= rows) break;             // uniform in the block
-                const bool on = r < rows && live;
-                const int rr = r < rows ? r : rows - 1;
-                const int lt = rr / H, h = rr % H, which = h >= a.heads[0], hh = which ? h - a.heads[0] : h;
-                float x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = 0.f;
-                if (on) unpack8(vx[j], x);
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-                for (int off = G / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-                float coef;
-                const float f = norm_factor(a, ss, coef);
-                const float scale = which ? 1.f : a.q_scale;
-                const float* w = sw + which * a.d + (live ? e0 : 0);
-                const float2* c = cs + lt * half;
-                if constexpr (!kBack) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = x[i] * f * w[i] * scale;
-                    if (half) rotate8<G>(x, a, c, e0, 1.f);
-                } else {
-                    float z[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) z[i] = 0.f;
-                    if (on) unpack8(vd[j], z);
-                    if (half) rotate8<G>(z, a, c, e0, -1.f);
-                    float dot = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        x[i] *= f;
-                        z[i] *= scale;
-                        const float dw = z[i] * x[i];
-                        if (which) acc[1][i] += dw; else acc[0][i] += dw;
-                        z[i] *= w[i];
-                        dot = fmaf(z[i], x[i], dot);
+                for (int j = 0; j < UR; ++j) {                  // all loads in flight
+                    const int h = hb + j * wpt * GP + lane / G;
+                    const bool on = live && h < a.heads[which];
+                    rx[j].zero();
+                    if (on) rx[j].load(xp + (long long)h * a.d);
+                    if constexpr (kBack) {
+                        rd[j].zero();
+                        if (on) rd[j].load(dp + (long long)h * a.d);
                     }
-#pragma unroll
-                    for (int off = G / 2; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = f * (z[i] - x[i] * (dot * coef));
                 }
-                if (on) st8(static_cast<TIn*>(a.out[which]) + ((long long)(t0 + lt) * a.heads[which] + hh) * a.d + e0, x);
+#pragma unroll
+                for (int j = 0; j < UR; ++j) {
+                    if (hb + j * wpt * GP >= a.heads[which]) break;                  // the warp's rows are done
+                    const int h = hb + j * wpt * GP + lane / G;
+                    float x[8], y[8];
+                    rx[j].unpack(x);
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) fma2(s0, s1, x[i], x[i + 1], x[i], x[i + 1]);
+                    float coef;
+                    const float f = norm_factor(a, group_sum<G>(s0 + s1), coef);
+                    const Raw8<TIn>& turned = kBack ? rd[kBack ? j : 0] : rx[j];
+                    (a.interleaved ? turned.swapped() : turned.from_lane(other, in)).unpack(y);
+                    if (a.interleaved && !in) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[i] = 0.f;
+                    }
+                    if constexpr (!kBack) {
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            mul2(x[i], x[i + 1], A[i], A[i + 1]);
+                            fma2(x[i], x[i + 1], y[i], y[i + 1], B[i], B[i + 1]);
+                            mul2(x[i], x[i + 1], f, f);
+                        }
+                    } else {
+                        float z[8], d0 = 0.f, d1 = 0.f;
+                        rd[j].unpack(z);
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            mul2(z[i], z[i + 1], A[i], A[i + 1]);
+                            fma2(z[i], z[i + 1], y[i], y[i + 1], B[i], B[i + 1]);
+                            mul2(x[i], x[i + 1], f, f);                              // xh
+                            fma2(acc[which][i], acc[which][i + 1], z[i], z[i + 1], x[i], x[i + 1]);
+                            mul2(z[i], z[i + 1], wt[i], wt[i + 1]);
+                            fma2(d0, d1, z[i], z[i + 1], x[i], x[i + 1]);
+                        }
+                        const float c = -coef * group_sum<G>(d0 + d1);
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            fma2(z[i], z[i + 1], x[i], x[i + 1], c, c);
+                            x[i] = z[i];
+                            x[i + 1] = z[i + 1];
+                            mul2(x[i], x[i + 1], f, f);
+                        }
+                    }
+                    if (live && h < a.heads[which]) Raw8<TIn>::store(op + (long long)h * a.d, x);
+                }
             }
         }
     }
     if constexpr (kBack) {
         if (a.partial == nullptr) return;
+        constexpr int GROUPS = 8 * GP;
+        float* red = smf;                                       // [GROUPS][d], over the angles
+#pragma unroll
         for (int s = 0; s < 2; ++s) {                           // groups in turn: one order of the sum
             __syncthreads();
-            float* red = smf;                                   // [GROUPS][d], over the angles
             if (live)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) red[grp * a.d + e0 + i] = s ? acc[1][i] : acc[0][i];
+                for (int i = 0; i < 8; ++i) red[(threadIdx.x / G) * a.d + e0 + i] = acc[s][i];
             __syncthreads();
             for (int c = threadIdx.x; c < a.d; c += 256) {
                 float sum = 0.f;
@@ -329,19 +371,23 @@ prep_row_kernel(const PrepArgs a) {
 }
 
 // dw of q (columns 0 .. d-1) and k (d .. 2d-1): the blocks' partial sums in a fixed order, one
-// block of 256 threads per 32 columns (8 strands of blocks, then the strands).
-__global__ void __launch_bounds__(256)
+// block of 1024 threads per 32 columns: 32 strands of blocks, each with its loads in flight, then
+// the strands.
+__global__ void __launch_bounds__(1024)
 prep_weight_kernel(const float* __restrict__ partial, int blocks, int d, float* __restrict__ dwq, float* __restrict__ dwk) {
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     const int lane = threadIdx.x & 31, strand = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float sum = 0.f;
-    if (c < 2 * d)
-        for (int b = strand; b < blocks; b += 8) sum += partial[(size_t)b * 2 * d + c];
+    if (c < 2 * d) {
+#pragma unroll 8
+        for (int b = strand; b < blocks; b += 32) sum += partial[(size_t)b * 2 * d + c];
+    }
     red[strand][lane] = sum;
     __syncthreads();
     if (strand == 0 && c < 2 * d) {
         float s = 0.f;
-        for (int i = 0; i < 8; ++i) s += red[i][lane];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s += red[i][lane];
         float* out = c < d ? dwq : dwk;
         if (out) out[c < d ? c : c - d] = s;
     }

@@ -16,6 +16,7 @@ namespace gated {
 
 constexpr int kCopyMaxPairs = 1024;
 constexpr int kCopyThreads = 256;
+constexpr size_t kCopyMaxSmem = 1024 * 8 * 16 + (2 * 2048 + 2 * 1024) * 4;     // the narrowest slice of the most pairs, and its table
 
 __host__ __device__ inline int copy_table(int pairs) {
     int n = 2;

@@ -17,35 +17,55 @@ to token). The full conventions are in include/ckda.h.
 """
 from __future__ import annotations
 
+from functools import lru_cache
+from math import prod
 from typing import Optional, Tuple
 
 import torch
 
-from ._lib import _check, _device, _dt, _ptr, _raise, _stream, load
+from ._lib import _device, _dt, _raise, load
 
 NORMS = {"none": 0, "l2": 1, "rms": 2}          # ckda_prep_norm_t
 LAYOUTS = {"half": 0, "interleaved": 1}
 MAX_COPY_PAIRS = 1024
+F32, I32 = torch.float32, torch.int32
 
 
-def _rows(t: torch.Tensor, name: str, lead: int, dtype, device) -> int:
-    """Checks a tensor of rows [..., heads, d] with `lead` leading token dimensions whose heads
-    and channels are contiguous; returns the distance from token to token in elements."""
+# The checks below run in front of calls of a few microseconds, so each is a few comparisons.
+
+def _on(t, name: str, dev) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {device}")
+    if t.device != dev:
+        if t.device.type != "cuda":
+            raise ValueError(f"{name} must be a CUDA tensor (no CPU path)")
+        raise ValueError(f"{name} is on {t.device}, the call's tensors are on {dev}")
+
+
+def _check(t, name: str, shape, dtype, dev) -> None:
+    """Type, device, shape, dtype and contiguity of one tensor argument."""
+    _on(t, name, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows(t, name: str, lead: int, dtype, dev) -> int:
+    """Checks a tensor of rows [..., heads, d] with `lead` leading token dimensions whose heads
+    and channels are contiguous; returns the distance from token to token in elements."""
+    _on(t, name, dev)
     if t.dim() != lead + 2:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {lead + 2} dimensions")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     heads, d = t.shape[-2:]
     inner = heads * d
-    st = t.stride()
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return max(inner, 1)
+    st = t.stride()
     if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d):
         raise ValueError(f"{name} must have contiguous heads and channels, has strides {st}")
     row = None                                    # the distance between tokens, over every leading dimension
@@ -63,74 +83,122 @@ def _rows(t: torch.Tensor, name: str, lead: int, dtype, device) -> int:
     return row
 
 
-def _int32(t: torch.Tensor, name: str, n: Optional[int], device):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    _check(t, name, tuple(t.shape) if n is None else (n,), torch.int32, device)
-    if t.dim() != 1:
-        raise ValueError(f"{name} must have one dimension, has shape {tuple(t.shape)}")
+def _indexes(t, name: str, n: Optional[int], dev) -> None:
+    _on(t, name, dev)
+    if t.dim() != 1 or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {'one dimension' if n is None else (n,)}")
+    if t.dtype != I32:
+        raise TypeError(f"{name} must be {I32}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _apart(out: Optional[torch.Tensor], name: str, others) -> None:
-    """An output that shares memory with an input (or another output) it must not share it with."""
-    if out is None or out.numel() == 0:
+def _span(t):
+    """[first, end) of a tensor's memory; None for no tensor or an empty one."""
+    if t is None:
+        return None
+    n = t.numel()
+    if n == 0:
+        return None
+    a = t.data_ptr()
+    if not t.is_contiguous():
+        n = sum((k - 1) * s for k, s in zip(t.shape, t.stride())) + 1
+    return a, a + n * t.element_size()
+
+
+def _apart(out, name: str, others) -> None:
+    """An output may share memory with none of `others` ((name, span) pairs of _span)."""
+    mine = _span(out)
+    if mine is None:
         return
-    a0 = out.data_ptr()
-    a1 = a0 + out.numel() * out.element_size()
-    for other, t in others.items():
-        if t is None or t.numel() == 0:
-            continue
-        b0 = t.data_ptr()
-        b1 = b0 + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
-        if a0 < b1 and b0 < a1:
+    a, b = mine
+    for other, span in others:
+        if span is not None and a < span[1] and span[0] < b:
             raise ValueError(f"{name} overlaps {other}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(dev, stream, fn, where: str, args) -> None:
+    """Calls fn(*args, stream) with `dev` as the current device, which the library launches on."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the call's tensors are on {dev}")
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream.cuda_stream)
+    _raise(st, where)
+
+
+@lru_cache(maxsize=4096)
+def _bytes(which: str, device_index: int, sizes) -> int:
+    """A workspace query: a function of the sizes and the device alone."""
+    with torch.cuda.device(device_index):
+        return int(getattr(load(), which)(*sizes))
+
+
+def _workspace(which: str, dev, sizes, workspace):
+    need = _bytes(which, dev.index, sizes)
+    if workspace is None:
+        if need == 0:
+            return None, 0
+        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
+        return workspace, need
+    _on(workspace, "workspace", dev)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _call_device(t, name: str = "q"):
+    dev = _device(t, name)
+    return dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
 class _Problem:
     """The checked inputs of a gated delta rule call."""
 
     def __init__(self, q, k, v, g, beta, S0, cu_seqlens):
-        dev = self.dev = _device(q)
+        dev = self.dev = _call_device(q)
         packed = cu_seqlens is not None
         lead = 1 if packed else 2
-        self.qs = _rows(q, "q", lead, None, dev)
+        qs = _rows(q, "q", lead, None, dev)
         dt = q.dtype
         self.dt = _dt(q)
-        self.ks = _rows(k, "k", lead, dt, dev)
-        self.vs = _rows(v, "v", lead, dt, dev)
+        ks, vs = _rows(k, "k", lead, dt, dev), _rows(v, "v", lead, dt, dev)
         tokens = tuple(q.shape[:lead])
-        self.Hk, self.dk = q.shape[-2:]
-        self.Hv, self.dv = v.shape[-2:]
-        if tuple(k.shape) != tuple(q.shape):
+        Hk, dk = q.shape[-2:]
+        Hv, dv = v.shape[-2:]
+        if k.shape != q.shape:
             raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(q.shape)}")
         if tuple(v.shape[:lead]) != tokens:
-            raise ValueError(f"v has shape {tuple(v.shape)}, expected {tokens + (self.Hv, self.dv)}")
-        if self.Hk < 1 or self.Hv % max(self.Hk, 1) != 0 or self.Hv < 1:
-            raise ValueError(f"v has {self.Hv} heads, not a multiple of the {self.Hk} of q and k")
-        _check(g, "g", tokens + (self.Hv,), torch.float32, dev)
-        _check(beta, "beta", tokens + (self.Hv,), torch.float32, dev)
+            raise ValueError(f"v has shape {tuple(v.shape)}, expected {tokens + (Hv, dv)}")
+        if Hk < 1 or Hv < 1 or Hv % Hk != 0:
+            raise ValueError(f"v has {Hv} heads, not a multiple of the {Hk} of q and k")
+        _check(g, "g", tokens + (Hv,), F32, dev)
+        _check(beta, "beta", tokens + (Hv,), F32, dev)
         if packed:
-            _int32(cu_seqlens, "cu_seqlens", None, dev)
-            if cu_seqlens.numel() < 1:
+            _indexes(cu_seqlens, "cu_seqlens", None, dev)
+            if cu_seqlens.shape[0] < 1:
                 raise ValueError("cu_seqlens must hold N + 1 offsets")
-            self.N, self.T, self.total = cu_seqlens.numel() - 1, 0, tokens[0]
+            N, T, total = cu_seqlens.shape[0] - 1, 0, tokens[0]
         else:
-            self.N, self.T = tokens
-            self.total = self.N * self.T
-        self.o_shape = tokens + (self.Hv, self.dv)
-        self.state_shape = (self.N, self.Hv, self.dk, self.dv)
+            N, T = tokens
+            total = N * T
+        self.o_shape = tokens + (Hv, dv)
+        self.g_shape = tokens + (Hv,)
+        self.state_shape = (N, Hv, dk, dv)
         if S0 is not None:
-            _check(S0, "S0", self.state_shape, torch.float32, dev)
-        self.inputs = {"q": q, "k": k, "v": v, "g": g, "beta": beta, "cu_seqlens": cu_seqlens}
-        self.sizes = (self.N, self.T, self.total, self.Hk, self.Hv, self.dk, self.dv, self.qs, self.ks, self.vs, self.dt)
-        self.ws_sizes = (self.N, self.total, self.Hk, self.Hv, self.dk, self.dv, self.dt)
-
-    def workspace(self, need: int, workspace):
-        if need and workspace is None:
-            workspace = torch.empty(need, device=self.dev, dtype=torch.uint8)
-        if workspace is not None:
-            _check(workspace, "workspace", tuple(workspace.shape), None, self.dev)
-        return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+            _check(S0, "S0", self.state_shape, F32, dev)
+        self.spans = [("q", _span(q)), ("k", _span(k)), ("v", _span(v)), ("g", _span(g)), ("beta", _span(beta)),
+                      ("cu_seqlens", _span(cu_seqlens))]
+        self.sizes = (N, T, total, Hk, Hv, dk, dv, qs, ks, vs, self.dt)
+        self.ws_sizes = (N, total, Hk, Hv, dk, dv, self.dt)
 
 
 def gated_fwd_workspace_bytes(N, total, Hk, Hv, dk, dv, dtype=torch.bfloat16) -> int:
@@ -143,23 +211,23 @@ def gated_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, o=None, S_T=N
     sequence are not written), S_T [N, Hv, dk, dv] fp32, which may be S0 itself. Allocates o, S_T
     and the workspace with torch when not given."""
     p = _Problem(q, k, v, g, beta, S0, cu_seqlens)
+    dev = p.dev
+    spans = p.spans
     if o is None:
-        o = torch.empty(p.o_shape, device=p.dev, dtype=v.dtype)
-    _check(o, "o", p.o_shape, v.dtype, p.dev)
-    if S_T is None and want_state:
-        S_T = torch.empty(p.state_shape, device=p.dev, dtype=torch.float32)
+        o = torch.empty(p.o_shape, device=dev, dtype=v.dtype)
+    else:
+        _check(o, "o", p.o_shape, v.dtype, dev)
+        _apart(o, "o", spans + [("S0", _span(S0))])
     if S_T is not None:
-        _check(S_T, "S_T", p.state_shape, torch.float32, p.dev)
-        _apart(S_T, "S_T", {**p.inputs, "o": o})
-        if S0 is not None and S_T.data_ptr() != S0.data_ptr():
-            _apart(S_T, "S_T", {"S0": S0})
-    _apart(o, "o", {**p.inputs, "S0": S0})
-    lib = load()
-    with torch.cuda.device(p.dev):
-        workspace, wbytes = p.workspace(int(lib.ckda_gated_fwd_workspace_bytes(*p.ws_sizes)), workspace)
-        st = lib.ckda_gated_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(o), _ptr(S_T),
-                                _ptr(cu_seqlens), *p.sizes, _ptr(workspace), wbytes, _stream(stream, p.dev))
-    _raise(st, "ckda_gated_fwd")
+        _check(S_T, "S_T", p.state_shape, F32, dev)
+        same = S0 is not None and S_T.data_ptr() == S0.data_ptr()
+        _apart(S_T, "S_T", spans + [("o", _span(o))] + ([] if same else [("S0", _span(S0))]))
+    elif want_state:
+        S_T = torch.empty(p.state_shape, device=dev, dtype=F32)
+    workspace, wbytes = _workspace("ckda_gated_fwd_workspace_bytes", dev, p.ws_sizes, workspace)
+    _launch(dev, stream, load().ckda_gated_fwd, "ckda_gated_fwd",
+            (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(o), _ptr(S_T), _ptr(cu_seqlens), *p.sizes,
+             _ptr(workspace), wbytes))
     return o, S_T
 
 
@@ -173,34 +241,32 @@ def gated_bwd(q, k, v, g, beta, grad_o, S0=None, grad_S_T=None, *, cu_seqlens=No
     dict with dq, dk, dv (in q's type), dg, dbeta, dS0 (fp32; dS0 None unless want_dS0). Output
     tensors may be passed in `grads` (same keys); dS0 may be grad_S_T itself."""
     p = _Problem(q, k, v, g, beta, S0, cu_seqlens)
-    _check(grad_o, "grad_o", p.o_shape, v.dtype, p.dev)
+    dev = p.dev
+    _check(grad_o, "grad_o", p.o_shape, v.dtype, dev)
     if grad_S_T is not None:
-        _check(grad_S_T, "grad_S_T", p.state_shape, torch.float32, p.dev)
+        _check(grad_S_T, "grad_S_T", p.state_shape, F32, dev)
     got = dict(grads or {})
-    f32 = torch.float32
-    shapes = {"dq": (tuple(q.shape), q.dtype), "dk": (tuple(q.shape), q.dtype), "dv": (p.o_shape, q.dtype),
-              "dg": (tuple(g.shape), f32), "dbeta": (tuple(g.shape), f32), "dS0": (p.state_shape, f32)}
+    shapes = {"dq": (q.shape, q.dtype), "dk": (q.shape, q.dtype), "dv": (p.o_shape, q.dtype), "dg": (p.g_shape, F32),
+              "dbeta": (p.g_shape, F32), "dS0": (p.state_shape, F32)}
+    given = []
     for name, (shape, dtype) in shapes.items():
         if name == "dS0" and not want_dS0:
             got[name] = None
-            continue
-        if got.get(name) is None:
-            got[name] = torch.empty(shape, device=p.dev, dtype=dtype)
-        _check(got[name], name, shape, dtype, p.dev)
-    for i, name in enumerate(shapes):
-        others = {**p.inputs, "grad_o": grad_o, "S0": S0, "grad_S_T": grad_S_T}
-        others.update({n: got[n] for n in list(shapes)[:i]})
-        if name == "dS0" and got[name] is not None and grad_S_T is not None and got[name].data_ptr() == grad_S_T.data_ptr():
-            others.pop("grad_S_T")
+        elif got.get(name) is None:
+            got[name] = torch.empty(shape, device=dev, dtype=dtype)
+        else:
+            _check(got[name], name, shape, dtype, dev)
+            given.append(name)
+    for i, name in enumerate(given):
+        others = p.spans + [("grad_o", _span(grad_o)), ("S0", _span(S0))] + [(n, _span(got[n])) for n in given[:i]]
+        if not (name == "dS0" and grad_S_T is not None and got[name].data_ptr() == grad_S_T.data_ptr()):
+            others.append(("grad_S_T", _span(grad_S_T)))
         _apart(got[name], name, others)
-    lib = load()
-    with torch.cuda.device(p.dev):
-        workspace, wbytes = p.workspace(int(lib.ckda_gated_bwd_workspace_bytes(*p.ws_sizes)), workspace)
-        st = lib.ckda_gated_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(grad_o), _ptr(grad_S_T),
-                                _ptr(got["dq"]), _ptr(got["dk"]), _ptr(got["dv"]), _ptr(got["dg"]), _ptr(got["dbeta"]),
-                                _ptr(got["dS0"]), _ptr(cu_seqlens), *p.sizes, _ptr(workspace), wbytes,
-                                _stream(stream, p.dev))
-    _raise(st, "ckda_gated_bwd")
+    workspace, wbytes = _workspace("ckda_gated_bwd_workspace_bytes", dev, p.ws_sizes, workspace)
+    _launch(dev, stream, load().ckda_gated_bwd, "ckda_gated_bwd",
+            (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(grad_o), _ptr(grad_S_T), _ptr(got["dq"]),
+             _ptr(got["dk"]), _ptr(got["dv"]), _ptr(got["dg"]), _ptr(got["dbeta"]), _ptr(got["dS0"]), _ptr(cu_seqlens),
+             *p.sizes, _ptr(workspace), wbytes))
     return got
 
 
@@ -208,38 +274,38 @@ def gated_decode_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None) -
     """ckda_gated_decode_step: one token of N sequences, q, k [N, Hk, dk], v [N, Hv, dv], g, beta
     [N, Hv]. Updates states of the pool S [P, Hv, dk, dv] in place: row n's is S[slots[n]] (int32;
     None: S[n]); rows with a negative slot are padding and keep their o. Returns o [N, Hv, dv]."""
-    dev = _device(q)
+    dev = _call_device(q)
     qs = _rows(q, "q", 1, None, dev)
     dt = q.dtype
     ks, vs = _rows(k, "k", 1, dt, dev), _rows(v, "v", 1, dt, dev)
     N, Hk, dk = q.shape
-    Hv, dv = v.shape[-2:]
-    if tuple(k.shape) != tuple(q.shape):
+    Hv, dv = v.shape[1:]
+    if k.shape != q.shape:
         raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(q.shape)}")
     if v.shape[0] != N:
         raise ValueError(f"v has shape {tuple(v.shape)}, expected {(N, Hv, dv)}")
     if Hk < 1 or Hv < 1 or Hv % Hk != 0:
         raise ValueError(f"v has {Hv} heads, not a multiple of the {Hk} of q and k")
-    _check(g, "g", (N, Hv), torch.float32, dev)
-    _check(beta, "beta", (N, Hv), torch.float32, dev)
+    _check(g, "g", (N, Hv), F32, dev)
+    _check(beta, "beta", (N, Hv), F32, dev)
     if not isinstance(S, torch.Tensor) or S.dim() != 4:
         raise ValueError("S must be a [pool, Hv, dk, dv] tensor")
-    _check(S, "S", (S.shape[0], Hv, dk, dv), torch.float32, dev)
-    if slots is None:
-        if S.shape[0] < N:
-            raise ValueError(f"S holds {S.shape[0]} states, the call has {N} rows")
-    else:
-        _int32(slots, "slots", N, dev)
+    pool = S.shape[0]
+    _check(S, "S", (pool, Hv, dk, dv), F32, dev)
+    if slots is not None:
+        _indexes(slots, "slots", N, dev)
+    elif pool < N:
+        raise ValueError(f"S holds {pool} states, the call has {N} rows")
+    spans = [("q", _span(q)), ("k", _span(k)), ("v", _span(v)), ("g", _span(g)), ("beta", _span(beta)), ("slots", _span(slots))]
+    _apart(S, "S", spans)
     if o is None:
-        o = torch.empty(N, Hv, dv, device=dev, dtype=dt)
-    _check(o, "o", (N, Hv, dv), dt, dev)
-    inputs = {"q": q, "k": k, "v": v, "g": g, "beta": beta, "slots": slots}
-    _apart(o, "o", {**inputs, "S": S})
-    _apart(S, "S", inputs)
-    with torch.cuda.device(dev):
-        st = load().ckda_gated_decode_step(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), _ptr(o), _ptr(slots),
-                                           N, S.shape[0], Hk, Hv, dk, dv, qs, ks, vs, _dt(q), _stream(stream, dev))
-    _raise(st, "ckda_gated_decode_step")
+        o = torch.empty((N, Hv, dv), device=dev, dtype=dt)
+    else:
+        _check(o, "o", (N, Hv, dv), dt, dev)
+        _apart(o, "o", spans + [("S", _span(S))])
+    _launch(dev, stream, load().ckda_gated_decode_step, "ckda_gated_decode_step",
+            (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), _ptr(o), _ptr(slots), N, pool, Hk, Hv, dk, dv, qs, ks,
+             vs, _dt(q)))
     return o
 
 
@@ -247,7 +313,7 @@ class _Prep:
     """The checked arguments that qk_norm_rope and its backward share."""
 
     def __init__(self, q, k, positions, inv_freq, norm, layout, q_weight, k_weight, eps, q_scale, rope_scale):
-        dev = self.dev = _device(q)
+        dev = self.dev = _call_device(q)
         if q.dim() < 3:
             raise ValueError(f"q has shape {tuple(q.shape)}, expected [..., heads, d]")
         lead = q.dim() - 2
@@ -261,9 +327,7 @@ class _Prep:
             if tuple(k.shape[:-2]) != self.tokens_shape or k.shape[-1] != self.d:
                 raise ValueError(f"k has shape {tuple(k.shape)}, expected {self.tokens_shape + (k.shape[-2], self.d)}")
             self.Hk = k.shape[-2]
-        tokens = 1
-        for n in self.tokens_shape:
-            tokens *= n
+        tokens = prod(self.tokens_shape)
         if tokens > 0x7fffffff:
             raise ValueError("more than 2**31 - 1 tokens")
         if norm not in NORMS:
@@ -272,12 +336,12 @@ class _Prep:
             raise ValueError(f"layout must be one of {sorted(LAYOUTS)}, got {layout!r}")
         for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
             if w is not None:
-                _check(w, name, (self.d,), torch.float32, dev)
+                _check(w, name, (self.d,), F32, dev)
         rotary, pos64 = 0, 0
         if inv_freq is not None:
             if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1:
                 raise ValueError("inv_freq must be a tensor of one dimension")
-            _check(inv_freq, "inv_freq", tuple(inv_freq.shape), torch.float64, dev)
+            _check(inv_freq, "inv_freq", inv_freq.shape, torch.float64, dev)
             rotary = 2 * inv_freq.numel()
             if rotary > self.d:
                 raise ValueError(f"inv_freq turns {rotary} channels, a head has {self.d}")
@@ -288,17 +352,19 @@ class _Prep:
                 raise TypeError("positions must be an int32 or int64 tensor")
             _check(positions, "positions", self.tokens_shape, positions.dtype, dev)
             pos64 = int(positions.dtype == torch.int64)
-        self.inputs = {"q": q, "k": k, "q_weight": q_weight, "k_weight": k_weight, "positions": positions,
-                       "inv_freq": inv_freq}
+        self.spans = [("q", _span(q)), ("k", _span(k)), ("q_weight", _span(q_weight)), ("k_weight", _span(k_weight)),
+                      ("positions", _span(positions)), ("inv_freq", _span(inv_freq))]
         self.ptrs = (_ptr(q_weight), _ptr(k_weight), _ptr(positions), pos64, _ptr(inv_freq))
         self.sizes = (tokens, max(1, self.tokens_shape[-1]), self.Hq, self.Hk, self.d, rotary, self.qs, self.ks, self.dt,
                       NORMS[norm], LAYOUTS[layout], float(eps), float(q_scale), float(rope_scale))
 
-    def out(self, t, name, heads, like):
+    def out(self, t, name, heads, dtype, others):
+        """An output of `heads` heads, allocated or checked."""
         shape = self.tokens_shape + (heads, self.d)
         if t is None:
-            t = torch.empty(shape, device=self.dev, dtype=like.dtype)
-        _check(t, name, shape, like.dtype, self.dev)
+            return torch.empty(shape, device=self.dev, dtype=dtype)
+        _check(t, name, shape, dtype, self.dev)
+        _apart(t, name, others)
         return t
 
 
@@ -311,18 +377,17 @@ def qk_norm_rope(q, k=None, *, positions=None, inv_freq=None, norm="l2", layout=
     tokens' shape, None: the index along the last token dimension. Returns (q_out, k_out), which may
     be q and k themselves where those are contiguous (k_out None without k)."""
     p = _Prep(q, k, positions, inv_freq, norm, layout, q_weight, k_weight, eps, q_scale, rope_scale)
-    q_out = p.out(q_out, "q_out", p.Hq, q)
-    k_out = p.out(k_out, "k_out", p.Hk, k) if k is not None else None
-    for name, t, own in (("q_out", q_out, "q"), ("k_out", k_out, "k")):
-        if t is None:
-            continue
-        src = p.inputs[own]
-        same = t.data_ptr() == src.data_ptr() and src.is_contiguous()
-        _apart(t, name, {n: x for n, x in p.inputs.items() if not (same and n == own)})
-    _apart(k_out, "k_out", {"q_out": q_out})
-    with torch.cuda.device(p.dev):
-        st = load().ckda_qk_prep(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), *p.ptrs, *p.sizes, _stream(stream, p.dev))
-    _raise(st, "ckda_qk_prep")
+    def others(t, src, own):
+        same = t is not None and src.is_contiguous() and t.data_ptr() == src.data_ptr()
+        return [x for x in p.spans if not (same and x[0] == own)]
+
+    q_out = p.out(q_out, "q_out", p.Hq, q.dtype, others(q_out, q, "q"))
+    if k is None:
+        k_out = None
+    else:
+        k_out = p.out(k_out, "k_out", p.Hk, k.dtype, others(k_out, k, "k") + [("q_out", _span(q_out))])
+    _launch(p.dev, stream, load().ckda_qk_prep, "ckda_qk_prep",
+            (_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), *p.ptrs, *p.sizes))
     return q_out, k_out
 
 
@@ -338,30 +403,29 @@ def qk_norm_rope_bwd(q, k, grad_q, grad_k=None, *, positions=None, inv_freq=None
     if k is not None:
         _check(grad_k, "grad_k", p.tokens_shape + (p.Hk, p.d), q.dtype, p.dev)
     got = dict(grads or {})
-    got["dq"] = p.out(got.get("dq"), "dq", p.Hq, q)
-    got["dk"] = p.out(got.get("dk"), "dk", p.Hk, k) if k is not None else None
+    spans = p.spans + [("grad_q", _span(grad_q)), ("grad_k", _span(grad_k))]
+    got["dq"] = p.out(got.get("dq"), "dq", p.Hq, q.dtype, spans)
+    spans.append(("dq", _span(got["dq"])))
+    got["dk"] = p.out(got.get("dk"), "dk", p.Hk, k.dtype, spans) if k is not None else None
+    spans.append(("dk", _span(got["dk"])))
+    weights = False
     for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
         if w is None:
             got[name] = None
             continue
+        weights = True
         if got.get(name) is None:
-            got[name] = torch.empty(p.d, device=p.dev, dtype=torch.float32)
-        _check(got[name], name, (p.d,), torch.float32, p.dev)
-    names = ["dq", "dk", "dq_weight", "dk_weight"]
-    for i, name in enumerate(names):
-        _apart(got[name], name, {**p.inputs, "grad_q": grad_q, "grad_k": grad_k, **{n: got[n] for n in names[:i]}})
-    lib = load()
-    with torch.cuda.device(p.dev):
-        need = int(lib.ckda_qk_prep_bwd_workspace_bytes(p.d)) if got["dq_weight"] is not None or got["dk_weight"] is not None else 0
-        if need and workspace is None:
-            workspace = torch.empty(need, device=p.dev, dtype=torch.uint8)
-        if workspace is not None:
-            _check(workspace, "workspace", tuple(workspace.shape), None, p.dev)
-        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = lib.ckda_qk_prep_bwd(_ptr(q), _ptr(k), _ptr(grad_q), _ptr(grad_k), _ptr(got["dq"]), _ptr(got["dk"]),
-                                  _ptr(got["dq_weight"]), _ptr(got["dk_weight"]), *p.ptrs, *p.sizes, _ptr(workspace),
-                                  wbytes, _stream(stream, p.dev))
-    _raise(st, "ckda_qk_prep_bwd")
+            got[name] = torch.empty(p.d, device=p.dev, dtype=F32)
+        else:
+            _check(got[name], name, (p.d,), F32, p.dev)
+            _apart(got[name], name, spans)
+        spans.append((name, _span(got[name])))
+    wbytes = 0
+    if weights or workspace is not None:
+        workspace, wbytes = _workspace("ckda_qk_prep_bwd_workspace_bytes", p.dev, (p.d,), workspace)
+    _launch(p.dev, stream, load().ckda_qk_prep_bwd, "ckda_qk_prep_bwd",
+            (_ptr(q), _ptr(k), _ptr(grad_q), _ptr(grad_k), _ptr(got["dq"]), _ptr(got["dk"]), _ptr(got["dq_weight"]),
+             _ptr(got["dk_weight"]), *p.ptrs, *p.sizes, _ptr(workspace), wbytes))
     return got
 
 
@@ -408,21 +472,16 @@ def state_copy(S, src, dst, *, pool_dim=0, stream=None) -> torch.Tensor:
     layer's, S [L, P, Hv, dk, dv] (pool_dim 1): slot dst[i] takes the state of slot src[i] as it was
     before the call, or zeros where src[i] is negative; a negative dst[i] names nothing; of pairs
     with the same dst the last counts. src, dst: int32, at most 1024. Returns S."""
-    dev = _device(S, "S")
+    dev = _call_device(S, "S")
     if pool_dim not in (0, 1) or S.dim() < pool_dim + 2:
         raise ValueError(f"S has shape {tuple(S.shape)}, with the pool in dimension {pool_dim}")
-    _check(S, "S", tuple(S.shape), torch.float32, dev)
-    _int32(src, "src", None, dev)
-    _int32(dst, "dst", src.numel(), dev)
-    _apart(S, "S", {"src": src, "dst": dst})
-    layers = S.shape[0] if pool_dim else 1
-    slots = S.shape[pool_dim]
-    row = 1
-    for n in S.shape[pool_dim + 1:]:
-        row *= n
+    _check(S, "S", S.shape, F32, dev)
+    _indexes(src, "src", None, dev)
+    _indexes(dst, "dst", src.shape[0], dev)
+    _apart(S, "S", [("src", _span(src)), ("dst", _span(dst))])
+    layers, slots = S.shape[0] if pool_dim else 1, S.shape[pool_dim]
     if slots == 0:
         raise ValueError("S holds no states")
-    with torch.cuda.device(dev):
-        st = load().ckda_state_copy(_ptr(S), _ptr(src), _ptr(dst), src.numel(), layers, slots, row, _stream(stream, dev))
-    _raise(st, "ckda_state_copy")
+    _launch(dev, stream, load().ckda_state_copy, "ckda_state_copy",
+            (_ptr(S), _ptr(src), _ptr(dst), src.shape[0], layers, slots, prod(S.shape[pool_dim + 1:])))
     return S
