@@ -262,13 +262,15 @@ cudaError_t run_chain_bwd(const Call& c, const Maps& m, const ChainIn& in) {
         m.q, m.k, m.v, m.o, in, c.dST, c.gv, c.gS0, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
     return cudaPeekAtLastError();
 }
-template <int DV>
+template <int DK, int DV>
 cudaError_t run_grads(const Call& c) {
-    constexpr size_t smem = GradSmem<DV>::BYTES;
-    cudaError_t e = kernel_ready(grad_kernel<DV>, smem);
+    constexpr size_t smem = GradSmem<DK, DV>::BYTES;
+    cudaError_t e = kernel_ready(grad_kernel<DK, DV>, smem);
     if (e != cudaSuccess) return e;
-    grad_kernel<DV><<<dim3((unsigned)Seqs::slots(c.s.N, c.s.total), (unsigned)c.s.Hk, (unsigned)((c.s.dk + 63) / 64)), 128, smem, c.st>>>(
-        c.q, c.k, c.grad_o, c.gv, c.gq, c.gk, c.gg, c.gb, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv, c.qs, c.ks);
+    const long long slots = (long long)Seqs::slots(c.s.N, c.s.total), items = slots * c.s.Hk;
+    if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+    grad_kernel<DK, DV><<<(unsigned)std::min<long long>(items, sm_count()), 256, smem, c.st>>>(
+        c.q, c.k, c.grad_o, c.gv, c.gq, c.gk, c.gg, c.gb, c.ws, c.seqs, (int)slots, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv, c.qs, c.ks);
     return cudaPeekAtLastError();
 }
 
@@ -286,7 +288,7 @@ cudaError_t run_chunked(const Call& c) {
     if (e == cudaSuccess) e = run_chain_fwd<DK, kBack>(c, m, in);
     if constexpr (kBack) {
         if (e == cudaSuccess) e = run_chain_bwd<DK>(c, m, in);
-        if (e == cudaSuccess) e = c.s.dv <= 64 ? run_grads<64>(c) : run_grads<128>(c);
+        if (e == cudaSuccess) e = c.s.dv <= 64 ? run_grads<DK, 64>(c) : run_grads<DK, 128>(c);
     }
     return e;
 }

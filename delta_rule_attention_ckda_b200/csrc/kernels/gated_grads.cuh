@@ -12,92 +12,195 @@
 // which cuts the error of the sum to a half of the one-sided one (1.04e-5 to 6e-6 of dg's norm).
 //
 // dQ and dK are rounded to bf16 at the end, so their operands go in one bf16 term; dg and
-// dbeta come from the chains' fp32 sums. One CTA of four warps per (chunk, key head, 64
-// channels of d_k), two CTAs an SM so that one's loads run under the other's products; a warp
-// owns 16 tokens. Value heads that share the key head are summed in the accumulators, in
-// head order.
+// dbeta come from the chains' fp32 sums. Memory-bound: per chunk and head 157 KB are read (states
+// and cotangents 64, the rest tokens) for 2500 warp products. One CTA of eight warps an SM walks
+// over (chunk, key head) pairs; every tile of the next pair is asked for as soon as the products
+// that read its place are done, so about 100 KB are always on their way. Dw and Da are formed by four warps each and pass through
+// shared memory, where they serve as left operands straight and transposed; then a warp owns 16
+// tokens and half of the channels. Value heads that share a key head are summed in the
+// accumulators, in head order.
 #pragma once
 #include "gated_mma.cuh"
 
 namespace ckda {
 namespace gated {
 
-template <int DV>
+// Shared memory (bytes): token tiles twice, states and keys once.
+template <int DK, int DV>
 struct GradSmem {
-    static constexpr int LDV = ld_bytes(DV);
-    static constexpr int DO = 0, U = DO + 64 * LDV, DVV = U + 64 * LDV, S = DVV + 64 * LDV, DS = S + DV * LD64,
-                         K = DS + DV * LD64, Q = K + 64 * LD64, VECS = Q + 64 * LD64, BYTES = VECS + VEC * 4;
+    static constexpr int LDV = ld_bytes(DV), LDK = ld_bytes(DK);
+    static constexpr int DO = 0, U = DO + 64 * LDV, DVV = U + 64 * LDV, VECS = DVV + 64 * LDV, TOKENS = VECS + VEC * 4;
+    static constexpr int S = 2 * TOKENS, DS = S + DV * LDK, K = DS + DV * LDK, Q = K + 64 * LDK, DW = Q + 64 * LDK,
+                         DA = DW + 64 * LD64, BYTES = DA + 64 * LD64;
+};
+static_assert(GradSmem<128, 128>::BYTES <= 232448, "more shared memory than an SM has");
+
+// One (chunk, value head): where its rows lie.
+struct GradUnit {
+    int item, r, c, nt;
+    size_t tok, wh;
 };
 
-template <int DV>
-__global__ void __launch_bounds__(128, 2)
+template <int DK, int DV>
+__global__ void __launch_bounds__(256, 1)
 grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ grad_o,
             const __nv_bfloat16* __restrict__ grad_v, __nv_bfloat16* __restrict__ grad_q, __nv_bfloat16* __restrict__ grad_k,
-            float* __restrict__ grad_g, float* __restrict__ grad_beta, ChunkWs ws, Seqs seqs, int Hk, int Hv, int dk, int dv,
-            long long qs, long long ks) {
-    using L = GradSmem<DV>;
-    constexpr int LDV = L::LDV;
+            float* __restrict__ grad_g, float* __restrict__ grad_beta, ChunkWs ws, Seqs seqs, int slots, int Hk, int Hv, int dk,
+            int dv, long long qs, long long ks) {
+    using L = GradSmem<DK, DV>;
+    constexpr int LDV = L::LDV, LDK = L::LDK, NH = DK / 16;             // tiles of 8 channels a warp owns
     extern __shared__ __align__(16) unsigned char sm[];
     const uint32_t base = s32(sm);
-    const int slot = blockIdx.x, hk = blockIdx.y, d0 = blockIdx.z * 64, rep = Hv / Hk;
+    const int rep = Hv / Hk, items = slots * Hk, strips = (dv + 31) / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, t2 = 2 * (lane & 3);
-    const int n = seqs.find(slot);
-    int start, len;
-    bool ok;
-    seqs.get(n, start, len, ok);
-    const int c = slot - seqs.first_slot(n, start);
-    if (c < 0 || (long long)c * C >= len) return;
-    const int nt = min(C, len - c * C), strips = (dv + 31) / 32;
-    const size_t tok = (size_t)start + (size_t)c * C, mat = (size_t)dk * dv;
-    const float* vec = reinterpret_cast<const float*>(sm + L::VECS);
-    load_rows<64, 128>(base + L::K, k + tok * ks + (size_t)hk * dk + d0, ks, nt, dk - d0);
-    load_rows<64, 128>(base + L::Q, q + tok * qs + (size_t)hk * dk + d0, qs, nt, dk - d0);
-    float gq[8][4], gk[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) gq[i][e] = gk[i][e] = 0.f;
-#pragma unroll 1
-    for (int r = 0; r < rep; ++r) {
-        const int h = hk * rep + r;
-        const size_t wh = (size_t)slot * Hv + h;
-        if (r > 0) __syncthreads();
-        load_rows<DV, 128>(base + L::DO, grad_o + (tok * Hv + h) * dv, (long long)Hv * dv, nt, dv);
-        load_rows<DV, 128>(base + L::U, ws.u + wh * 64 * dv, dv, 64, dv);
-        load_rows<DV, 128>(base + L::DVV, grad_v + (tok * Hv + h) * dv, (long long)Hv * dv, nt, dv);
-        for (int e = tid; e < VEC / 4; e += 128) cp16(base + L::VECS + e * 16, ws.vec + wh * VEC + e * 4, true);
-        cp_commit();
-#pragma unroll
-        for (int e = tid; e < DV * 8; e += 128) {
-            const int row = e % DV, p = e / DV;
-            const bool in = row < dv && d0 + p * 8 < dk;
-            const size_t from = wh * mat + (in ? ((size_t)(d0 / 8 + p) * dv + row) * 8 : 0);
-            cp16(base + L::S + row * LD64 + p * 16, ws.shi + from, in);
-            cp16(base + L::DS + row * LD64 + p * 16, ws.dshi + from, in);
+    const int rb = warp & 3, part2 = warp >> 2, d0 = part2 * (DK / 2);  // row block, half of the channels
+    const size_t mat = (size_t)dk * dv;
+
+    // the next unit: the next head of the item, else the next item that names a chunk
+    auto advance = [&](GradUnit& u) {
+        if (u.item >= 0 && u.item < items && u.r + 1 < rep) {
+            ++u.r;
+            ++u.wh;
+            return;
         }
+        u.r = 0;
+        while (true) {
+            u.item = u.item < 0 ? (int)blockIdx.x : u.item + (int)gridDim.x;
+            if (u.item >= items) return;
+            const int slot = u.item / Hk, n = seqs.find(slot);
+            int start, len;
+            bool ok;
+            seqs.get(n, start, len, ok);
+            u.c = slot - seqs.first_slot(n, start);
+            if (u.c < 0 || (long long)u.c * C >= len) continue;
+            u.nt = min(C, len - u.c * C);
+            u.tok = (size_t)start + (size_t)u.c * C;
+            u.wh = (size_t)slot * Hv + (u.item % Hk) * rep;
+            return;
+        }
+    };
+    auto load_tokens = [&](const GradUnit& u, int b) {
+        const uint32_t to = base + b * L::TOKENS;
+        const int h = (u.item % Hk) * rep + u.r;
+        load_rows<DV, 256>(to + L::DO, grad_o + (u.tok * Hv + h) * dv, (long long)Hv * dv, u.nt, dv);
+        load_rows<DV, 256>(to + L::U, ws.u + u.wh * 64 * dv, dv, 64, dv);
+        load_rows<DV, 256>(to + L::DVV, grad_v + (u.tok * Hv + h) * dv, (long long)Hv * dv, u.nt, dv);
+        for (int e = tid; e < VEC / 4; e += 256) cp16(to + L::VECS + e * 16, ws.vec + u.wh * VEC + e * 4, true);
+    };
+
+    auto load_state = [&](const GradUnit& u, int to, const __nv_bfloat16* from) {
+#pragma unroll 4
+        for (int e = tid; e < DV * (DK / 8); e += 256) {
+            const int row = e % DV, p = e / DV;
+            const bool in = row < dv && p * 8 < dk;
+            cp16(base + to + row * LDK + p * 16, from + u.wh * mat + (in ? ((size_t)p * dv + row) * 8 : 0), in);
+        }
+    };
+
+    float gq[NH][4], gk[NH][4];
+    GradUnit u{-1, 0, 0, 0, 0, 0};
+    advance(u);
+    // groups in flight at the loop's top: the tokens (arrived), S, dS
+    if (u.item < items) load_tokens(u, 0);
+    cp_commit();
+    if (u.item < items) load_state(u, L::S, ws.shi);
+    cp_commit();
+    if (u.item < items) load_state(u, L::DS, ws.dshi);
+    cp_commit();
+    cp_wait<2>();
+#pragma unroll 1
+    for (int b = 0; u.item < items; b ^= 1) {
+        const int hk = u.item % Hk, h = hk * rep + u.r;
+        const uint32_t tk = base + b * L::TOKENS;
+        const float* vec = reinterpret_cast<const float*>(sm + b * L::TOKENS + L::VECS);
+        __syncthreads();                       // the tokens are in; the last products of the unit before are done
+        load_rows<DK, 256>(base + L::K, k + u.tok * ks + (size_t)hk * dk, ks, u.nt, dk);
+        load_rows<DK, 256>(base + L::Q, q + u.tok * qs + (size_t)hk * dk, qs, u.nt, dk);
         cp_commit();
-        if (blockIdx.z == 0 && warp == 3) {    // dg and dbeta: two tokens a lane, summed from the end
-            const float* part = ws.parts + wh * strips * PARTS;
-            // <S, dS> at the chunk's end, and at its start: the end of the chunk before, or SDS0
-            const float* before = c > 0 ? part - (size_t)Hv * strips * PARTS + PART_SDS : part + PART_SDS0;
-            double x[2];
-            float db[2] = {0.f, 0.f}, end = 0.f, begin = 0.f;
+        if (u.r == 0) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float a = 0.f, b = 0.f;
-                for (int sidx = 0; sidx < strips; ++sidx) {
-                    const float* p = part + (size_t)sidx * PARTS + 2 * lane + i;
-                    a += p[PART_DOO];
-                    b += p[PART_DVV];
-                    db[i] += p[PART_DB];
+            for (int i = 0; i < NH; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) gq[i][e] = gk[i][e] = 0.f;
+        }
+        // warp 0: the sums that dg and dbeta come from, in flight (two tokens a lane; lanes 0 .. 7 the
+        // parts of <S, dS> at the chunk's end, 8 .. 15 those at its start: the end of the chunk before,
+        // or SDS0)
+        float2 doo[4], dvv[4], wy[4];
+        float edge = 0.f;
+        if (warp == 0) {
+            const float* part = ws.parts + u.wh * strips * PARTS;
+            const float* before = u.c > 0 ? part - (size_t)Hv * strips * PARTS + PART_SDS : part + PART_SDS0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2* p = reinterpret_cast<const float2*>(part + (size_t)i * PARTS) + lane;
+                const bool in = i < strips;
+                doo[i] = in ? p[PART_DOO / 2] : make_float2(0.f, 0.f);
+                dvv[i] = in ? p[PART_DVV / 2] : make_float2(0.f, 0.f);
+                wy[i] = in ? p[PART_DB / 2] : make_float2(0.f, 0.f);
+            }
+            const int i = (lane & 7) / 2;
+            if (lane < 16 && i < strips) edge = (lane < 8 ? part + PART_SDS : before)[(size_t)i * PARTS + (lane & 1)];
+        }
+        {                                      // Dw (warps 0 .. 3) and Da (4 .. 7): 16 rows, columns to the diagonal
+            float w[8][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[i][e] = 0.f;
+            const uint32_t left = tk + (part2 ? L::DVV : L::DO);
+#pragma unroll
+            for (int d = 0; d < DV; d += 16) {
+                uint32_t f[4];
+                ldm4(f, left + ofs_a(LDV) + at(16 * rb, d, LDV));
+#pragma unroll
+                for (int jp = 0; jp < 4; ++jp)
+                    if (jp <= rb) {
+                        uint32_t x[4];
+                        ldm4(x, tk + L::U + ofs_n(LDV) + at(16 * jp, d, LDV));
+                        mma(w[2 * jp], f, x[0], x[1]);
+                        mma(w[2 * jp + 1], f, x[2], x[3]);
+                    }
+            }
+            unsigned char* out = sm + (part2 ? L::DA : L::DW);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i / 2 > rb) continue;
+                const int j0 = 8 * i + t2;
+                const float2 gh = *reinterpret_cast<const float2*>(vec + VEC_GHI + j0), gl = *reinterpret_cast<const float2*>(vec + VEC_GLO + j0);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int row = 16 * rb + gi + 8 * half;
+                    const float rh = vec[VEC_GHI + row], rl = vec[VEC_GLO + row];
+                    float x[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = j0 + e;
+                        const float D = expf((rh - (e ? gh.y : gh.x)) + (rl - (e ? gl.y : gl.x)));
+                        x[e] = part2 ? (j < row ? -D * w[i][2 * half + e] : 0.f) : (j <= row ? D * w[i][2 * half + e] : 0.f);
+                    }
+                    *reinterpret_cast<uint32_t*>(out + row * LD64 + j0 * 2) = pack2(x[0], x[1]);
                 }
-                x[i] = (double)a - (double)b;
             }
-            for (int sidx = 0; sidx < strips; ++sidx) {
-                end += part[(size_t)sidx * PARTS + PART_SDS] + part[(size_t)sidx * PARTS + PART_SDS + 1];
-                begin += before[(size_t)sidx * PARTS] + before[(size_t)sidx * PARTS + 1];
+        }
+        GradUnit next = u;
+        advance(next);
+        const bool more = next.item < items;
+        if (more) load_tokens(next, b ^ 1);
+        cp_commit();
+        if (warp == 0) {                       // dg and dbeta
+            float a[2] = {0.f, 0.f}, e[2] = {0.f, 0.f}, db[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[0] += doo[i].x; a[1] += doo[i].y;
+                e[0] += dvv[i].x; e[1] += dvv[i].y;
+                db[0] += wy[i].x; db[1] += wy[i].y;
             }
-            double sum = x[0] + x[1];                              // of this lane's tokens and all later ones
+#pragma unroll
+            for (int off = 4; off > 0; off >>= 1) edge += __shfl_xor_sync(0xffffffffu, edge, off);
+            const double end = __shfl_sync(0xffffffffu, edge, 0), begin = __shfl_sync(0xffffffffu, edge, 8);
+            const double x[2] = {(double)a[0] - (double)e[0], (double)a[1] - (double)e[1]};
+            double sum = x[0] + x[1];          // of this lane's tokens and all later ones
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const double y = __shfl_down_sync(0xffffffffu, sum, off);
@@ -107,155 +210,110 @@ grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
-                if (t < nt) {
-                    const double f = (double)t / nt;
-                    grad_g[(tok + t) * Hv + h] = (float)(f * (from[i] + end) + (1.0 - f) * (begin - (all - from[i])));
-                    grad_beta[(tok + t) * Hv + h] = db[i];
+                if (t < u.nt) {
+                    const double f = (double)t / u.nt;
+                    grad_g[(u.tok + t) * Hv + h] = (float)(f * (from[i] + end) + (1.0 - f) * (begin - (all - from[i])));
+                    grad_beta[(u.tok + t) * Hv + h] = db[i];
                 }
             }
         }
-        cp_wait<1>();
-        __syncthreads();
-        // Dw, Da: rows 16 warp .. + 15, as the operands of the next products
-        uint32_t aw[4][4], aa[4][4];
-        {
-            float w[8][4], a[8][4];
+        cp_wait<3>();
+        __syncthreads();                       // S is in; Dw and Da are written
+        const float eg[2] = {vec[VEC_EG + 16 * rb + gi], vec[VEC_EG + 16 * rb + gi + 8]};
+        const float dc[2] = {vec[VEC_DEC + 16 * rb + gi], vec[VEC_DEC + 16 * rb + gi + 8]};
+        // rows times states: acc = X M, X a [64][DV] tile, M [DV][this warp's channels]
+        auto times = [&](int X, int M, float (&acc)[NH][4]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[i][e] = a[i][e] = 0.f;
-#pragma unroll
-            for (int d = 0; d < DV; d += 16) {
-                uint32_t fo[4], fv[4];
-                ldm4(fo, base + L::DO + ofs_a(LDV) + at(16 * warp, d, LDV));
-                ldm4(fv, base + L::DVV + ofs_a(LDV) + at(16 * warp, d, LDV));
-#pragma unroll
-                for (int jp = 0; jp < 4; ++jp)
-                    if (jp <= warp) {
-                        uint32_t b[4];
-                        ldm4(b, base + L::U + ofs_n(LDV) + at(16 * jp, d, LDV));
-                        mma(w[2 * jp], fo, b[0], b[1]);
-                        mma(w[2 * jp + 1], fo, b[2], b[3]);
-                        mma(a[2 * jp], fv, b[0], b[1]);
-                        mma(a[2 * jp + 1], fv, b[2], b[3]);
-                    }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int j0 = 8 * i + t2;
-                const float2 gh = *reinterpret_cast<const float2*>(vec + VEC_GHI + j0), gl = *reinterpret_cast<const float2*>(vec + VEC_GLO + j0);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 16 * warp + gi + 8 * (e >> 1), j = j0 + (e & 1);
-                    const float hj = (e & 1) ? gh.y : gh.x, lj = (e & 1) ? gl.y : gl.x;
-                    const float D = j <= row ? expf((vec[VEC_GHI + row] - hj) + (vec[VEC_GLO + row] - lj)) : 0.f;
-                    w[i][e] = j <= row ? D * w[i][e] : 0.f;
-                    a[i][e] = j < row ? -D * a[i][e] : 0.f;
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                operand(w[2 * j], w[2 * j + 1], aw[j]);
-                operand(a[2 * j], a[2 * j + 1], aa[j]);
-            }
-        }
-        cp_wait<0>();
-        __syncthreads();
-        // rows times states: acc = X M for X a [64][DV] tile and M a [DV][64] one
-        const float eg[2] = {vec[VEC_EG + 16 * warp + gi], vec[VEC_EG + 16 * warp + gi + 8]};
-        const float dc[2] = {vec[VEC_DEC + 16 * warp + gi], vec[VEC_DEC + 16 * warp + gi + 8]};
-        auto times = [&](int X, int M, float (&acc)[8][4]) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < NH; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 #pragma unroll
             for (int d = 0; d < DV; d += 16) {
                 uint32_t f[4];
-                ldm4(f, base + X + ofs_a(LDV) + at(16 * warp, d, LDV));
+                ldm4(f, tk + X + ofs_a(LDV) + at(16 * rb, d, LDV));
 #pragma unroll
-                for (int jp = 0; jp < 4; ++jp) {
-                    uint32_t b[4];
-                    ldm4t(b, base + M + ofs_k(LD64) + at(d, 16 * jp, LD64));
-                    mma(acc[2 * jp], f, b[0], b[1]);
-                    mma(acc[2 * jp + 1], f, b[2], b[3]);
+                for (int jp = 0; jp < NH / 2; ++jp) {
+                    uint32_t x[4];
+                    ldm4t(x, base + M + ofs_k(LDK) + at(d, d0 + 16 * jp, LDK));
+                    mma(acc[2 * jp], f, x[0], x[1]);
+                    mma(acc[2 * jp + 1], f, x[2], x[3]);
                 }
             }
         };
         {
-            float acc[8][4];
+            float acc[NH][4];
             times(L::DO, L::S, acc);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < NH; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) gq[i][e] = fmaf(eg[e >> 1], acc[i][e], gq[i][e]);
             times(L::DVV, L::S, acc);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < NH; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) gk[i][e] = fmaf(-eg[e >> 1], acc[i][e], gk[i][e]);
+            cp_wait<2>();
+            __syncthreads();                   // dS is in; S is done with
+            if (more) load_state(next, L::S, ws.shi);
+            cp_commit();
             times(L::U, L::DS, acc);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < NH; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) gk[i][e] = fmaf(dc[e >> 1], acc[i][e], gk[i][e]);
         }
-        // Dw K, Da K
+        cp_wait<2>();
+        __syncthreads();                       // K and Q are in; dS is done with
+        if (more) load_state(next, L::DS, ws.dshi);
+        cp_commit();
+#pragma unroll 1
+        for (int j = 0; j <= rb; ++j) {        // Dw K, Da K
+            uint32_t fw[4], fa[4];
+            ldm4(fw, base + L::DW + ofs_a(LD64) + at(16 * rb, 16 * j, LD64));
+            ldm4(fa, base + L::DA + ofs_a(LD64) + at(16 * rb, 16 * j, LD64));
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j <= warp) {
-#pragma unroll
-                for (int jp = 0; jp < 4; ++jp) {
-                    uint32_t b[4];
-                    ldm4t(b, base + L::K + ofs_k(LD64) + at(16 * j, 16 * jp, LD64));
-                    mma(gq[2 * jp], aw[j], b[0], b[1]);
-                    mma(gq[2 * jp + 1], aw[j], b[2], b[3]);
-                    mma(gk[2 * jp], aa[j], b[0], b[1]);
-                    mma(gk[2 * jp + 1], aa[j], b[2], b[3]);
-                }
-            }
-        // Dw^T Q, Da^T K: through the tiles of dO and dV, which are done with
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j <= warp) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int off = (16 * warp + gi + 8 * (e & 1)) * LD64 + (16 * j + 8 * (e >> 1) + t2) * 2;
-                    *reinterpret_cast<uint32_t*>(sm + L::DO + off) = aw[j][e];
-                    *reinterpret_cast<uint32_t*>(sm + L::DVV + off) = aa[j][e];
-                }
-            }
-        __syncthreads();
-#pragma unroll
-        for (int ip = 0; ip < 4; ++ip)
-            if (ip >= warp) {
-                uint32_t fw[4], fa[4];
-                ldm4t(fw, base + L::DO + ofs_at(LD64) + at(16 * ip, 16 * warp, LD64));
-                ldm4t(fa, base + L::DVV + ofs_at(LD64) + at(16 * ip, 16 * warp, LD64));
-#pragma unroll
-                for (int jp = 0; jp < 4; ++jp) {
-                    uint32_t b[4];
-                    ldm4t(b, base + L::Q + ofs_k(LD64) + at(16 * ip, 16 * jp, LD64));
-                    mma(gk[2 * jp], fw, b[0], b[1]);
-                    mma(gk[2 * jp + 1], fw, b[2], b[3]);
-                    ldm4t(b, base + L::K + ofs_k(LD64) + at(16 * ip, 16 * jp, LD64));
-                    mma(gk[2 * jp], fa, b[0], b[1]);
-                    mma(gk[2 * jp + 1], fa, b[2], b[3]);
-                }
-            }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int row = 16 * warp + gi + 8 * half, d = d0 + 8 * i + t2;
-            if (row < nt && d < dk) {
-                const size_t to = ((tok + row) * Hk + hk) * dk + d;
-                *reinterpret_cast<uint32_t*>(grad_q + to) = pack2(gq[i][2 * half], gq[i][2 * half + 1]);
-                *reinterpret_cast<uint32_t*>(grad_k + to) = pack2(gk[i][2 * half], gk[i][2 * half + 1]);
+            for (int jp = 0; jp < NH / 2; ++jp) {
+                uint32_t x[4];
+                ldm4t(x, base + L::K + ofs_k(LDK) + at(16 * j, d0 + 16 * jp, LDK));
+                mma(gq[2 * jp], fw, x[0], x[1]);
+                mma(gq[2 * jp + 1], fw, x[2], x[3]);
+                mma(gk[2 * jp], fa, x[0], x[1]);
+                mma(gk[2 * jp + 1], fa, x[2], x[3]);
             }
         }
+#pragma unroll 1
+        for (int ip = rb; ip < 4; ++ip) {      // Dw^T Q, Da^T K
+            uint32_t fw[4], fa[4];
+            ldm4t(fw, base + L::DW + ofs_at(LD64) + at(16 * ip, 16 * rb, LD64));
+            ldm4t(fa, base + L::DA + ofs_at(LD64) + at(16 * ip, 16 * rb, LD64));
+#pragma unroll
+            for (int jp = 0; jp < NH / 2; ++jp) {
+                uint32_t x[4];
+                ldm4t(x, base + L::Q + ofs_k(LDK) + at(16 * ip, d0 + 16 * jp, LDK));
+                mma(gk[2 * jp], fw, x[0], x[1]);
+                mma(gk[2 * jp + 1], fw, x[2], x[3]);
+                ldm4t(x, base + L::K + ofs_k(LDK) + at(16 * ip, d0 + 16 * jp, LDK));
+                mma(gk[2 * jp], fa, x[0], x[1]);
+                mma(gk[2 * jp + 1], fa, x[2], x[3]);
+            }
+        }
+        if (u.r == rep - 1) {
+#pragma unroll
+            for (int i = 0; i < NH; ++i)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int row = 16 * rb + gi + 8 * half, d = d0 + 8 * i + t2;
+                    if (row < u.nt && d < dk) {
+                        const size_t to = ((u.tok + row) * Hk + hk) * dk + d;
+                        *reinterpret_cast<uint32_t*>(grad_q + to) = pack2(gq[i][2 * half], gq[i][2 * half + 1]);
+                        *reinterpret_cast<uint32_t*>(grad_k + to) = pack2(gk[i][2 * half], gk[i][2 * half + 1]);
+                    }
+                }
+        }
+        u = next;
+        cp_wait<2>();                          // the next unit's tokens
+    }
+    cp_wait<0>();
 }
 
 }  // namespace gated
