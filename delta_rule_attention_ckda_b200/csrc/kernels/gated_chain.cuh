@@ -19,9 +19,9 @@
 //
 // Rounding: raw K, Q, V are exact; every other operand (S, beta X, Z, U, P) is two bf16 terms
 // (2.7e-6 of a value at RMS), o is rounded once at its store. Sums are fp32; S' is formed in
-// registers. Backward (kBack): S and U in three terms, because dg sums differences of <dO, o> and
-// <dV, v> (a model of this arithmetic in fp64: dg off by 1.9e-6 in place of 2.1e-5 where the
-// states are large, by 1.3e-6 in place of 1.4e-5 elsewhere).
+// registers. Backward: U in three terms, and the adjoint's operands of the state too, because dg
+// sums differences of <dO, o> and <dV, v> (a model of this arithmetic in fp64: dg off by 4e-6 in
+// place of 2.1e-5 where the states are large, by 1.3e-6 in place of 1.4e-5 elsewhere).
 #pragma once
 #include "gated_mma.cuh"
 #include "tc_primitives.cuh"
@@ -93,6 +93,13 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, u
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
                  "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(c0), "r"(head), "r"(token)
                  : "memory");
+}
+
+// One lane of a warp that walks together: it issues the products, with operands the whole warp holds.
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // What a chain kernel reads by rows: tensor maps over [tokens][heads][channels] (boxes of 64
@@ -217,18 +224,20 @@ __device__ __forceinline__ void put_state_terms(const float* s, uint32_t tl, int
     put_terms<TERMS>(s, to);
 }
 
-// s <- whole s + the H update columns at `from`, all loads in flight.
-template <int H>
+// s <- whole s + the H update columns at `from`, N at a time (as registers allow).
+template <int H, int N>
 __device__ __forceinline__ void add_update(float (&s)[H], float whole, uint32_t from) {
-    float d[H / 32][32];
 #pragma unroll
-    for (int i = 0; i < H / 32; ++i) tc::tmem_ld32<32>(from + 32 * i, d[i]);
-    tc::tmem_ld_wait();
+    for (int k = 0; k < H; k += N) {
+        float d[N];
+        tc::tmem_ld32<N>(from + k, d);
+        tc::tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < H; i += 2) {
-        fma2(d[i / 32][i % 32], d[i / 32][i % 32 + 1], s[i], s[i + 1], whole, whole);
-        s[i] = d[i / 32][i % 32];
-        s[i + 1] = d[i / 32][i % 32 + 1];
+        for (int i = 0; i < N; i += 2) {
+            fma2(d[i], d[i + 1], s[k + i], s[k + i + 1], whole, whole);
+            s[k + i] = d[i];
+            s[k + i + 1] = d[i + 1];
+        }
     }
 }
 
@@ -333,7 +342,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 chain_load<DK, kBack>(base + (c & 1) * L::BYTES, &bars.full[c & 1], x, in, &mq, &mk, &mv, &mo, ws,
                                       (size_t)(slot0 + c) * Hv + h, start + c * C, min(C, len - c * C), h, hk, Hv, dk, dv);
             }
-        } else if (lane == 0) {                // ------------------------------------------ products
+        } else {                               // ------------------------------------------ products
             constexpr uint32_t i128 = tc::idesc_bf16(128, 128, 0, 0), i64 = tc::idesc_bf16(128, 64, 0, 0),
                                iS = tc::idesc_bf16(128, DK, 0, 1);
             // The output's product of a chunk is issued behind the next chunk's first one: it runs under the
@@ -343,14 +352,16 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 if (c > 0) chain_wait(bars, &bars.out, (c - 1) & 1);   // P U of the chunk before is read
                 chain_wait(bars, &bars.uo, c & 1);
                 tc::tc_fence_after();
+                if (elected()) {
 #pragma unroll
-                for (int term = 0; term < 3; ++term)               // P U: hi lo, lo hi, hi hi
+                    for (int term = 0; term < 3; ++term)               // P U: hi lo, lo hi, hi hi
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        tc::mma_ts(tm + TM_PU, tm + TM_UZ + 64 + (j / 2) * 32 + (term == 1 ? 16 : 0) + (j % 2) * 8,
-                                   tc::sdesc(st + L::P + (term == 0 ? 8192 : 0) + j * 32, 16, 1024), i64, (term | j) != 0);
-                tc::mma_commit(&bars.o);
-                tc::mma_commit(&bars.empty[c & 1]);
+                        for (int j = 0; j < 4; ++j)
+                            tc::mma_ts(tm + TM_PU, tm + TM_UZ + 64 + (j / 2) * 32 + (term == 1 ? 16 : 0) + (j % 2) * 8,
+                                       tc::sdesc(st + L::P + (term == 0 ? 8192 : 0) + j * 32, 16, 1024), i64, (term | j) != 0);
+                    tc::mma_commit(&bars.o);
+                    tc::mma_commit(&bars.empty[c & 1]);
+                }
             };
             if (chunks > 0) chain_wait(bars, &bars.full[0], 0);
 #pragma unroll 1
@@ -359,36 +370,41 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 if (c > 0) chain_wait(bars, &bars.qs, (c - 1) & 1);    // Q S of the chunk before is read
                 chain_wait(bars, &bars.s, ph);
                 tc::tc_fence_after();
+                if (elected()) {
 #pragma unroll
-                for (int term = 0; term < (kBack ? 3 : 2); ++term) // [K S | Q S]
+                    for (int term = 0; term < 2; ++term)               // [K S | Q S]
 #pragma unroll
-                    for (int j = 0; j < DK / 16; ++j) {
-                        const int half = j / (H / 16), jj = j % (H / 16);
-                        const uint32_t a = term < 2 ? TM_S + half * H + term * (H / 2) : TM_X + half * (H / 2);
-                        tc::mma_ts(tm + TM_ACC, tm + a + jj * 8, tc::sdesc(st + L::KQ + (j / 4) * 16384 + (j % 4) * 32, 16, 1024),
-                                   i128, (term | j) != 0);
-                    }
-                tc::mma_commit(&bars.m1);
+                        for (int j = 0; j < DK / 16; ++j) {
+                            const int half = j / (H / 16), jj = j % (H / 16);
+                            tc::mma_ts(tm + TM_ACC, tm + TM_S + half * H + term * (H / 2) + jj * 8,
+                                       tc::sdesc(st + L::KQ + (j / 4) * 16384 + (j % 4) * 32, 16, 1024), i128, (term | j) != 0);
+                        }
+                    tc::mma_commit(&bars.m1);
+                }
                 if (c > 0) output(c - 1);
                 chain_wait(bars, &bars.x, ph);
                 tc::tc_fence_after();
+                if (elected()) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)                        // beta X [Z_hi | Z_lo]
-                    tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 32, 16, 1024), i128, j != 0);
+                    for (int j = 0; j < 4; ++j)                        // beta X [Z_hi | Z_lo]
+                        tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 32, 16, 1024), i128, j != 0);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + 16 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 32, 16, 1024), i64, 1);
-                tc::mma_commit(&bars.m2);
+                    for (int j = 0; j < 4; ++j)
+                        tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + 16 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 32, 16, 1024), i64, 1);
+                    tc::mma_commit(&bars.m2);
+                }
                 chain_wait(bars, &bars.u, ph);
                 tc::tc_fence_after();
+                if (elected()) {
 #pragma unroll
-                for (int term = 0; term < (kBack ? 3 : 2); ++term) // the state's update
+                    for (int term = 0; term < (kBack ? 3 : 2); ++term) // the state's update
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t a = term < 2 ? TM_UZ + (j / 2) * 32 + term * 16 + (j % 2) * 8 : TM_X + (j / 2) * 32 + (j % 2) * 8;
-                        tc::mma_ts(tm + TM_S, tm + a, tc::sdesc(st + L::KQ + j * 2048, 16384, 1024), iS, (term | j) != 0);
-                    }
-                tc::mma_commit(&bars.m3);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a = term < 2 ? TM_UZ + (j / 2) * 32 + term * 16 + (j % 2) * 8 : TM_X + (j / 2) * 32 + (j % 2) * 8;
+                            tc::mma_ts(tm + TM_S, tm + a, tc::sdesc(st + L::KQ + j * 2048, 16384, 1024), iS, (term | j) != 0);
+                        }
+                    tc::mma_commit(&bars.m3);
+                }
                 if (c + 1 < chunks) chain_wait(bars, &bars.full[(c + 1) & 1], ((c + 1) >> 1) & 1);
             }
             if (chunks > 0) {
@@ -396,7 +412,6 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 chain_wait(bars, &bars.o, (chunks - 1) & 1);       // nothing in flight past this point
             }
         }
-        __syncwarp();
     } else if (warp >= kEpiWarps) {            // ------------------------------------------ output
         regs_down<kRegOut>();
         const int quarter = warp & 3, row = 32 * quarter + lane, x = threadIdx.x - 32 * kEpiWarps;
@@ -478,13 +493,13 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 const float whole = reinterpret_cast<const float*>(sm + ((c - 1) & 1) * L::BYTES + L::VECS)[VEC_EG + 63];
                 chain_wait(bars, &bars.m3, (c - 1) & 1);
                 tc::tc_fence_after();
-                add_update<H>(s, whole, tl + TM_S + wg * H);
+                add_update<H, 32>(s, whole, tl + TM_S + wg * H);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bars.empty[(c - 1) & 1]);
             }
             if (c < chunks) {
 #pragma unroll
-                for (int i = 0; i < H; i += 32) put_state_terms<kBack ? 3 : 2, H>(s + i, tl, wg, i);
+                for (int i = 0; i < H; i += 32) put_state_terms<2, H>(s + i, tl, wg, i);
                 tc::tmem_st_wait();
                 tc::tc_fence_before();
                 tc::mbar_arrive(&bars.s);
@@ -625,11 +640,17 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll 1
             for (int it = 0; it < chunks; ++it) {
                 const int c = chunks - 1 - it;
+                if (x == 32) {                 // what the epilogues read straight from memory, into L2
+                    const size_t wh = (size_t)(slot0 + c) * Hv + h;
+                    tc::prefetch_l2_bulk(ws.shi + (wh + (it ? 0 : Hv)) * mat, (uint32_t)(mat * 2));
+                    tc::prefetch_l2_bulk(ws.slo + (wh + (it ? 0 : Hv)) * mat, (uint32_t)(mat * 2));
+                    tc::prefetch_l2_bulk(ws.w + wh * 64 * dv, (uint32_t)(64 * dv * 4));
+                }
                 if (it >= 2) chain_wait(bars, &bars.empty[it & 1], ((it >> 1) - 1) & 1);
                 chain_load<DK, true>(base + (it & 1) * L::BYTES, &bars.full[it & 1], x, in, &mq, &mk, &mv, &mo, ws,
                                      (size_t)(slot0 + c) * Hv + h, start + c * C, min(C, len - c * C), h, hk, Hv, dk, dv);
             }
-        } else if (lane == 0) {                // ------------------------------------------ products
+        } else {                               // ------------------------------------------ products
             constexpr uint32_t iE = tc::idesc_bf16(128, 64, 1, 1), iK = tc::idesc_bf16(128, 64, 0, 0),
                                iZ = tc::idesc_bf16(128, 128, 0, 1), iZ64 = tc::idesc_bf16(128, 64, 0, 1),
                                iS = tc::idesc_bf16(128, DK, 0, 1);
@@ -639,58 +660,67 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 chain_wait(bars, &bars.full[it & 1], (it >> 1) & 1);
                 if (it > 0) chain_wait(bars, &bars.m3, (it - 1) & 1);
                 tc::tc_fence_after();
+                if (elected()) {
 #pragma unroll
-                for (int term = 1; term >= 0; --term)              // P^T dO, both terms of P
+                    for (int term = 1; term >= 0; --term)              // P^T dO, both terms of P
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        tc::mma_ss(tm + TM_PU, tc::sdesc(st + L::DO + j * 2048, 8192, 1024),
-                                   tc::sdesc(st + L::P + term * 8192 + j * 2048, 8192, 1024), iE, term == 0 || j != 0);
+                        for (int j = 0; j < 4; ++j)
+                            tc::mma_ss(tm + TM_PU, tc::sdesc(st + L::DO + j * 2048, 8192, 1024),
+                                       tc::sdesc(st + L::P + term * 8192 + j * 2048, 8192, 1024), iE, term == 0 || j != 0);
+                }
                 chain_wait(bars, &bars.s, ph);
                 tc::tc_fence_after();
+                if (elected()) {
 #pragma unroll
-                for (int term = 0; term < 3; ++term)               // K dS
+                    for (int term = 0; term < 3; ++term)               // K dS
 #pragma unroll
-                    for (int j = 0; j < DK / 16; ++j) {
-                        const int half = j / (H / 16), jj = j % (H / 16);
-                        const uint32_t a = term < 2 ? TM_S + half * H + term * (H / 2) : TM_X + half * (H / 2);
-                        tc::mma_ts(tm + TM_ACC, tm + a + jj * 8, tc::sdesc(st + L::KQ + (j / 4) * 16384 + (j % 4) * 32, 16, 1024),
-                                   iK, (term | j) != 0);
-                    }
-                tc::mma_commit(&bars.m1);
+                        for (int j = 0; j < DK / 16; ++j) {
+                            const int half = j / (H / 16), jj = j % (H / 16);
+                            const uint32_t a = term < 2 ? TM_S + half * H + term * (H / 2) : TM_X + half * (H / 2);
+                            tc::mma_ts(tm + TM_ACC, tm + a + jj * 8, tc::sdesc(st + L::KQ + (j / 4) * 16384 + (j % 4) * 32, 16, 1024),
+                                       iK, (term | j) != 0);
+                        }
+                    tc::mma_commit(&bars.m1);
+                }
                 if (it > 0) chain_wait(bars, &bars.out, (it - 1) & 1);   // y of the chunk before is read
                 chain_wait(bars, &bars.x, ph);
                 tc::tc_fence_after();
+                if (elected()) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)                        // beta dU [Z_hi | Z_lo], transposed
-                    tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 2048, 8192, 1024), iZ, j != 0);
+                    for (int j = 0; j < 4; ++j)                        // beta dU [Z_hi | Z_lo], transposed
+                        tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 2048, 8192, 1024), iZ, j != 0);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + 16 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 2048, 8192, 1024), iZ64, 1);
-                tc::mma_commit(&bars.m2);
+                    for (int j = 0; j < 4; ++j)
+                        tc::mma_ts(tm + TM_UZ, tm + TM_X + (j / 2) * 32 + 16 + (j % 2) * 8, tc::sdesc(st + L::Z + j * 2048, 8192, 1024), iZ64, 1);
+                    tc::mma_commit(&bars.m2);
+                }
                 chain_wait(bars, &bars.d, ph);
                 tc::tc_fence_after();
+                if (elected()) {
 #pragma unroll
-                for (int term = 0; term < 3; ++term)               // Q^T (e^G dO)
+                    for (int term = 0; term < 3; ++term)               // Q^T (e^G dO)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t a = (term < 2 ? TM_ACC + term * 16 : TM_PU) + (j / 2) * 32 + (j % 2) * 8;
-                        tc::mma_ts(tm + TM_S, tm + a, tc::sdesc(st + L::KQ + 8192 + j * 2048, 16384, 1024), iS, (term | j) != 0);
-                    }
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a = (term < 2 ? TM_ACC + term * 16 : TM_PU) + (j / 2) * 32 + (j % 2) * 8;
+                            tc::mma_ts(tm + TM_S, tm + a, tc::sdesc(st + L::KQ + 8192 + j * 2048, 16384, 1024), iS, (term | j) != 0);
+                        }
+                }
                 chain_wait(bars, &bars.u, ph);
                 tc::tc_fence_after();
+                if (elected()) {
 #pragma unroll
-                for (int term = 0; term < 3; ++term)               // - K^T (e^G dV)
+                    for (int term = 0; term < 3; ++term)               // - K^T (e^G dV)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t a = TM_UZ + (term < 2 ? term * 16 : 64) + (j / 2) * 32 + (j % 2) * 8;
-                        tc::mma_ts(tm + TM_S, tm + a, tc::sdesc(st + L::KQ + j * 2048, 16384, 1024), iS, 1);
-                    }
-                tc::mma_commit(&bars.m3);
-                tc::mma_commit(&bars.empty[it & 1]);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t a = TM_UZ + (term < 2 ? term * 16 : 64) + (j / 2) * 32 + (j % 2) * 8;
+                            tc::mma_ts(tm + TM_S, tm + a, tc::sdesc(st + L::KQ + j * 2048, 16384, 1024), iS, 1);
+                        }
+                    tc::mma_commit(&bars.m3);
+                    tc::mma_commit(&bars.empty[it & 1]);
+                }
             }
             if (chunks > 0) chain_wait(bars, &bars.m3, (chunks - 1) & 1);
         }
-        __syncwarp();
     } else if (warp >= kEpiWarps) {            // ------------------------------------------ e^G dO; dV and sums over y
         regs_down<kRegOut>();
         const int quarter = warp & 3, row = 32 * quarter + lane, x = threadIdx.x - 32 * kEpiWarps;
@@ -718,6 +748,16 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             tc::tmem_st_wait();
             tc::tc_fence_before();
             tc::mbar_arrive(&bars.d);
+            float w[32];
+            const float4* wp = reinterpret_cast<const float4*>(ws.w + wh * 64 * dv) + (live ? row : 0);
+            auto load_w = [&](int half) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 a = live ? wp[(size_t)(8 * half + i) * dv] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+                }
+            };
+            load_w(0);
             chain_wait(bars, &bars.u, it & 1);
             tc::tc_fence_after();
 #pragma unroll 1
@@ -729,18 +769,11 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     tc::tc_fence_before();
                     tc::mbar_arrive(&bars.out);
                 }
-                {
-                    float w[32];
-                    const float4* wp = reinterpret_cast<const float4*>(ws.w + wh * 64 * dv) + (size_t)(8 * half) * dv + (live ? row : 0);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 a = live ? wp[i * dv] : make_float4(0.f, 0.f, 0.f, 0.f);
-                        w[4 * i] = a.x * y[4 * i]; w[4 * i + 1] = a.y * y[4 * i + 1];
-                        w[4 * i + 2] = a.z * y[4 * i + 2]; w[4 * i + 3] = a.w * y[4 * i + 3];
-                    }
-                    const float db = lane_sums(w);
-                    if (quarter < strips) part[PART_DB + 32 * half + lane] = db;
-                }
+                for (int i = 0; i < 32; i += 2) mul2(w[i], w[i + 1], y[i], y[i + 1]);
+                const float db = lane_sums(w);
+                if (quarter < strips) part[PART_DB + 32 * half + lane] = db;
+                if (half == 0) load_w(1);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     y[i] *= vec[VEC_BETA + 32 * half + i];
@@ -770,11 +803,21 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll 1
         for (int it = 0; it <= chunks; ++it) {
             const int c = chunks - 1 - it;
+            // the state behind the chunk (after the first chunk: before it), asked for while the update's
+            // product runs
+            uint4 sh[H / 8], sl[H / 8];
+            const size_t next = ((size_t)(slot0 + c + 1) * Hv + h) * mat + ((size_t)(wg * H / 8) * dv + row) * 8;
+#pragma unroll
+            for (int i = 0; i < H / 8; ++i) {
+                const bool in = live && chunks > 0 && wg * H + 8 * i < dk;
+                sh[i] = in ? *reinterpret_cast<const uint4*>(ws.shi + next + (size_t)i * dv * 8) : make_uint4(0, 0, 0, 0);
+                sl[i] = in ? *reinterpret_cast<const uint4*>(ws.slo + next + (size_t)i * dv * 8) : make_uint4(0, 0, 0, 0);
+            }
             if (it > 0) {                      // dS <- e^{G_C} dS + update
                 const float whole = reinterpret_cast<const float*>(sm + ((it - 1) & 1) * L::BYTES + L::VECS)[VEC_EG + 63];
                 chain_wait(bars, &bars.m3, (it - 1) & 1);
                 tc::tc_fence_after();
-                add_update<H>(s, whole, tl + TM_S + wg * H);
+                add_update<H, 16>(s, whole, tl + TM_S + wg * H);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bars.empty[(it - 1) & 1]);
             }
@@ -785,29 +828,21 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 tc::tc_fence_before();
                 tc::mbar_arrive(&bars.s);
             }
-            // <S', dS> with the state behind the chunk (after the first chunk: with the one before it), and
-            // dS itself for the gradients of k
+            // <S', dS>, and dS itself for the gradients of k
             if (quarter < strips && chunks > 0) {
-                float dot = 0.f;
-                if (live) {
-                    const size_t col = ((size_t)(wg * H / 8) * dv + row) * 8, at0 = ((size_t)(slot0 + c) * Hv + h) * mat + col;
-                    const size_t next = at0 + Hv * mat;
+                float dot0 = 0.f, dot1 = 0.f;
 #pragma unroll
-                    for (int i = 0; i < H; i += 8) {
-                        if (wg * H + i >= dk) break;
-                        const size_t at = (size_t)(i / 8) * dv * 8;
-                        const uint4 a = *reinterpret_cast<const uint4*>(ws.shi + next + at), b = *reinterpret_cast<const uint4*>(ws.slo + next + at);
-                        const uint32_t hi[4] = {a.x, a.y, a.z, a.w}, lo[4] = {b.x, b.y, b.z, b.w};
-                        uint32_t out[4];
+                for (int i = 0; i < H / 8; ++i) {
+                    const uint32_t hi[4] = {sh[i].x, sh[i].y, sh[i].z, sh[i].w}, lo[4] = {sl[i].x, sl[i].y, sl[i].z, sl[i].w};
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            dot = fmaf(state_lo(hi[j], lo[j]), s[i + 2 * j], dot);
-                            dot = fmaf(state_hi(hi[j], lo[j]), s[i + 2 * j + 1], dot);
-                            out[j] = pack2(s[i + 2 * j], s[i + 2 * j + 1]);
-                        }
-                        if (it < chunks) *reinterpret_cast<uint4*>(ws.dshi + at0 + at) = make_uint4(out[0], out[1], out[2], out[3]);
-                    }
+                    for (int j = 0; j < 4; ++j)
+                        fma2(dot0, dot1, state_lo(hi[j], lo[j]), state_hi(hi[j], lo[j]), s[8 * i + 2 * j], s[8 * i + 2 * j + 1]);
+                    if (it < chunks && live && wg * H + 8 * i < dk)
+                        *reinterpret_cast<uint4*>(ws.dshi + next - Hv * mat + (size_t)i * dv * 8) =
+                            make_uint4(pack2(s[8 * i], s[8 * i + 1]), pack2(s[8 * i + 2], s[8 * i + 3]), pack2(s[8 * i + 4], s[8 * i + 5]),
+                                       pack2(s[8 * i + 6], s[8 * i + 7]));
                 }
+                float dot = dot0 + dot1;
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
                 if (lane == 0)
