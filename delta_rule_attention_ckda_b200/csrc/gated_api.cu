@@ -263,14 +263,18 @@ cudaError_t run_chain_bwd(const Call& c, const Maps& m, const ChainIn& in) {
     return cudaPeekAtLastError();
 }
 template <int DK, int DV>
-cudaError_t run_grads(const Call& c) {
+cudaError_t run_grads(const Call& c, const Maps& m, const ChainIn& in) {
     constexpr size_t smem = GradSmem<DK, DV>::BYTES;
     cudaError_t e = kernel_ready(grad_kernel<DK, DV>, smem);
     if (e != cudaSuccess) return e;
     const long long slots = (long long)Seqs::slots(c.s.N, c.s.total), items = slots * c.s.Hk;
-    if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (slots * c.s.Hv * C > 0x7fffffffLL) return cudaErrorInvalidValue;      // row numbers of the updates
+    CUtensorMap gv{}, u{};
+    if (in.maps && !(rows_map(&gv, c.gv, c.s.total, c.s.Hv, c.s.dv, (long long)c.s.Hv * c.s.dv) &&
+                     rows_map(&u, c.ws.u, slots * c.s.Hv * C, 1, c.s.dv, c.s.dv)))
+        return cudaErrorInvalidValue;
     grad_kernel<DK, DV><<<(unsigned)std::min<long long>(items, sm_count()), 256, smem, c.st>>>(
-        c.q, c.k, c.grad_o, c.gv, c.gq, c.gk, c.gg, c.gb, c.ws, c.seqs, (int)slots, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv, c.qs, c.ks);
+        m.q, m.k, m.o, gv, u, in, c.gv, c.gq, c.gk, c.gg, c.gb, c.ws, c.seqs, (int)slots, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
     return cudaPeekAtLastError();
 }
 
@@ -288,7 +292,7 @@ cudaError_t run_chunked(const Call& c) {
     if (e == cudaSuccess) e = run_chain_fwd<DK, kBack>(c, m, in);
     if constexpr (kBack) {
         if (e == cudaSuccess) e = run_chain_bwd<DK>(c, m, in);
-        if (e == cudaSuccess) e = c.s.dv <= 64 ? run_grads<DK, 64>(c) : run_grads<DK, 128>(c);
+        if (e == cudaSuccess) e = c.s.dv <= 64 ? run_grads<DK, 64>(c, m, in) : run_grads<DK, 128>(c, m, in);
     }
     return e;
 }

@@ -15,25 +15,55 @@
 // dbeta come from the chains' fp32 sums. Memory-bound: per chunk and head 157 KB are read (states
 // and cotangents 64, the rest tokens) for 2500 warp products. One CTA of eight warps an SM walks
 // over (chunk, key head) pairs; every tile of the next pair is asked for as soon as the products
-// that read its place are done, so about 100 KB are always on their way. Dw and Da are formed by four warps each and pass through
+// that read its place are done, so about 100 KB are always on their way. The tiles come by bulk
+// and tensor copies: the same loop on cp.async, 16 bytes a thread, spent 40% of its time issuing
+// them. A chunk that ends inside comes row by row, with zeros behind its end. Dw and Da are formed by four warps each and pass through
 // shared memory, where they serve as left operands straight and transposed; then a warp owns 16
 // tokens and half of the channels. Value heads that share a key head are summed in the
 // accumulators, in head order.
 #pragma once
-#include "gated_mma.cuh"
+#include "gated_chain.cuh"
 
 namespace ckda {
 namespace gated {
 
-// Shared memory (bytes): token tiles twice, states and keys once.
+// Shared memory (bytes from a 1024-aligned base): token tiles twice, states and keys once. Token
+// tiles are blocks of [64][64] with the 128-byte swizzle; states lie as in the workspace.
 template <int DK, int DV>
 struct GradSmem {
-    static constexpr int LDV = ld_bytes(DV), LDK = ld_bytes(DK);
-    static constexpr int DO = 0, U = DO + 64 * LDV, DVV = U + 64 * LDV, VECS = DVV + 64 * LDV, TOKENS = VECS + VEC * 4;
-    static constexpr int S = 2 * TOKENS, DS = S + DV * LDK, K = DS + DV * LDK, Q = K + 64 * LDK, DW = Q + 64 * LDK,
-                         DA = DW + 64 * LD64, BYTES = DA + 64 * LD64;
+    static constexpr int TILE = DV / 64 * 8192, KTILE = DK / 64 * 8192;
+    static constexpr int DO = 0, U = DO + TILE, DVV = U + TILE, VECS = DVV + TILE, TOKENS = VECS + 2048;
+    static constexpr int S = 2 * TOKENS, DS = S + DK * DV * 2, K = DS + DK * DV * 2, Q = K + KTILE, DW = Q + KTILE,
+                         DA = DW + 64 * LD64, BYTES = DA + 64 * LD64 + 1024;
 };
 static_assert(GradSmem<128, 128>::BYTES <= 232448, "more shared memory than an SM has");
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(tc::smem_u32(bar))
+                 : "memory");
+}
+
+// This lane's part of an ldmatrix address in a swizzled tile: rows as ofs_n or ofs_k; the fragment's
+// column c0 (a multiple of 16) enters by frag().
+__device__ __forceinline__ uint32_t swz_lane(bool rows_by_bit4) {
+    const int l = threadIdx.x & 31, hi = (l >> 4) & 1, lo = (l >> 3) & 1;
+    const int row = (l & 7) + (rows_by_bit4 ? hi : lo) * 8, piece = rows_by_bit4 ? lo : hi;
+    return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ uint32_t frag(uint32_t lane, int r0, int c0) {
+    return (lane ^ (uint32_t)((c0 % 64) * 2)) + (uint32_t)(r0 * 128 + (c0 / 64) * 8192);
+}
+
+struct GradBars {
+    uint64_t tokens[2], s, ds, kq;
+    int dead;
+};
+__device__ __forceinline__ void grad_wait(GradBars& b, uint64_t* bar, uint32_t phase) {
+    if (tc::mbar_try_wait(bar, phase)) return;
+    if (*reinterpret_cast<volatile int*>(&b.dead)) return;
+    if (!tc::mbar_wait(bar, phase)) *reinterpret_cast<volatile int*>(&b.dead) = 1;
+}
 
 // One (chunk, value head): where its rows lie.
 struct GradUnit {
@@ -43,13 +73,15 @@ struct GradUnit {
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(256, 1)
-grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ grad_o,
+grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mo,
+            const __grid_constant__ CUtensorMap mgv, const __grid_constant__ CUtensorMap mu, const ChainIn in,
             const __nv_bfloat16* __restrict__ grad_v, __nv_bfloat16* __restrict__ grad_q, __nv_bfloat16* __restrict__ grad_k,
-            float* __restrict__ grad_g, float* __restrict__ grad_beta, ChunkWs ws, Seqs seqs, int slots, int Hk, int Hv, int dk,
-            int dv, long long qs, long long ks) {
+            float* __restrict__ grad_g, float* __restrict__ grad_beta, ChunkWs ws, Seqs seqs, int slots, int Hk, int Hv, int dk, int dv) {
     using L = GradSmem<DK, DV>;
-    constexpr int LDV = L::LDV, LDK = L::LDK, NH = DK / 16;             // tiles of 8 channels a warp owns
-    extern __shared__ __align__(16) unsigned char sm[];
+    constexpr int NH = DK / 16;                                         // tiles of 8 channels a warp owns
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ GradBars bars;
     const uint32_t base = s32(sm);
     const int rep = Hv / Hk, items = slots * Hk, strips = (dv + 31) / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, t2 = 2 * (lane & 3);
@@ -79,44 +111,95 @@ grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
             return;
         }
     };
+    // rows of a tensor into a swizzled tile, zeros behind the chunk's end and the head's channels
+    auto rows = [&](uint32_t to, const __nv_bfloat16* from, long long stride, int nt, int d, int width) {
+#pragma unroll 1
+        for (int e = tid; e < 8 * width; e += 256) {
+            const int r = e / (width / 8), p = e % (width / 8);
+            const bool is = r < nt && p * 8 < d;
+            cp16(to + (p / 8) * 8192 + swz(r, p & 7), is ? from + r * stride + p * 8 : from, is);
+        }
+    };
     auto load_tokens = [&](const GradUnit& u, int b) {
         const uint32_t to = base + b * L::TOKENS;
         const int h = (u.item % Hk) * rep + u.r;
-        load_rows<DV, 256>(to + L::DO, grad_o + (u.tok * Hv + h) * dv, (long long)Hv * dv, u.nt, dv);
-        load_rows<DV, 256>(to + L::U, ws.u + u.wh * 64 * dv, dv, 64, dv);
-        load_rows<DV, 256>(to + L::DVV, grad_v + (u.tok * Hv + h) * dv, (long long)Hv * dv, u.nt, dv);
-        for (int e = tid; e < VEC / 4; e += 256) cp16(to + L::VECS + e * 16, ws.vec + u.wh * VEC + e * 4, true);
-    };
-
-    auto load_state = [&](const GradUnit& u, int to, const __nv_bfloat16* from) {
-#pragma unroll 4
-        for (int e = tid; e < DV * (DK / 8); e += 256) {
-            const int row = e % DV, p = e / DV;
-            const bool in = row < dv && p * 8 < dk;
-            cp16(base + to + row * LDK + p * 16, from + u.wh * mat + (in ? ((size_t)p * dv + row) * 8 : 0), in);
+        const bool tiles = in.maps && u.nt == C;
+        if (tid == 0) {
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive_expect_tx(&bars.tokens[b], VEC * 4 + (tiles ? 3 * L::TILE : 0));
+            bulk_copy(to + L::VECS, ws.vec + u.wh * VEC, VEC * 4, &bars.tokens[b]);
+            if (tiles) {
+#pragma unroll
+                for (int x = 0; x < DV / 64; ++x) {
+                    tma_rows(to + L::DO + x * 8192, &mo, &bars.tokens[b], 64 * x, h, (int)u.tok);
+                    tma_rows(to + L::U + x * 8192, &mu, &bars.tokens[b], 64 * x, 0, (int)(u.wh * 64));
+                    tma_rows(to + L::DVV + x * 8192, &mgv, &bars.tokens[b], 64 * x, h, (int)u.tok);
+                }
+            }
         }
+        if (!tiles) {
+            rows(to + L::DO, in.dO + (u.tok * Hv + h) * dv, (long long)Hv * dv, u.nt, dv, DV);
+            rows(to + L::U, ws.u + u.wh * 64 * dv, dv, 64, dv, DV);
+            rows(to + L::DVV, grad_v + (u.tok * Hv + h) * dv, (long long)Hv * dv, u.nt, dv, DV);
+        }
+        cp_commit();
     };
+    auto load_keys = [&](const GradUnit& u) {
+        const int hk = u.item % Hk;
+        const bool tiles = in.maps && u.nt == C;
+        if (tid == 0) {
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive_expect_tx(&bars.kq, tiles ? 2 * L::KTILE : 0);
+            if (tiles) {
+#pragma unroll
+                for (int x = 0; x < DK / 64; ++x) {
+                    tma_rows(base + L::K + x * 8192, &mk, &bars.kq, 64 * x, hk, (int)u.tok);
+                    tma_rows(base + L::Q + x * 8192, &mq, &bars.kq, 64 * x, hk, (int)u.tok);
+                }
+            }
+        }
+        if (!tiles) {
+            rows(base + L::K, in.k + u.tok * in.ks + (size_t)hk * dk, in.ks, u.nt, dk, DK);
+            rows(base + L::Q, in.q + u.tok * in.qs + (size_t)hk * dk, in.qs, u.nt, dk, DK);
+        }
+        cp_commit();
+    };
+    // a state as it lies in the workspace, [dk / 8][dv][8]: group p of 8 channels at p * dv * 16 bytes
+    auto load_state = [&](const GradUnit& u, int to, const __nv_bfloat16* from, uint64_t* bar) {
+        if (tid != 0) return;
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive_expect_tx(bar, (uint32_t)(mat * 2));
+        bulk_copy(base + to, from + u.wh * mat, (uint32_t)(mat * 2), bar);
+    };
+    if (tid == 0) {
+        for (uint64_t* e : {&bars.tokens[0], &bars.tokens[1], &bars.s, &bars.ds, &bars.kq}) tc::mbar_init(e, 1);
+        bars.dead = 0;
+        tc::fence_mbar_init();
+    }
+    for (int i = tid; i < (L::BYTES - 1024) / 16; i += 256) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    const uint32_t ln = swz_lane(true), lk = swz_lane(false);           // as ofs_n / ofs_at, as ofs_k / ofs_a
+    // rows of a state tile as the right operand's k: this lane's row and group of channels
+    const uint32_t ls = (uint32_t)(((lane & 7) + ((lane >> 3) & 1) * 8) * 16 + ((lane >> 4) & 1) * dv * 16);
 
     float gq[NH][4], gk[NH][4];
     GradUnit u{-1, 0, 0, 0, 0, 0};
     advance(u);
-    // groups in flight at the loop's top: the tokens (arrived), S, dS
-    if (u.item < items) load_tokens(u, 0);
-    cp_commit();
-    if (u.item < items) load_state(u, L::S, ws.shi);
-    cp_commit();
-    if (u.item < items) load_state(u, L::DS, ws.dshi);
-    cp_commit();
-    cp_wait<2>();
+    if (u.item < items) {
+        load_tokens(u, 0);
+        load_state(u, L::S, ws.shi, &bars.s);
+        load_state(u, L::DS, ws.dshi, &bars.ds);
+    }
 #pragma unroll 1
-    for (int b = 0; u.item < items; b ^= 1) {
-        const int hk = u.item % Hk, h = hk * rep + u.r;
+    for (int it = 0; u.item < items; ++it) {
+        const int hk = u.item % Hk, h = hk * rep + u.r, b = it & 1;
+        const bool tiles = in.maps && u.nt == C;                        // else its rows come by cp.async
         const uint32_t tk = base + b * L::TOKENS;
         const float* vec = reinterpret_cast<const float*>(sm + b * L::TOKENS + L::VECS);
+        grad_wait(bars, &bars.tokens[b], (it >> 1) & 1);
+        if (!tiles) cp_wait<0>();
         __syncthreads();                       // the tokens are in; the last products of the unit before are done
-        load_rows<DK, 256>(base + L::K, k + u.tok * ks + (size_t)hk * dk, ks, u.nt, dk);
-        load_rows<DK, 256>(base + L::Q, q + u.tok * qs + (size_t)hk * dk, qs, u.nt, dk);
-        cp_commit();
+        load_keys(u);
         if (u.r == 0) {
 #pragma unroll
             for (int i = 0; i < NH; ++i)
@@ -152,12 +235,12 @@ grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
 #pragma unroll
             for (int d = 0; d < DV; d += 16) {
                 uint32_t f[4];
-                ldm4(f, left + ofs_a(LDV) + at(16 * rb, d, LDV));
+                ldm4(f, left + frag(lk, 16 * rb, d));
 #pragma unroll
                 for (int jp = 0; jp < 4; ++jp)
                     if (jp <= rb) {
                         uint32_t x[4];
-                        ldm4(x, tk + L::U + ofs_n(LDV) + at(16 * jp, d, LDV));
+                        ldm4(x, tk + L::U + frag(ln, 16 * jp, d));
                         mma(w[2 * jp], f, x[0], x[1]);
                         mma(w[2 * jp + 1], f, x[2], x[3]);
                     }
@@ -187,7 +270,6 @@ grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
         advance(next);
         const bool more = next.item < items;
         if (more) load_tokens(next, b ^ 1);
-        cp_commit();
         if (warp == 0) {                       // dg and dbeta
             float a[2] = {0.f, 0.f}, e[2] = {0.f, 0.f}, db[2] = {0.f, 0.f};
 #pragma unroll
@@ -217,7 +299,7 @@ grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
                 }
             }
         }
-        cp_wait<3>();
+        grad_wait(bars, &bars.s, it & 1);
         __syncthreads();                       // S is in; Dw and Da are written
         const float eg[2] = {vec[VEC_EG + 16 * rb + gi], vec[VEC_EG + 16 * rb + gi + 8]};
         const float dc[2] = {vec[VEC_DEC + 16 * rb + gi], vec[VEC_DEC + 16 * rb + gi + 8]};
@@ -230,11 +312,11 @@ grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
 #pragma unroll
             for (int d = 0; d < DV; d += 16) {
                 uint32_t f[4];
-                ldm4(f, tk + X + ofs_a(LDV) + at(16 * rb, d, LDV));
+                ldm4(f, tk + X + frag(lk, 16 * rb, d));
 #pragma unroll
                 for (int jp = 0; jp < NH / 2; ++jp) {
                     uint32_t x[4];
-                    ldm4t(x, base + M + ofs_k(LDK) + at(d, d0 + 16 * jp, LDK));
+                    ldm4t(x, base + M + ls + (uint32_t)(((d0 + 16 * jp) / 8 * dv + d) * 16));
                     mma(acc[2 * jp], f, x[0], x[1]);
                     mma(acc[2 * jp + 1], f, x[2], x[3]);
                 }
@@ -252,20 +334,19 @@ grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
             for (int i = 0; i < NH; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) gk[i][e] = fmaf(-eg[e >> 1], acc[i][e], gk[i][e]);
-            cp_wait<2>();
+            grad_wait(bars, &bars.ds, it & 1);
             __syncthreads();                   // dS is in; S is done with
-            if (more) load_state(next, L::S, ws.shi);
-            cp_commit();
+            if (more) load_state(next, L::S, ws.shi, &bars.s);
             times(L::U, L::DS, acc);
 #pragma unroll
             for (int i = 0; i < NH; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) gk[i][e] = fmaf(dc[e >> 1], acc[i][e], gk[i][e]);
         }
-        cp_wait<2>();
+        grad_wait(bars, &bars.kq, it & 1);
+        if (!tiles) cp_wait<0>();
         __syncthreads();                       // K and Q are in; dS is done with
-        if (more) load_state(next, L::DS, ws.dshi);
-        cp_commit();
+        if (more) load_state(next, L::DS, ws.dshi, &bars.ds);
 #pragma unroll 1
         for (int j = 0; j <= rb; ++j) {        // Dw K, Da K
             uint32_t fw[4], fa[4];
@@ -274,7 +355,7 @@ grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
 #pragma unroll
             for (int jp = 0; jp < NH / 2; ++jp) {
                 uint32_t x[4];
-                ldm4t(x, base + L::K + ofs_k(LDK) + at(16 * j, d0 + 16 * jp, LDK));
+                ldm4t(x, base + L::K + frag(lk, 16 * j, d0 + 16 * jp));
                 mma(gq[2 * jp], fw, x[0], x[1]);
                 mma(gq[2 * jp + 1], fw, x[2], x[3]);
                 mma(gk[2 * jp], fa, x[0], x[1]);
@@ -289,10 +370,10 @@ grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
 #pragma unroll
             for (int jp = 0; jp < NH / 2; ++jp) {
                 uint32_t x[4];
-                ldm4t(x, base + L::Q + ofs_k(LDK) + at(16 * ip, d0 + 16 * jp, LDK));
+                ldm4t(x, base + L::Q + frag(lk, 16 * ip, d0 + 16 * jp));
                 mma(gk[2 * jp], fw, x[0], x[1]);
                 mma(gk[2 * jp + 1], fw, x[2], x[3]);
-                ldm4t(x, base + L::K + ofs_k(LDK) + at(16 * ip, d0 + 16 * jp, LDK));
+                ldm4t(x, base + L::K + frag(lk, 16 * ip, d0 + 16 * jp));
                 mma(gk[2 * jp], fa, x[0], x[1]);
                 mma(gk[2 * jp + 1], fa, x[2], x[3]);
             }
@@ -311,9 +392,7 @@ grad_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict
                 }
         }
         u = next;
-        cp_wait<2>();                          // the next unit's tokens
     }
-    cp_wait<0>();
 }
 
 }  // namespace gated
