@@ -110,6 +110,30 @@ struct ChainIn {
     int maps;                       // whether the maps are usable (heads of at least 64 channels)
 };
 
+// Long sequences on few heads run as segments of `cps` chunks side by side. A segment acts on the
+// state entering it as S -> M S + N; pass kSegMaps builds every segment's N (from zero, the first
+// from S0) and M (from the identity, with v = 0) at once, segment_prefix_kernel chains them into the
+// state behind every segment, and pass kSegRun runs the segments again from those. Segment j of
+// sequence n has place start / (cps C) + n + j of its own, as chunks have.
+enum { kSegWhole = 0, kSegMaps = 1, kSegRun = 2 };
+struct SegArgs {
+    int mode, cps;
+    int apart;                      // the final states go to the last segments' places: S_T is S0, which others still read
+    float* states;                  // [place][Hv][dk][dv] fp32: N, then the state behind the segment
+    float* maps;                    // [place][Hv][dk][dk] fp32: M, transposed
+    __host__ __device__ static size_t places(int N, int total, int cps) { return (size_t)total / ((size_t)cps * C) + (size_t)N; }
+    __device__ __forceinline__ int first_place(int n, int start) const { return start / (cps * C) + n; }
+    __device__ __forceinline__ int find(const Seqs& seqs, int place) const {
+        int lo = 0, hi = seqs.N - 1;
+        while (lo < hi) {
+            const int m = (lo + hi + 1) / 2;
+            const int start = seqs.cu == nullptr ? m * seqs.T : min(max(__ldg(seqs.cu + m), 0), seqs.total);
+            if (first_place(m, start) <= place) lo = m; else hi = m - 1;
+        }
+        return lo;
+    }
+};
+
 // The loading warps' share (thread x) of a chunk into stage `st`, completing on `full`: k, q, v, dO
 // by tensor copies where the chunk is whole, else by rows with zeros behind the sequence's end;
 // the lower blocks of Z and P (those above the block diagonal stay the zeros the kernel starts
@@ -282,12 +306,12 @@ __device__ __forceinline__ float state_hi(uint32_t h, uint32_t l) {
 }
 
 // What both chains set up and take down.
-__device__ __forceinline__ void chain_begin(ChainBars& b, unsigned char* stages, uint32_t bytes) {
+__device__ __forceinline__ void chain_begin(ChainBars& b, unsigned char* stages, uint32_t bytes, int out_warps) {
     if (threadIdx.x / 32 == kMmaWarp) tc::tmem_alloc(&b.tmem, TM_COLS);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&b.full[i], 32 * kLoadWarps + 1);
-            tc::mbar_init(&b.empty[i], 1 + kEpiWarps + kOutWarps);
+            tc::mbar_init(&b.empty[i], 1 + kEpiWarps + out_warps);
         }
         for (uint64_t* e : {&b.s, &b.x, &b.u, &b.uo}) tc::mbar_init(e, 32 * kEpiWarps);
         for (uint64_t* e : {&b.d, &b.out, &b.qs}) tc::mbar_init(e, 32 * kOutWarps);
@@ -315,21 +339,45 @@ template <int DK, bool kBack>
 __global__ void __launch_bounds__(kChainThreads, 1)
 chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                  const __grid_constant__ CUtensorMap mo, const ChainIn in, const float* S0, __nv_bfloat16* __restrict__ o, float* ST,
-                 ChunkWs ws, Seqs seqs, int Hk, int Hv, int dk, int dv) {
+                 ChunkWs ws, Seqs seqs, SegArgs sg, int Hk, int Hv, int dk, int dv) {
     using L = ChainStage<DK, kBack>;
     constexpr int H = DK / 2;                  // channels of an epilogue thread
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ ChainBars bars;
-    const int n = blockIdx.x / Hv, h = blockIdx.x % Hv, hk = h / (Hv / Hk);
+    const int h = blockIdx.x % Hv, hk = h / (Hv / Hk), place = blockIdx.x / Hv;
+    const int n = !kBack && sg.mode ? sg.find(seqs, place) : place;
+    const bool maps = !kBack && sg.mode == kSegMaps, transition = maps && blockIdx.y == 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int start, len;
     bool ok;
     seqs.get(n, start, len, ok);
     if (!ok && h == 0 && threadIdx.x == 0) report_index_error();
-    const int chunks = (len + C - 1) / C, slot0 = seqs.first_slot(n, start), strips = (dv + 31) / 32;
+    int slot0 = seqs.first_slot(n, start);
+    const int strips = (dv + 31) / 32;
     const size_t mat = (size_t)dk * dv, sbase = ((size_t)n * Hv + h) * mat;
-    chain_begin(bars, sm, 2 * L::BYTES);
+    const float* from = S0 == nullptr ? nullptr : S0 + sbase;          // the entering state
+    float* to = ST == nullptr ? nullptr : ST + sbase;                  // where the leaving state goes
+    if (!kBack && sg.mode) {                   // this segment's chunks, as a sequence of their own
+        const int j = place - sg.first_place(n, start), skip = j * sg.cps;
+        if (j < 0 || (j > 0 && (long long)skip * C >= len)) return;
+        const bool last = (long long)(skip + sg.cps) * C >= len;
+        if (maps && (last || (transition && j == 0))) return;
+        const size_t own = (size_t)place * Hv + h;
+        if (maps) {
+            if (j > 0) from = nullptr;
+            to = transition ? sg.maps + own * dk * dk : sg.states + own * mat;
+        } else {
+            if (j > 0) from = sg.states + (own - Hv) * mat;
+            if (!last) to = nullptr;
+            else if (sg.apart) to = sg.states + own * mat;
+        }
+        slot0 += skip;
+        start += skip * C;
+        len = last ? len - skip * C : sg.cps * C;
+    }
+    const int chunks = (len + C - 1) / C, cols = transition ? dk : dv;  // columns of the state
+    chain_begin(bars, sm, 2 * L::BYTES, maps ? 0 : kOutWarps);
     const uint32_t tm = bars.tmem, base = s32(sm);
 
     if (warp >= kMmaWarp) {
@@ -367,7 +415,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t st = fresh(base + (c & 1) * L::BYTES), ph = c & 1;
-                if (c > 0) chain_wait(bars, &bars.qs, (c - 1) & 1);    // Q S of the chunk before is read
+                if (c > 0 && !maps) chain_wait(bars, &bars.qs, (c - 1) & 1);    // Q S of the chunk before is read
                 chain_wait(bars, &bars.s, ph);
                 tc::tc_fence_after();
                 if (elected()) {
@@ -381,7 +429,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                         }
                     tc::mma_commit(&bars.m1);
                 }
-                if (c > 0) output(c - 1);
+                if (c > 0 && !maps) output(c - 1);
                 chain_wait(bars, &bars.x, ph);
                 tc::tc_fence_after();
                 if (elected()) {
@@ -404,12 +452,13 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                             tc::mma_ts(tm + TM_S, tm + a, tc::sdesc(st + L::KQ + j * 2048, 16384, 1024), iS, (term | j) != 0);
                         }
                     tc::mma_commit(&bars.m3);
+                    if (maps) tc::mma_commit(&bars.empty[c & 1]);
                 }
                 if (c + 1 < chunks) chain_wait(bars, &bars.full[(c + 1) & 1], ((c + 1) >> 1) & 1);
             }
-            if (chunks > 0) {
-                output(chunks - 1);
-                chain_wait(bars, &bars.o, (chunks - 1) & 1);       // nothing in flight past this point
+            if (chunks > 0) {                  // nothing in flight past this point
+                if (!maps) output(chunks - 1);
+                chain_wait(bars, maps ? &bars.m3 : &bars.o, (chunks - 1) & 1);
             }
         }
     } else if (warp >= kEpiWarps) {            // ------------------------------------------ output
@@ -418,7 +467,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
         const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
         unsigned char* tile = sm + L::OUT;
 #pragma unroll 1
-        for (int c = 0; c < chunks; ++c) {
+        for (int c = 0; c < (maps ? 0 : chunks); ++c) {
             const unsigned char* st = sm + (c & 1) * L::BYTES;
             const float* eg = reinterpret_cast<const float*>(st + L::VECS) + VEC_EG;
             const int tok = start + c * C, nt = min(C, len - c * C);
@@ -479,13 +528,14 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     } else {                                   // ------------------------------------------ epilogues of the chain
         regs_up<kRegEpi>();
         const int quarter = warp & 3, wg = warp >> 2, row = 32 * quarter + lane;
-        const bool live = row < dv;
+        const bool live = row < cols;
         const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
         float s[H];
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             const int d = wg * H + i;
-            s[i] = (S0 != nullptr && live && d < dk) ? S0[sbase + (size_t)d * dv + row] : 0.f;
+            s[i] = (from != nullptr && live && d < dk) ? from[(size_t)d * dv + row] : 0.f;
+            if (transition && d == row && live) s[i] = 1.f;
         }
 #pragma unroll 1
         for (int c = 0; c <= chunks; ++c) {
@@ -518,6 +568,10 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             chain_wait(bars, &bars.full[c & 1], (c >> 1) & 1);
 #pragma unroll
             for (int i = 0; i < 32; ++i) y[i] = tile_value(st + L::V, 32 * wg + i, row);
+            if (transition) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = 0.f;
+            }
             chain_wait(bars, &bars.m1, c & 1);
             tc::tc_fence_after();
             tc::tmem_ld32<32>(tl + TM_ACC + 32 * wg, x);
@@ -594,16 +648,65 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
         }
         if constexpr (!kBack) {
-            if (ST != nullptr && live) {
+            if (to != nullptr && live) {
 #pragma unroll
                 for (int i = 0; i < H; ++i) {
                     const int d = wg * H + i;
-                    if (d < dk) ST[sbase + (size_t)d * dv + row] = s[i];
+                    if (d < dk) to[transition ? (size_t)row * dk + d : (size_t)d * dv + row] = s[i];
                 }
             }
         }
     }
     chain_end(bars);
+}
+
+// The state behind every segment, in place of its N: S_j = M_j S_{j-1} + N_j, fp32, in order. A CTA of
+// 256 threads takes 32 columns of one (sequence, head); a thread one row and 16 columns.
+__global__ void __launch_bounds__(256)
+segment_prefix_kernel(SegArgs sg, Seqs seqs, int Hv, int dk, int dv) {
+    __shared__ float S[128][33];
+    const int n = blockIdx.x / Hv, h = blockIdx.x % Hv, i = threadIdx.x & 127, j0 = (threadIdx.x >> 7) * 16, c0 = blockIdx.y * 32;
+    int start, len;
+    bool ok;
+    seqs.get(n, start, len, ok);
+    const int first = sg.first_place(n, start), count = (len + sg.cps * C - 1) / (sg.cps * C) - 1;   // the last needs none
+    const size_t mat = (size_t)dk * dv;
+    for (int seg = 0; seg < count; ++seg) {
+        const size_t own = (size_t)(first + seg) * Hv + h;
+        float* st = sg.states + own * mat;
+        float acc[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[j] = i < dk && c0 + j0 + j < dv ? st[(size_t)i * dv + c0 + j0 + j] : 0.f;
+        if (seg > 0 && i < dk) {
+            const float* M = sg.maps + own * dk * dk + i;
+#pragma unroll 8
+            for (int d = 0; d < dk; ++d) {
+                const float m = M[(size_t)d * dk];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[j] = fmaf(m, S[d][j0 + j], acc[j]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            if (i < dk) S[i][j0 + j] = acc[j];
+            if (seg > 0 && i < dk && c0 + j0 + j < dv) st[(size_t)i * dv + c0 + j0 + j] = acc[j];
+        }
+        __syncthreads();
+    }
+}
+
+// The final states from the last segments' places to S_T.
+__global__ void __launch_bounds__(256)
+segment_final_kernel(SegArgs sg, Seqs seqs, float* __restrict__ ST, int Hv, int mat) {
+    const int n = blockIdx.x / Hv, h = blockIdx.x % Hv;
+    int start, len;
+    bool ok;
+    seqs.get(n, start, len, ok);
+    const int last = sg.first_place(n, start) + max((len + sg.cps * C - 1) / (sg.cps * C) - 1, 0);
+    const float4* from = reinterpret_cast<const float4*>(sg.states + ((size_t)last * Hv + h) * mat);
+    float4* to = reinterpret_cast<float4*>(ST + (size_t)blockIdx.x * mat);
+    for (int i = threadIdx.x; i < mat / 4; i += 256) to[i] = from[i];
 }
 
 // The adjoint chain, chunks last to first, dS the cotangent of the state leaving a chunk:
@@ -630,7 +733,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     seqs.get(n, start, len, ok);
     const int chunks = (len + C - 1) / C, slot0 = seqs.first_slot(n, start), strips = (dv + 31) / 32;
     const size_t mat = (size_t)dk * dv, sbase = ((size_t)n * Hv + h) * mat;
-    chain_begin(bars, sm, 2 * L::BYTES);
+    chain_begin(bars, sm, 2 * L::BYTES, kOutWarps);
     const uint32_t tm = bars.tmem, base = s32(sm);
 
     if (warp >= kMmaWarp) {

@@ -205,6 +205,11 @@ def gated_fwd_workspace_bytes(N, total, Hk, Hv, dk, dv, dtype=torch.bfloat16) ->
     return int(load().ckda_gated_fwd_workspace_bytes(N, total, Hk, Hv, dk, dv, _dt(torch.empty(0, dtype=dtype))))
 
 
+def gated_segment_tokens(N, total, Hk, Hv, dk, dv, dtype=torch.bfloat16) -> int:
+    """Tokens in a segment where gated_chunk_fwd runs long sequences as segments (0: whole)."""
+    return int(load().ckda_gated_fwd_segment_tokens(N, total, Hk, Hv, dk, dv, _dt(torch.empty(0, dtype=dtype))))
+
+
 def gated_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, o=None, S_T=None, want_state=True, workspace=None,
                     stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """ckda_gated_fwd. Returns (o, S_T): o in v's type and shape (rows behind the last packed

@@ -79,6 +79,32 @@ def test_forward_packed(ck, case):
     assert (o[sum(lens):] == 7.0).all()
 
 
+SEGMENTED = [  # lengths (None: dense), Hk, Hv, dk, dv: long enough, on few heads, to run in segments
+    ((1, 2500), 1, 2, 128, 128), ((2, 2111), 1, 1, 64, 128), ((1, 2305), 1, 1, 128, 64), ((1, 2200), 1, 2, 96, 80),
+    ([4000, 70, 0, 4300], 1, 2, 128, 128), ([1, 6000], 2, 2, 64, 64),
+]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("case", SEGMENTED, ids=str)
+def test_forward_in_segments(ck, case, in_place):
+    lens, Hk, Hv, dk, dv = case
+    if isinstance(lens, tuple):
+        cu, lead, N, total = None, lens, lens[0], lens[0] * lens[1]
+    else:
+        cu, total = packed(lens, 3)
+        lead, N = (total,), len(lens)
+    assert 0 < ck.gated_segment_tokens(N, total, Hk, Hv, dk, dv) < total // N
+    q, k, v, g, b, S0, _, _ = make(lead, Hk, Hv, dk, dv, BF, total, N, gate=-5.0)      # a long memory
+    x = dev(q, k, v, g, b, S0)
+    o, ST = ck.gated_chunk_fwd(*x, cu_seqlens=None if cu is None else cu.cuda(), S_T=x[5] if in_place else None)
+    fine(ck)
+    o_ref, S_ref = ref.gated_fwd(q, k, v, g, b, S0, cu)
+    n = total if cu is None else sum(lens)
+    near("o", o.flatten(0, 1)[:n] if cu is None else o[:n], o_ref.flatten(0, 1)[:n] if cu is None else o_ref[:n])
+    near("S_T", ST, S_ref)
+
+
 @pytest.mark.parametrize("dt,d", [(BF, 128), (BF, 64), (F32, 32)])
 def test_forward_strided(ck, dt, d):
     """q, k and v as slices of one projection's rows."""
