@@ -245,16 +245,6 @@ struct Call {
     cudaStream_t st;
 };
 
-template <int DK>
-cudaError_t run_intra(const Call& c) {
-    constexpr size_t smem = intra_smem(DK);
-    cudaError_t e = kernel_ready(intra_kernel<DK>, smem);
-    if (e != cudaSuccess) return e;
-    intra_kernel<DK><<<dim3((unsigned)Seqs::slots(c.s.N, c.s.total), (unsigned)c.s.Hk), 128, smem, c.st>>>(
-        c.q, c.k, c.g, c.beta, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.qs, c.ks);
-    return cudaPeekAtLastError();
-}
-
 // Tensor map over [tokens][heads][channels] rows a token stride apart, boxes of 64 channels of one
 // head of 64 tokens, 128-byte swizzle; channels beyond the head read as zeros.
 bool rows_map(CUtensorMap* map, const bf16* base, long long tokens, int heads, int d, long long stride) {
@@ -271,6 +261,16 @@ bool rows_map(CUtensorMap* map, const bf16* base, long long tokens, int heads, i
 struct Maps {
     CUtensorMap q, k, v, o;
 };
+
+template <int DK>
+cudaError_t run_intra(const Call& c, const Maps& m, const ChainIn& in) {
+    constexpr size_t smem = intra_smem(DK);
+    cudaError_t e = kernel_ready(intra_kernel<DK>, smem);
+    if (e != cudaSuccess) return e;
+    intra_kernel<DK><<<dim3((unsigned)Seqs::slots(c.s.N, c.s.total), (unsigned)c.s.Hk), 128, smem, c.st>>>(
+        m.q, m.k, in, c.g, c.beta, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk);
+    return cudaPeekAtLastError();
+}
 
 template <int DK, bool kBack>
 cudaError_t run_chain_fwd(const Call& c, const Maps& m, const ChainIn& in) {
@@ -334,7 +334,7 @@ cudaError_t run_chunked(const Call& c) {
                         (!kBack || rows_map(&m.o, c.grad_o, c.s.total, c.s.Hv, c.s.dv, (long long)c.s.Hv * c.s.dv));
         if (!ok) return cudaErrorInvalidValue;
     }
-    cudaError_t e = run_intra<DK>(c);
+    cudaError_t e = run_intra<DK>(c, m, in);
     if (e == cudaSuccess) e = run_chain_fwd<DK, kBack>(c, m, in);
     if constexpr (kBack) {
         if (e == cudaSuccess) e = run_chain_bwd<DK>(c, m, in);

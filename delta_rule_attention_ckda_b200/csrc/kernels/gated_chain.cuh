@@ -82,17 +82,10 @@ __device__ __forceinline__ uint32_t fresh(uint32_t x) {
 template <int R> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-__device__ __forceinline__ uint32_t swz(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
 // Element (token, channel) of a tile of 64-channel blocks, read by the thread that owns the channel.
 __device__ __forceinline__ float tile_value(const unsigned char* tile, int token, int ch) {
     const uint16_t x = *reinterpret_cast<const uint16_t*>(tile + (ch / 64) * 8192 + swz(token, (ch % 64) / 8) + (ch % 8) * 2);
     return __uint_as_float((uint32_t)x << 16);
-}
-
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int head, int token) {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(c0), "r"(head), "r"(token)
-                 : "memory");
 }
 
 // One lane of a warp that walks together: it issues the products, with operands the whole warp holds.
@@ -101,14 +94,6 @@ __device__ __forceinline__ bool elected() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
-
-// What a chain kernel reads by rows: tensor maps over [tokens][heads][channels] (boxes of 64
-// tokens of one head's 64 channels), and plain pointers for the rows at a sequence's end.
-struct ChainIn {
-    const __nv_bfloat16 *q, *k, *v, *dO;
-    long long qs, ks, vs;
-    int maps;                       // whether the maps are usable (heads of at least 64 channels)
-};
 
 // Long sequences on few heads run as segments of `cps` chunks side by side. A segment acts on the
 // state entering it as S -> M S + N; pass kSegMaps builds every segment's N (from zero, the first

@@ -44,17 +44,6 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// This lane's part of an ldmatrix address in a swizzled tile: rows as ofs_n or ofs_k; the fragment's
-// column c0 (a multiple of 16) enters by frag().
-__device__ __forceinline__ uint32_t swz_lane(bool rows_by_bit4) {
-    const int l = threadIdx.x & 31, hi = (l >> 4) & 1, lo = (l >> 3) & 1;
-    const int row = (l & 7) + (rows_by_bit4 ? hi : lo) * 8, piece = rows_by_bit4 ? lo : hi;
-    return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4));
-}
-__device__ __forceinline__ uint32_t frag(uint32_t lane, int r0, int c0) {
-    return (lane ^ (uint32_t)((c0 % 64) * 2)) + (uint32_t)(r0 * 128 + (c0 / 64) * 8192);
-}
-
 struct GradBars {
     uint64_t tokens[2], s, ds, kq;
     int dead;
@@ -111,15 +100,6 @@ grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             return;
         }
     };
-    // rows of a tensor into a swizzled tile, zeros behind the chunk's end and the head's channels
-    auto rows = [&](uint32_t to, const __nv_bfloat16* from, long long stride, int nt, int d, int width) {
-#pragma unroll 1
-        for (int e = tid; e < 8 * width; e += 256) {
-            const int r = e / (width / 8), p = e % (width / 8);
-            const bool is = r < nt && p * 8 < d;
-            cp16(to + (p / 8) * 8192 + swz(r, p & 7), is ? from + r * stride + p * 8 : from, is);
-        }
-    };
     auto load_tokens = [&](const GradUnit& u, int b) {
         const uint32_t to = base + b * L::TOKENS;
         const int h = (u.item % Hk) * rep + u.r;
@@ -138,9 +118,9 @@ grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             }
         }
         if (!tiles) {
-            rows(to + L::DO, in.dO + (u.tok * Hv + h) * dv, (long long)Hv * dv, u.nt, dv, DV);
-            rows(to + L::U, ws.u + u.wh * 64 * dv, dv, 64, dv, DV);
-            rows(to + L::DVV, grad_v + (u.tok * Hv + h) * dv, (long long)Hv * dv, u.nt, dv, DV);
+            tile_rows<256>(to + L::DO, in.dO + (u.tok * Hv + h) * dv, (long long)Hv * dv, u.nt, dv, DV, tid);
+            tile_rows<256>(to + L::U, ws.u + u.wh * 64 * dv, dv, 64, dv, DV, tid);
+            tile_rows<256>(to + L::DVV, grad_v + (u.tok * Hv + h) * dv, (long long)Hv * dv, u.nt, dv, DV, tid);
         }
         cp_commit();
     };
@@ -159,8 +139,8 @@ grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             }
         }
         if (!tiles) {
-            rows(base + L::K, in.k + u.tok * in.ks + (size_t)hk * dk, in.ks, u.nt, dk, DK);
-            rows(base + L::Q, in.q + u.tok * in.qs + (size_t)hk * dk, in.qs, u.nt, dk, DK);
+            tile_rows<256>(base + L::K, in.k + u.tok * in.ks + (size_t)hk * dk, in.ks, u.nt, dk, DK, tid);
+            tile_rows<256>(base + L::Q, in.q + u.tok * in.qs + (size_t)hk * dk, in.qs, u.nt, dk, DK, tid);
         }
         cp_commit();
     };

@@ -4,6 +4,7 @@
 //
 #pragma once
 #include "gated_common.cuh"
+#include "tc_primitives.cuh"
 
 namespace ckda {
 namespace gated {
@@ -115,18 +116,45 @@ __device__ __forceinline__ void operand(const float (&u)[4], const float (&v)[4]
     a[3] = pack2(v[2], v[3]);
 }
 
-// Rows of a [tokens][...] tensor into a padded tile: `rows` of 64 rows present, `cols` of COLS
-// columns present (both padded with zeros). cols is a multiple of 8.
-template <int COLS, int NT>
-__device__ __forceinline__ void load_rows(uint32_t dst, const __nv_bfloat16* src, long long stride, int rows, int cols) {
-    constexpr int P = COLS / 8;
-#pragma unroll
-    for (int e = threadIdx.x; e < 64 * P; e += NT) {
-        const int r = e / P, p = e % P;
-        const bool in = r < rows && p * 8 < cols;
-        cp16(dst + r * ld_bytes(COLS) + p * 16, in ? src + r * stride + p * 8 : src, in);
+// Tiles of 64 tokens as tensor copies write them: blocks of [64 rows][64 channels], rows of 128
+// bytes, the 16-byte pieces of a row exchanged by its number (the 128-byte swizzle).
+__device__ __forceinline__ uint32_t swz(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int head, int token) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(tc::smem_u32(bar)), "r"(c0), "r"(head), "r"(token)
+                 : "memory");
+}
+
+// What the chunked kernels read by rows: tensor maps over [tokens][heads][channels] (boxes of 64
+// tokens of one head's 64 channels), and plain pointers for the rows at a sequence's end.
+struct ChainIn {
+    const __nv_bfloat16 *q, *k, *v, *dO;
+    long long qs, ks, vs;
+    int maps;                       // whether the maps are usable (heads of at least 64 channels)
+};
+
+// Rows of a tensor into such a tile of `width` channels, zeros behind the chunk's end (nt) and the
+// head's channels (d); thread x of NT.
+template <int NT>
+__device__ __forceinline__ void tile_rows(uint32_t to, const __nv_bfloat16* from, long long stride, int nt, int d, int width, int x) {
+#pragma unroll 1
+    for (int e = x; e < 8 * width; e += NT) {
+        const int r = e / (width / 8), p = e % (width / 8);
+        const bool is = r < nt && p * 8 < d;
+        cp16(to + (p / 8) * 8192 + swz(r, p & 7), is ? from + r * stride + p * 8 : from, is);
     }
 }
+// This lane's part of an ldmatrix address in a swizzled tile: rows as ofs_n or ofs_k; the fragment's
+// column c0 (a multiple of 16) enters by frag().
+__device__ __forceinline__ uint32_t swz_lane(bool rows_by_bit4) {
+    const int l = threadIdx.x & 31, hi = (l >> 4) & 1, lo = (l >> 3) & 1;
+    const int row = (l & 7) + (rows_by_bit4 ? hi : lo) * 8, piece = rows_by_bit4 ? lo : hi;
+    return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ uint32_t frag(uint32_t lane, int r0, int c0) {
+    return (lane ^ (uint32_t)((c0 % 64) * 2)) + (uint32_t)(r0 * 128 + (c0 / 64) * 8192);
+}
+
 // ---------------------------------------------------------------- workspace of the chunked kernels
 
 // Per chunk and value head, floats: e^G, e^{G_C - G}, beta, then G in two parts (G = hi + lo).
