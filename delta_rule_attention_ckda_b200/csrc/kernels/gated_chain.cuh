@@ -8,8 +8,8 @@
 // chunks; everything is held transposed, d_v on the 128 TMEM lanes, so that an epilogue thread
 // has one column of the state and each product's result, split into bf16 terms, is written
 // back to TMEM as the left operand of the next without crossing threads. Eight epilogue warps
-// (two per lane quarter, half of the channels or tokens each) keep S in fp32 registers; four
-// warps form the output; one thread issues the products; three warps load the next chunk's
+// (two per lane quarter, half of the channels or tokens each; sixteen with half the registers
+// measured 7 to 20% slower) keep S in fp32 registers; four warps form the output; one thread issues the products; three warps load the next chunk's
 // tiles, by tensor copies, or row by row where a chunk ends inside (zeros behind a packed
 // sequence's end, where a tile copy would bring the next sequence's rows).
 //
@@ -79,8 +79,12 @@ __device__ __forceinline__ uint32_t fresh(uint32_t x) {
     asm volatile("" : "+r"(x));
     return x;
 }
-template <int R> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+// A warp's registers from here on, above or below those of the launch (each has its own instruction).
+template <int R>
+__device__ __forceinline__ void set_regs() {
+    if constexpr (R > kRegLaunch) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R));
+    else if constexpr (R < kRegLaunch) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R));
+}
 
 // Element (token, channel) of a tile of 64-channel blocks, read by the thread that owns the channel.
 __device__ __forceinline__ float tile_value(const unsigned char* tile, int token, int ch) {
@@ -366,7 +370,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const uint32_t tm = bars.tmem, base = s32(sm);
 
     if (warp >= kMmaWarp) {
-        regs_down<kRegOther>();
+        set_regs<kRegOther>();
         if (warp > kMmaWarp) {                 // ------------------------------------------ loads
             const int x = threadIdx.x - 32 * (kMmaWarp + 1);
 #pragma unroll 1
@@ -447,7 +451,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
         }
     } else if (warp >= kEpiWarps) {            // ------------------------------------------ output
-        regs_down<kRegOut>();
+        set_regs<kRegOut>();
         const int quarter = warp & 3, row = 32 * quarter + lane, x = threadIdx.x - 32 * kEpiWarps;
         const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
         unsigned char* tile = sm + L::OUT;
@@ -511,7 +515,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
         }
     } else {                                   // ------------------------------------------ epilogues of the chain
-        regs_up<kRegEpi>();
+        set_regs<kRegEpi>();
         const int quarter = warp & 3, wg = warp >> 2, row = 32 * quarter + lane;
         const bool live = row < cols;
         const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
@@ -722,7 +726,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const uint32_t tm = bars.tmem, base = s32(sm);
 
     if (warp >= kMmaWarp) {
-        regs_down<kRegOther>();
+        set_regs<kRegOther>();
         if (warp > kMmaWarp) {                 // ------------------------------------------ loads
             const int x = threadIdx.x - 32 * (kMmaWarp + 1);
 #pragma unroll 1
@@ -810,7 +814,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             if (chunks > 0) chain_wait(bars, &bars.m3, (chunks - 1) & 1);
         }
     } else if (warp >= kEpiWarps) {            // ------------------------------------------ e^G dO; dV and sums over y
-        regs_down<kRegOut>();
+        set_regs<kRegOut>();
         const int quarter = warp & 3, row = 32 * quarter + lane, x = threadIdx.x - 32 * kEpiWarps;
         const bool live = row < dv;
         const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
@@ -878,7 +882,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             out_sync();
         }
     } else {                                   // ------------------------------------------ epilogues of the chain
-        regs_up<kRegEpi>();
+        set_regs<kRegEpi>();
         const int quarter = warp & 3, wg = warp >> 2, row = 32 * quarter + lane;
         const bool live = row < dv;
         const uint32_t tl = tm + ((uint32_t)(32 * quarter) << 16);
