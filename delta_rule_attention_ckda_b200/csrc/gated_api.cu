@@ -519,7 +519,7 @@ namespace {
 
 // Blocks of the backward pass, which each leave a partial sum of the weights' gradients: fixed by
 // the sizes alone, so those sums have one order.
-constexpr int kPrepMaxBlocks = 148 * 2;
+constexpr int kPrepMaxBlocks = 148 * 3;
 int prep_blocks(long long units) { return (int)std::max(1LL, std::min(units, (long long)kPrepMaxBlocks)); }
 
 ckda_status_t prep_args(PrepArgs& a, const void* q, const void* k, const float* qw, const float* kw, const void* pos,

@@ -17,7 +17,7 @@ namespace ckda {
 namespace gated {
 
 template <int DK, int CW, typename TIn>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 2)
 decode_kernel(const TIn* __restrict__ q, const TIn* __restrict__ k, const TIn* __restrict__ v,
               const float* __restrict__ g, const float* __restrict__ beta, float* __restrict__ S, TIn* __restrict__ o,
               const int* __restrict__ slots, int pool, int Hk, int Hv, int dv, long long qs, long long ks, long long vs) {

@@ -107,13 +107,19 @@ def _span(t):
 
 
 def _apart(out, name: str, others) -> None:
-    """An output may share memory with none of `others` ((name, span) pairs of _span)."""
+    """An output may share memory with none of `others` ((name, tensor) pairs; None names none)."""
     mine = _span(out)
     if mine is None:
         return
     a, b = mine
-    for other, span in others:
-        if span is not None and a < span[1] and span[0] < b:
+    for other, t in others:
+        if t is None:
+            continue
+        p = t.data_ptr()
+        if p >= b or p == 0:
+            continue
+        span = _span(t)
+        if span is not None and a < span[1]:
             raise ValueError(f"{name} overlaps {other}")
 
 
@@ -121,18 +127,25 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle of a device, without making a stream object where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _launch(dev, stream, fn, where: str, args) -> None:
     """Calls fn(*args, stream) with `dev` as the current device, which the library launches on."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
+        raw = _raw_stream(dev.index)
     elif stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the call's tensors are on {dev}")
+    else:
+        raw = stream.cuda_stream
     if torch.cuda.current_device() == dev.index:
-        st = fn(*args, stream.cuda_stream)
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, stream.cuda_stream)
-    _raise(st, where)
+            st = fn(*args, raw)
+    if st:
+        _raise(st, where)
 
 
 @lru_cache(maxsize=4096)
@@ -195,8 +208,8 @@ class _Problem:
         self.state_shape = (N, Hv, dk, dv)
         if S0 is not None:
             _check(S0, "S0", self.state_shape, F32, dev)
-        self.spans = [("q", _span(q)), ("k", _span(k)), ("v", _span(v)), ("g", _span(g)), ("beta", _span(beta)),
-                      ("cu_seqlens", _span(cu_seqlens))]
+        self.spans = [("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta),
+                      ("cu_seqlens", cu_seqlens)]
         self.sizes = (N, T, total, Hk, Hv, dk, dv, qs, ks, vs, self.dt)
         self.ws_sizes = (N, total, Hk, Hv, dk, dv, self.dt)
 
@@ -222,11 +235,11 @@ def gated_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, o=None, S_T=N
         o = torch.empty(p.o_shape, device=dev, dtype=v.dtype)
     else:
         _check(o, "o", p.o_shape, v.dtype, dev)
-        _apart(o, "o", spans + [("S0", _span(S0))])
+        _apart(o, "o", spans + [("S0", S0)])
     if S_T is not None:
         _check(S_T, "S_T", p.state_shape, F32, dev)
         same = S0 is not None and S_T.data_ptr() == S0.data_ptr()
-        _apart(S_T, "S_T", spans + [("o", _span(o))] + ([] if same else [("S0", _span(S0))]))
+        _apart(S_T, "S_T", spans + [("o", o)] + ([] if same else [("S0", S0)]))
     elif want_state:
         S_T = torch.empty(p.state_shape, device=dev, dtype=F32)
     workspace, wbytes = _workspace("ckda_gated_fwd_workspace_bytes", dev, p.ws_sizes, workspace)
@@ -263,9 +276,9 @@ def gated_bwd(q, k, v, g, beta, grad_o, S0=None, grad_S_T=None, *, cu_seqlens=No
             _check(got[name], name, shape, dtype, dev)
             given.append(name)
     for i, name in enumerate(given):
-        others = p.spans + [("grad_o", _span(grad_o)), ("S0", _span(S0))] + [(n, _span(got[n])) for n in given[:i]]
+        others = p.spans + [("grad_o", grad_o), ("S0", S0)] + [(n, got[n]) for n in given[:i]]
         if not (name == "dS0" and grad_S_T is not None and got[name].data_ptr() == grad_S_T.data_ptr()):
-            others.append(("grad_S_T", _span(grad_S_T)))
+            others.append(("grad_S_T", grad_S_T))
         _apart(got[name], name, others)
     workspace, wbytes = _workspace("ckda_gated_bwd_workspace_bytes", dev, p.ws_sizes, workspace)
     _launch(dev, stream, load().ckda_gated_bwd, "ckda_gated_bwd",
@@ -301,13 +314,13 @@ def gated_decode_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None) -
         _indexes(slots, "slots", N, dev)
     elif pool < N:
         raise ValueError(f"S holds {pool} states, the call has {N} rows")
-    spans = [("q", _span(q)), ("k", _span(k)), ("v", _span(v)), ("g", _span(g)), ("beta", _span(beta)), ("slots", _span(slots))]
+    spans = [("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("slots", slots)]
     _apart(S, "S", spans)
     if o is None:
         o = torch.empty((N, Hv, dv), device=dev, dtype=dt)
     else:
         _check(o, "o", (N, Hv, dv), dt, dev)
-        _apart(o, "o", spans + [("S", _span(S))])
+        _apart(o, "o", spans + [("S", S)])
     _launch(dev, stream, load().ckda_gated_decode_step, "ckda_gated_decode_step",
             (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S), _ptr(o), _ptr(slots), N, pool, Hk, Hv, dk, dv, qs, ks,
              vs, _dt(q)))
@@ -357,8 +370,8 @@ class _Prep:
                 raise TypeError("positions must be an int32 or int64 tensor")
             _check(positions, "positions", self.tokens_shape, positions.dtype, dev)
             pos64 = int(positions.dtype == torch.int64)
-        self.spans = [("q", _span(q)), ("k", _span(k)), ("q_weight", _span(q_weight)), ("k_weight", _span(k_weight)),
-                      ("positions", _span(positions)), ("inv_freq", _span(inv_freq))]
+        self.spans = [("q", q), ("k", k), ("q_weight", q_weight), ("k_weight", k_weight),
+                      ("positions", positions), ("inv_freq", inv_freq)]
         self.ptrs = (_ptr(q_weight), _ptr(k_weight), _ptr(positions), pos64, _ptr(inv_freq))
         self.sizes = (tokens, max(1, self.tokens_shape[-1]), self.Hq, self.Hk, self.d, rotary, self.qs, self.ks, self.dt,
                       NORMS[norm], LAYOUTS[layout], float(eps), float(q_scale), float(rope_scale))
@@ -390,7 +403,7 @@ def qk_norm_rope(q, k=None, *, positions=None, inv_freq=None, norm="l2", layout=
     if k is None:
         k_out = None
     else:
-        k_out = p.out(k_out, "k_out", p.Hk, k.dtype, others(k_out, k, "k") + [("q_out", _span(q_out))])
+        k_out = p.out(k_out, "k_out", p.Hk, k.dtype, others(k_out, k, "k") + [("q_out", q_out)])
     _launch(p.dev, stream, load().ckda_qk_prep, "ckda_qk_prep",
             (_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), *p.ptrs, *p.sizes))
     return q_out, k_out
@@ -408,11 +421,11 @@ def qk_norm_rope_bwd(q, k, grad_q, grad_k=None, *, positions=None, inv_freq=None
     if k is not None:
         _check(grad_k, "grad_k", p.tokens_shape + (p.Hk, p.d), q.dtype, p.dev)
     got = dict(grads or {})
-    spans = p.spans + [("grad_q", _span(grad_q)), ("grad_k", _span(grad_k))]
+    spans = p.spans + [("grad_q", grad_q), ("grad_k", grad_k)]
     got["dq"] = p.out(got.get("dq"), "dq", p.Hq, q.dtype, spans)
-    spans.append(("dq", _span(got["dq"])))
+    spans.append(("dq", got["dq"]))
     got["dk"] = p.out(got.get("dk"), "dk", p.Hk, k.dtype, spans) if k is not None else None
-    spans.append(("dk", _span(got["dk"])))
+    spans.append(("dk", got["dk"]))
     weights = False
     for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
         if w is None:
@@ -424,7 +437,7 @@ def qk_norm_rope_bwd(q, k, grad_q, grad_k=None, *, positions=None, inv_freq=None
         else:
             _check(got[name], name, (p.d,), F32, p.dev)
             _apart(got[name], name, spans)
-        spans.append((name, _span(got[name])))
+        spans.append((name, got[name]))
     wbytes = 0
     if weights or workspace is not None:
         workspace, wbytes = _workspace("ckda_qk_prep_bwd_workspace_bytes", p.dev, (p.d,), workspace)
@@ -483,7 +496,7 @@ def state_copy(S, src, dst, *, pool_dim=0, stream=None) -> torch.Tensor:
     _check(S, "S", S.shape, F32, dev)
     _indexes(src, "src", None, dev)
     _indexes(dst, "dst", src.shape[0], dev)
-    _apart(S, "S", [("src", _span(src)), ("dst", _span(dst))])
+    _apart(S, "S", [("src", src), ("dst", dst)])
     layers, slots = S.shape[0] if pool_dim else 1, S.shape[pool_dim]
     if slots == 0:
         raise ValueError("S holds no states")
