@@ -162,12 +162,14 @@ ckda_status_t simt_bwd(const Shape& s, const void* q, const void* k, const void*
 
 // ---------------------------------------------------------------- the chunked kernels
 
-// They take bf16 with heads of a multiple of 8 channels (16-byte rows); channels are padded to
-// 64 or 128 in shared memory.
+// They take bf16 with heads of a multiple of 8 channels, whose rows have to start on 16 bytes;
+// channels are padded to 64 or 128 in shared memory.
 bool chunked(const Shape& s) { return s.dt == CKDA_BF16 && s.dk % 8 == 0 && s.dv % 8 == 0; }
-bool chunked(const Shape& s, long long qs, long long ks, long long vs) {
-    return chunked(s) && qs % 8 == 0 && ks % 8 == 0 && vs % 8 == 0;
+bool rows_aligned(const Shape& s, long long qs, long long ks, long long vs) {
+    return !chunked(s) || (qs % 8 == 0 && ks % 8 == 0 && vs % 8 == 0);
 }
+// Whether grids and row numbers of the chunked kernels hold the call.
+bool chunked_fits(const Shape& s) { return s.Hk <= 65535 && (long long)Seqs::slots(s.N, s.total) * s.Hv * C <= 0x7fffffffLL; }
 
 // Chunks in a segment (0: whole sequences run), for a call's sizes alone. Time is counted in chunks
 // one after the other: whole sequences take the average sequence's (its longest is not known on the
@@ -314,7 +316,6 @@ cudaError_t run_grads(const Call& c, const Maps& m, const ChainIn& in) {
     cudaError_t e = kernel_ready(grad_kernel<DK, DV>, smem);
     if (e != cudaSuccess) return e;
     const long long slots = (long long)Seqs::slots(c.s.N, c.s.total), items = slots * c.s.Hk;
-    if (slots * c.s.Hv * C > 0x7fffffffLL) return cudaErrorInvalidValue;      // row numbers of the updates
     CUtensorMap gv{}, u{};
     if (in.maps && !(rows_map(&gv, c.gv, c.s.total, c.s.Hv, c.s.dv, (long long)c.s.Hv * c.s.dv) &&
                      rows_map(&u, c.ws.u, slots * c.s.Hv * C, 1, c.s.dv, c.s.dv)))
@@ -381,6 +382,8 @@ ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const 
     if (c != CKDA_OK) return c;
     if (total > 0 && (!q || !k || !v || !g || !beta || !o)) return CKDA_ERR_INVALID_ARG;
     if (!strides_ok(s, q_stride, k_stride, v_stride)) return CKDA_ERR_INVALID_ARG;
+    if (!rows_aligned(s, q_stride, k_stride, v_stride)) return CKDA_ERR_MISALIGNED;
+    if (chunked(s) && !chunked_fits(s)) return CKDA_ERR_UNSUPPORTED;
     const void* ptrs[] = {q, k, v, S0, o, S_T, workspace};
     for (const void* p : ptrs)
         if (p && !aligned16(p)) return CKDA_ERR_MISALIGNED;
@@ -391,7 +394,7 @@ ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const 
     if (N == 0) return CKDA_OK;
     if (total == 0) return clear_or_copy(S0, S_T, (size_t)N * Hv * dk * dv, st);
     const Seqs seqs{cu_seqlens, N, T, total};
-    if (chunked(s, q_stride, k_stride, v_stride)) {
+    if (chunked(s)) {
         Call a{};
         a.s = s;
         a.seqs = seqs;
@@ -414,8 +417,7 @@ ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const 
 size_t ckda_gated_bwd_workspace_bytes(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt) {
     const Shape s{N, 0, total, Hk, Hv, dk, dv, dt};
     if (check_shape(s, true) != CKDA_OK || N == 0 || total == 0) return 0;
-    // rows whose stride the chunked kernels cannot read go to the CUDA cores: room for either
-    return chunked(s) ? std::max(chunk_layout(s, true).total, simt_bwd_layout(s).total) : simt_bwd_layout(s).total;
+    return chunked(s) ? chunk_layout(s, true).total : simt_bwd_layout(s).total;
 }
 
 ckda_status_t ckda_gated_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -429,6 +431,8 @@ ckda_status_t ckda_gated_bwd(const void* q, const void* k, const void* v, const 
     if (total > 0 && (!q || !k || !v || !g || !beta || !grad_o || !grad_q || !grad_k || !grad_v || !grad_g || !grad_beta))
         return CKDA_ERR_INVALID_ARG;
     if (!strides_ok(s, q_stride, k_stride, v_stride)) return CKDA_ERR_INVALID_ARG;
+    if (!rows_aligned(s, q_stride, k_stride, v_stride)) return CKDA_ERR_MISALIGNED;
+    if (chunked(s) && !chunked_fits(s)) return CKDA_ERR_UNSUPPORTED;
     const void* ptrs[] = {q, k, v, S0, grad_o, grad_S_T, grad_q, grad_k, grad_v, grad_S0, workspace};
     for (const void* p : ptrs)
         if (p && !aligned16(p)) return CKDA_ERR_MISALIGNED;
@@ -442,7 +446,7 @@ ckda_status_t ckda_gated_bwd(const void* q, const void* k, const void* v, const 
     if (total == 0) return clear_or_copy(grad_S_T, grad_S0, (size_t)N * Hv * dk * dv, st);
     const Seqs seqs{cu_seqlens, N, T, total};
     char* ws = static_cast<char*>(workspace);
-    if (chunked(s, q_stride, k_stride, v_stride)) {
+    if (chunked(s)) {
         Call a{};
         a.s = s;
         a.seqs = seqs;
@@ -519,7 +523,7 @@ namespace {
 
 // Blocks of the backward pass, which each leave a partial sum of the weights' gradients: fixed by
 // the sizes alone, so those sums have one order.
-constexpr int kPrepMaxBlocks = 148 * 3;
+constexpr int kPrepMaxBlocks = 148 * 2;
 int prep_blocks(long long units) { return (int)std::max(1LL, std::min(units, (long long)kPrepMaxBlocks)); }
 
 ckda_status_t prep_args(PrepArgs& a, const void* q, const void* k, const float* qw, const float* kw, const void* pos,
@@ -565,7 +569,7 @@ bool prep_vector(const PrepArgs& a, ckda_dtype_t dt) {
 
 template <typename TIn, bool kBack>
 ckda_status_t prep_launch(const PrepArgs& a, ckda_dtype_t dt, int* blocks_out, cudaStream_t st) {
-    constexpr int UR = kBack ? 2 : 4;
+    constexpr int UR = 4;
     if (prep_vector(a, dt)) {
         const int G = a.d <= 64 ? 8 : (a.d <= 128 ? 16 : 32), gp = 32 / G;
         // Warps to a token: one, more while tokens are too few to give every SM two blocks and the

@@ -189,15 +189,6 @@ __device__ __forceinline__ void chain_load(uint32_t st, uint64_t* full, int x, c
     tc::mbar_arrive(full);
 }
 
-// 32 consecutive floats of shared memory that every thread reads alike.
-__device__ __forceinline__ void read32(float (&x)[32], const float* p) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float4 y = *reinterpret_cast<const float4*>(p + 4 * i);
-        x[4 * i] = y.x; x[4 * i + 1] = y.y; x[4 * i + 2] = y.z; x[4 * i + 3] = y.w;
-    }
-}
-
 // The out warps' [64][128] tile of bf16 rows in shared memory to global rows, 16 bytes a lane.
 __device__ __forceinline__ void rows_out(const unsigned char* tile, int x, __nv_bfloat16* dst, long long stride, int rows, int cols) {
 #pragma unroll

@@ -10,7 +10,6 @@ namespace ckda {
 namespace gated {
 
 constexpr int LD64 = 144;                      // bytes of a padded row of 64 bf16 (9 x 16: conflict-free ldmatrix)
-__host__ __device__ constexpr int ld_bytes(int cols) { return cols * 2 + 16; }
 
 __device__ __forceinline__ uint32_t s32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 

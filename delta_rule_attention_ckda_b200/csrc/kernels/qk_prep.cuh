@@ -147,7 +147,7 @@ __device__ __forceinline__ float group_sum(float x) {
 // Vector path: d a multiple of 8, rows 16-byte aligned, R a multiple of 16 (half) or 8 (interleaved).
 // `wpt` warps share a token's heads.
 template <typename TIn, int G, int UR, bool kBack>
-__global__ void __launch_bounds__(256, 3)
+__global__ void __launch_bounds__(256, kBack ? 2 : 3)
 prep_vec_kernel(const PrepArgs a, int wpt) {
     extern __shared__ __align__(16) float smf[];
     constexpr int GP = 32 / G;                                  // rows a warp takes at once

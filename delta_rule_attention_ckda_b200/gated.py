@@ -13,7 +13,9 @@ The rule, per sequence and value head, with one decay e^{g_t} per token:
 q and k have Hk heads, v, g, beta and the states Hv, a multiple of Hk. Dense tensors are
 [B, T, heads, d]; with cu_seqlens (int32 [N+1], device) they are packed, [total, heads, d].
 q, k and v may be slices of wider rows (heads and channels contiguous, one distance from token
-to token). The full conventions are in include/ckda.h.
+to token); for the tensor cores, which take bf16 heads of a multiple of 8 channels, they start
+on 16 bytes and that distance is a multiple of 8 elements. The full conventions are in
+include/ckda.h.
 """
 from __future__ import annotations
 
@@ -155,16 +157,27 @@ def _bytes(which: str, device_index: int, sizes) -> int:
         return int(getattr(load(), which)(*sizes))
 
 
-def _workspace(which: str, dev, sizes, workspace):
+def _empty(shape, dev, dtype, stream):
+    """New memory for a call on `stream`: of that stream, so that torch hands it out again only behind
+    the call, whatever the current stream is."""
+    if stream is None:
+        return torch.empty(shape, device=dev, dtype=dtype)
+    if stream.device != dev:
+        raise ValueError(f"stream is on {stream.device}, the call's tensors are on {dev}")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, device=dev, dtype=dtype)
+
+
+def _workspace(which: str, dev, sizes, workspace, stream, used):
     need = _bytes(which, dev.index, sizes)
     if workspace is None:
         if need == 0:
             return None, 0
-        workspace = torch.empty(need, device=dev, dtype=torch.uint8)
-        return workspace, need
+        return _empty(need, dev, torch.uint8, stream), need
     _on(workspace, "workspace", dev)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
+    _apart(workspace, "workspace", used)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -232,7 +245,7 @@ def gated_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, o=None, S_T=N
     dev = p.dev
     spans = p.spans
     if o is None:
-        o = torch.empty(p.o_shape, device=dev, dtype=v.dtype)
+        o = _empty(p.o_shape, dev, v.dtype, stream)
     else:
         _check(o, "o", p.o_shape, v.dtype, dev)
         _apart(o, "o", spans + [("S0", S0)])
@@ -241,8 +254,9 @@ def gated_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, o=None, S_T=N
         same = S0 is not None and S_T.data_ptr() == S0.data_ptr()
         _apart(S_T, "S_T", spans + [("o", o)] + ([] if same else [("S0", S0)]))
     elif want_state:
-        S_T = torch.empty(p.state_shape, device=dev, dtype=F32)
-    workspace, wbytes = _workspace("ckda_gated_fwd_workspace_bytes", dev, p.ws_sizes, workspace)
+        S_T = _empty(p.state_shape, dev, F32, stream)
+    workspace, wbytes = _workspace("ckda_gated_fwd_workspace_bytes", dev, p.ws_sizes, workspace, stream,
+                                   spans + [("S0", S0), ("o", o), ("S_T", S_T)])
     _launch(dev, stream, load().ckda_gated_fwd, "ckda_gated_fwd",
             (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(o), _ptr(S_T), _ptr(cu_seqlens), *p.sizes,
              _ptr(workspace), wbytes))
@@ -271,7 +285,7 @@ def gated_bwd(q, k, v, g, beta, grad_o, S0=None, grad_S_T=None, *, cu_seqlens=No
         if name == "dS0" and not want_dS0:
             got[name] = None
         elif got.get(name) is None:
-            got[name] = torch.empty(shape, device=dev, dtype=dtype)
+            got[name] = _empty(shape, dev, dtype, stream)
         else:
             _check(got[name], name, shape, dtype, dev)
             given.append(name)
@@ -280,7 +294,8 @@ def gated_bwd(q, k, v, g, beta, grad_o, S0=None, grad_S_T=None, *, cu_seqlens=No
         if not (name == "dS0" and grad_S_T is not None and got[name].data_ptr() == grad_S_T.data_ptr()):
             others.append(("grad_S_T", grad_S_T))
         _apart(got[name], name, others)
-    workspace, wbytes = _workspace("ckda_gated_bwd_workspace_bytes", dev, p.ws_sizes, workspace)
+    workspace, wbytes = _workspace("ckda_gated_bwd_workspace_bytes", dev, p.ws_sizes, workspace, stream,
+                                   p.spans + [("S0", S0), ("grad_o", grad_o), ("grad_S_T", grad_S_T), *got.items()])
     _launch(dev, stream, load().ckda_gated_bwd, "ckda_gated_bwd",
             (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(grad_o), _ptr(grad_S_T), _ptr(got["dq"]),
              _ptr(got["dk"]), _ptr(got["dv"]), _ptr(got["dg"]), _ptr(got["dbeta"]), _ptr(got["dS0"]), _ptr(cu_seqlens),
@@ -317,7 +332,7 @@ def gated_decode_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None) -
     spans = [("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("slots", slots)]
     _apart(S, "S", spans)
     if o is None:
-        o = torch.empty((N, Hv, dv), device=dev, dtype=dt)
+        o = _empty((N, Hv, dv), dev, dt, stream)
     else:
         _check(o, "o", (N, Hv, dv), dt, dev)
         _apart(o, "o", spans + [("S", S)])
@@ -376,11 +391,11 @@ class _Prep:
         self.sizes = (tokens, max(1, self.tokens_shape[-1]), self.Hq, self.Hk, self.d, rotary, self.qs, self.ks, self.dt,
                       NORMS[norm], LAYOUTS[layout], float(eps), float(q_scale), float(rope_scale))
 
-    def out(self, t, name, heads, dtype, others):
+    def out(self, t, name, heads, dtype, others, stream):
         """An output of `heads` heads, allocated or checked."""
         shape = self.tokens_shape + (heads, self.d)
         if t is None:
-            return torch.empty(shape, device=self.dev, dtype=dtype)
+            return _empty(shape, self.dev, dtype, stream)
         _check(t, name, shape, dtype, self.dev)
         _apart(t, name, others)
         return t
@@ -399,11 +414,11 @@ def qk_norm_rope(q, k=None, *, positions=None, inv_freq=None, norm="l2", layout=
         same = t is not None and src.is_contiguous() and t.data_ptr() == src.data_ptr()
         return [x for x in p.spans if not (same and x[0] == own)]
 
-    q_out = p.out(q_out, "q_out", p.Hq, q.dtype, others(q_out, q, "q"))
+    q_out = p.out(q_out, "q_out", p.Hq, q.dtype, others(q_out, q, "q"), stream)
     if k is None:
         k_out = None
     else:
-        k_out = p.out(k_out, "k_out", p.Hk, k.dtype, others(k_out, k, "k") + [("q_out", q_out)])
+        k_out = p.out(k_out, "k_out", p.Hk, k.dtype, others(k_out, k, "k") + [("q_out", q_out)], stream)
     _launch(p.dev, stream, load().ckda_qk_prep, "ckda_qk_prep",
             (_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), *p.ptrs, *p.sizes))
     return q_out, k_out
@@ -422,9 +437,9 @@ def qk_norm_rope_bwd(q, k, grad_q, grad_k=None, *, positions=None, inv_freq=None
         _check(grad_k, "grad_k", p.tokens_shape + (p.Hk, p.d), q.dtype, p.dev)
     got = dict(grads or {})
     spans = p.spans + [("grad_q", grad_q), ("grad_k", grad_k)]
-    got["dq"] = p.out(got.get("dq"), "dq", p.Hq, q.dtype, spans)
+    got["dq"] = p.out(got.get("dq"), "dq", p.Hq, q.dtype, spans, stream)
     spans.append(("dq", got["dq"]))
-    got["dk"] = p.out(got.get("dk"), "dk", p.Hk, k.dtype, spans) if k is not None else None
+    got["dk"] = p.out(got.get("dk"), "dk", p.Hk, k.dtype, spans, stream) if k is not None else None
     spans.append(("dk", got["dk"]))
     weights = False
     for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
@@ -433,14 +448,14 @@ def qk_norm_rope_bwd(q, k, grad_q, grad_k=None, *, positions=None, inv_freq=None
             continue
         weights = True
         if got.get(name) is None:
-            got[name] = torch.empty(p.d, device=p.dev, dtype=F32)
+            got[name] = _empty(p.d, p.dev, F32, stream)
         else:
             _check(got[name], name, (p.d,), F32, p.dev)
             _apart(got[name], name, spans)
         spans.append((name, got[name]))
     wbytes = 0
     if weights or workspace is not None:
-        workspace, wbytes = _workspace("ckda_qk_prep_bwd_workspace_bytes", p.dev, (p.d,), workspace)
+        workspace, wbytes = _workspace("ckda_qk_prep_bwd_workspace_bytes", p.dev, (p.d,), workspace, stream, spans)
     _launch(p.dev, stream, load().ckda_qk_prep_bwd, "ckda_qk_prep_bwd",
             (_ptr(q), _ptr(k), _ptr(grad_q), _ptr(grad_k), _ptr(got["dq"]), _ptr(got["dk"]), _ptr(got["dq_weight"]),
              _ptr(got["dk_weight"]), *p.ptrs, *p.sizes, _ptr(workspace), wbytes))

@@ -362,8 +362,9 @@ CKDA_API ckda_status_t ckda_decode_step_ex(const void* q, const void* k, const v
  *   cu_seqlens[n] .. cu_seqlens[n+1] - 1 (int32 [N+1], device memory; T is ignored), empty
  *   sequences allowed; rows outside every sequence are neither read nor written.
  * - q, k and v may be slices of wider rows: *_stride is the distance from token to token in
- *   elements (at least heads * channels); heads and channels are contiguous. Every other
- *   tensor is contiguous.
+ *   elements (at least heads * channels); heads and channels are contiguous. With bf16 heads of
+ *   a multiple of 8 channels, which the tensor cores take, the strides of the gated delta rule
+ *   are multiples of 8 (CKDA_ERR_MISALIGNED). Every other tensor is contiguous.
  * - o, and every gradient, has the type of its tensor: bf16 with bf16 q, k, v; g, beta, the
  *   states and their gradients are fp32.
  * - g, beta, their gradients, positions, inv_freq and the indexes in device memory

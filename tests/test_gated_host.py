@@ -34,6 +34,7 @@ def test_forward_rejects(lib):
         assert fwd(lib, **bad) == 1, bad
     for bad in (dict(q=ODD16), dict(S0=ODD16), dict(ST=ODD16), dict(g=ODD4), dict(beta=ODD4), dict(cu=ODD4), dict(ws=ODD16)):
         assert fwd(lib, **bad) == 3, bad
+    assert fwd(lib, qs=20) == 3 and fwd(lib, vs=17) == 3                  # bf16 rows off 16 bytes
     assert fwd(lib, ws=None, wb=0) == 6
     assert fwd(lib, N=1 << 20, T=1 << 12, total=0x7fffffff) in (1, 2)
     assert fwd(lib, N=0, total=0) == 0                                    # nothing to do

@@ -453,6 +453,46 @@ def test_graph_streams_and_two_calls(ck):
             assert torch.equal(gr[n], g0[n]), n
 
 
+def test_other_sequences_values_stay_out(ck):
+    """NaN and infinities in one sequence of a packed batch, and behind the last, change nothing in
+    the others: chunks that end inside take no rows of the sequence that follows."""
+    lens = [70, 33, 128, 65]
+    cu, total = packed(lens, 9)
+    x = dev(*make((total,), 1, 2, 128, 128, BF, 3, len(lens)))
+    q, k, v, g, b, S0, do, dST = x
+    clean = (ck.gated_chunk_fwd(*x[:6], cu_seqlens=cu.cuda()), ck.gated_bwd(q, k, v, g, b, do, S0, dST, cu_seqlens=cu.cuda()))
+    for t in (q, k, v, do):
+        t[70:103] = float("nan")
+        t[296:] = float("inf")
+    g[70:103], b[70:103], g[296:] = float("nan"), float("inf"), float("nan")
+    (o, ST), got = (ck.gated_chunk_fwd(*x[:6], cu_seqlens=cu.cuda()), ck.gated_bwd(q, k, v, g, b, do, S0, dST, cu_seqlens=cu.cuda()))
+    fine(ck)
+    keep = torch.cat([torch.arange(70), torch.arange(103, 296)]).cuda()
+    seqs = torch.tensor([0, 2, 3]).cuda()
+    assert torch.equal(o[keep], clean[0][0][keep]) and torch.equal(ST[seqs], clean[0][1][seqs])
+    assert torch.isnan(o[70:103].float()).any()
+    for n in ("dq", "dk", "dv", "dg", "dbeta"):
+        assert torch.equal(got[n][keep], clean[1][n][keep]), n
+    assert torch.equal(got["dS0"][seqs], clean[1]["dS0"][seqs])
+
+
+def test_stream_of_its_own(ck):
+    """Calls on a stream that is not the current one allocate for that stream: memory that the current
+    stream frees and takes again meanwhile is not theirs."""
+    x = dev(*make((4, 640), 2, 2, 128, 128, BF, 6, 4))
+    want = ck.gated_bwd(*x[:5], x[6], x[5], x[7])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = ck.gated_bwd(*x[:5], x[6], x[5], x[7], stream=side)
+    scratch = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(32)]
+    side.synchronize()
+    fine(ck)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    del scratch
+
+
 def test_same_result_every_run(ck):
     cu, total = packed([700, 3, 260], 0)
     q, k, v, g, b, S0, do, dST = dev(*make((total,), 1, 4, 128, 128, BF, 6, 3))
