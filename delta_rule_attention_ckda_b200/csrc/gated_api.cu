@@ -569,7 +569,7 @@ bool prep_vector(const PrepArgs& a, ckda_dtype_t dt) {
 
 template <typename TIn, bool kBack>
 ckda_status_t prep_launch(const PrepArgs& a, ckda_dtype_t dt, int* blocks_out, cudaStream_t st) {
-    constexpr int UR = 4;
+    constexpr int UR = kBack ? 2 : 4;
     if (prep_vector(a, dt)) {
         const int G = a.d <= 64 ? 8 : (a.d <= 128 ? 16 : 32), gp = 32 / G;
         // Warps to a token: one, more while tokens are too few to give every SM two blocks and the
@@ -577,7 +577,7 @@ ckda_status_t prep_launch(const PrepArgs& a, ckda_dtype_t dt, int* blocks_out, c
         int wpt = 1;
         while (wpt < 8 && (long long)a.tokens * wpt < 16LL * sm_count() && wpt * gp < a.heads[0] + a.heads[1]) wpt *= 2;
         const long long units = ((long long)a.tokens * wpt + 7) / 8;
-        const int blocks = kBack ? prep_blocks(units) : (int)units;
+        const int blocks = kBack ? prep_blocks(units) : (int)std::min<long long>(units, (long long)sm_count() * 3);
         size_t smem = (size_t)8 * a.rotary * sizeof(float);
         if (kBack) smem = std::max(smem, (size_t)8 * gp * a.d * sizeof(float));
         *blocks_out = blocks;

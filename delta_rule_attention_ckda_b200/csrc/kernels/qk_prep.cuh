@@ -14,7 +14,11 @@
 // a million turns an fp32 angle by 0.06 rad), once per token and pair.
 //
 // Vector path: a warp takes a token (several warps where tokens are few), G lanes a head row, 16
-// bytes each, UR rows in flight. What a lane does to a channel is the same for every head of
+// bytes each, UR rows in work and UR more on their way. Blocks stay for all their tokens, so
+// loads also run under the next token's angles. 32768 tokens of 16 + 16 heads of 128: 107 us,
+// 77% of the measured copy bandwidth (without the rows on their way 8% slower; 4 blocks an SM
+// instead of 3 spill, 18% slower). Backward, 16383 tokens of 16 + 8 heads: 77 us and 4 for the
+// weights' sums, 57%: 8 loads of 16 bytes a lane in flight fill the registers. What a lane does to a channel is the same for every head of
 // the token, out = r (x A + x' B) with x' the pair's other channel (from a lane R/16 away, or the
 // neighbour in the same register), so weight, cosine, sine and scale are folded into A and B once
 // per token. Warps share nothing and meet at no barrier. Rows of other sizes or alignments take
@@ -162,22 +166,42 @@ prep_vec_kernel(const PrepArgs a, int wpt) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[0][i] = acc[1][i] = 0.f;
     }
-    const int per = 8 / wpt;                                    // tokens a block takes at once
-    for (int t = blockIdx.x * per + warp / wpt; t < a.tokens; t += gridDim.x * per) {
+    const int per = 8 / wpt, step = wpt * GP * UR, h0 = (warp % wpt) * GP;      // tokens a block takes at once; heads a warp does
+    // Rows on their way: batches of UR rows a lane group, over heads, then keys, then the next token.
+    struct Batch {
+        Raw8<TIn> x[UR], d[kBack ? UR : 1];
+    };
+    auto fetch = [&](Batch& b, long long t, int which, int hb) {
+        const TIn* xp = static_cast<const TIn*>(a.x[which]) + t * a.stride[which] + e0;
+        const TIn* dp = kBack ? static_cast<const TIn*>(a.dy[which]) + t * a.heads[which] * a.d + e0 : nullptr;
+#pragma unroll
+        for (int j = 0; j < UR; ++j) {
+            const int h = hb + j * wpt * GP + lane / G;
+            const bool on = live && t < a.tokens && h < a.heads[which];
+            b.x[j].zero();
+            if (on) b.x[j].load(xp + (long long)h * a.d);
+            if constexpr (kBack) {
+                b.d[j].zero();
+                if (on) b.d[j].load(dp + (long long)h * a.d);
+            }
+        }
+    };
+    Batch now, next;
+    const long long t0 = (long long)blockIdx.x * per + warp / wpt, hop = (long long)gridDim.x * per;
+    const int q0 = h0 < a.heads[0] ? 0 : 1;
+    fetch(now, t0, q0, h0);
+    for (long long t = t0; t < a.tokens; t += hop) {
         if (half) {
             __syncwarp();
-            for (int p = lane; p < half; p += 32) cs[p] = turn(a, t, p);
+            for (int p = lane; p < half; p += 32) cs[p] = turn(a, (int)t, p);
             __syncwarp();
         }
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-            if (a.heads[which] == 0) continue;
+            if (h0 >= a.heads[which]) continue;
             const float scale = which ? 1.f : a.q_scale;
             const float* w = a.w[which];
-            const TIn* xp = static_cast<const TIn*>(a.x[which]) + t * a.stride[which] + e0;
-            const long long row0 = (long long)t * a.heads[which] * a.d + e0;
-            const TIn* dp = kBack ? static_cast<const TIn*>(a.dy[which]) + row0 : nullptr;
-            TIn* op = static_cast<TIn*>(a.out[which]) + row0;
+            TIn* op = static_cast<TIn*>(a.out[which]) + t * a.heads[which] * a.d + e0;
             // forward: A, B with the weights of the channel and of its partner; backward: of dy, without
             float A[8], B[8], wt[8];
 #pragma unroll
@@ -195,31 +219,23 @@ prep_vec_kernel(const PrepArgs a, int wpt) {
                     B[i] = wo * scale * (plus != kBack ? c.y : -c.y);
                 }
             }
-            for (int hb = (warp % wpt) * GP; hb < a.heads[which]; hb += wpt * GP * UR) {
-                Raw8<TIn> rx[UR], rd[kBack ? UR : 1];
-#pragma unroll
-                for (int j = 0; j < UR; ++j) {                  // all loads in flight
-                    const int h = hb + j * wpt * GP + lane / G;
-                    const bool on = live && h < a.heads[which];
-                    rx[j].zero();
-                    if (on) rx[j].load(xp + (long long)h * a.d);
-                    if constexpr (kBack) {
-                        rd[j].zero();
-                        if (on) rd[j].load(dp + (long long)h * a.d);
-                    }
-                }
+#pragma unroll 1
+            for (int hb = h0; hb < a.heads[which]; hb += step) {
+                if (hb + step < a.heads[which]) fetch(next, t, which, hb + step);
+                else if (which == 0 && h0 < a.heads[1]) fetch(next, t, 1, h0);
+                else fetch(next, t + hop, q0, h0);
 #pragma unroll
                 for (int j = 0; j < UR; ++j) {
                     if (hb + j * wpt * GP >= a.heads[which]) break;                  // the warp's rows are done
                     const int h = hb + j * wpt * GP + lane / G;
                     float x[8], y[8];
-                    rx[j].unpack(x);
+                    now.x[j].unpack(x);
                     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) fma2(s0, s1, x[i], x[i + 1], x[i], x[i + 1]);
                     float coef;
                     const float f = norm_factor(a, group_sum<G>(s0 + s1), coef);
-                    const Raw8<TIn>& turned = kBack ? rd[kBack ? j : 0] : rx[j];
+                    const Raw8<TIn>& turned = kBack ? now.d[kBack ? j : 0] : now.x[j];
                     (a.interleaved ? turned.swapped() : turned.from_lane(other, in)).unpack(y);
                     if (a.interleaved && !in) {
 #pragma unroll
@@ -234,7 +250,7 @@ prep_vec_kernel(const PrepArgs a, int wpt) {
                         }
                     } else {
                         float z[8], d0 = 0.f, d1 = 0.f;
-                        rd[j].unpack(z);
+                        now.d[j].unpack(z);
 #pragma unroll
                         for (int i = 0; i < 8; i += 2) {
                             mul2(z[i], z[i + 1], A[i], A[i + 1]);
@@ -255,6 +271,7 @@ prep_vec_kernel(const PrepArgs a, int wpt) {
                     }
                     if (live && h < a.heads[which]) Raw8<TIn>::store(op + (long long)h * a.d, x);
                 }
+                now = next;
             }
         }
     }
@@ -298,14 +315,14 @@ prep_row_kernel(const PrepArgs a) {
         const float y = buf[warp][o], s = sign * cs[p].y;
         return first ? x * cs[p].x - y * s : x * cs[p].x + y * s;
     };
-    for (int t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+    for (long long t = blockIdx.x; t < a.tokens; t += gridDim.x) {
         __syncthreads();
-        for (int p = threadIdx.x; p < half; p += 256) cs[p] = turn(a, t, p);
+        for (int p = threadIdx.x; p < half; p += 256) cs[p] = turn(a, (int)t, p);
         __syncthreads();
         for (int h = warp; h < H; h += 8) {
             const int which = h >= a.heads[0], hh = which ? h - a.heads[0] : h;
             const TIn* xp = static_cast<const TIn*>(a.x[which]) + t * a.stride[which] + (long long)hh * a.d;
-            const long long row = ((long long)t * a.heads[which] + hh) * a.d;
+            const long long row = (t * a.heads[which] + hh) * a.d;
             const float* w = a.w[which];
             const float scale = which ? 1.f : a.q_scale;
             float x[8], z[8], ss = 0.f, coef;

@@ -272,6 +272,7 @@ PREP = [  # tokens, Hq, Hk, d, rotary, norm, layout, weights, dtype
     (20, 4, 2, 96, 24, "rms", "half", True, BF), (21, 4, 2, 96, 24, "none", "interleaved", False, BF),
     (5, 2, 2, 37, 10, "l2", "half", True, F32), (9, 1, 1, 1, 0, "rms", "half", True, F32),
     (40, 2, 2, 64, 0, "l2", "half", False, F32), (300, 8, 2, 128, 128, "none", "half", True, BF),
+    (4001, 3, 2, 64, 32, "l2", "half", True, BF), (9000, 1, 3, 128, 128, "rms", "half", False, BF),
     (1000, 4, 4, 64, 16, "rms", "interleaved", True, F32), (17, 2, 0, 128, 32, "l2", "interleaved", False, BF),
 ]
 
@@ -369,6 +370,17 @@ def test_prep_strided_in_place_and_default_positions(ck):
     for x, y, z in zip(a, b, c):
         assert torch.equal(x, y) and torch.equal(x, z)
     assert torch.equal(o1, odd)
+
+
+@pytest.mark.parametrize("tokens,d", [((1 << 30) + 9, 8), ((1 << 31) - 1, 1)], ids=["rows", "scalars"])
+def test_prep_most_tokens(ck, tokens, d):
+    """Token numbers close to 2^31, offsets beyond it: rows at both ends and in between."""
+    q = torch.empty(tokens, 1, d, dtype=BF, device="cuda").normal_()
+    some = torch.tensor([0, 1, tokens // 2, (1 << 30) - 1, 1 << 30, tokens - 2, tokens - 1]).cuda()
+    out, _ = ck.qk_norm_rope(q, norm="rms")
+    fine(ck)
+    x = q[some].double().cpu()
+    prep_near("q", out[some], ref.prep(x, None, None, norm="rms", layout="half", weight=None, scale=1.0, rope_scale=1.0))
 
 
 # ------------------------------------------------------------------- copies of states
