@@ -40,7 +40,7 @@ static_assert(256 * kRegEpi + 128 * kRegOut + 128 * kRegOther <= kChainThreads *
 
 // Tensor memory columns
 constexpr uint32_t TM_ACC = 0;      // [K S | Q S]; backward: K dS | y
-constexpr uint32_t TM_S = 128;      // the state's operand (per half of the channels: hi, lo), then its update
+constexpr uint32_t TM_S = 128;      // the state's operand (per 32 channels: hi, lo), then its update
 constexpr uint32_t TM_UZ = 256;     // the products with both terms of Z; then the operands U' and U (e^G dV)
 constexpr uint32_t TM_X = 384;      // beta X (per half of the tokens: hi, lo); then U' third term
 constexpr uint32_t TM_PU = 448;     // P U; backward: P^T dO
@@ -63,7 +63,7 @@ struct ChainStage {
 static_assert(ChainStage<128, true>::SMEM <= 232448, "more shared memory than an SM has");
 
 struct ChainBars {
-    uint64_t full[2], empty[2], s, m1, x, m2, d, u, uo, m3, o, out, qs;
+    uint64_t full[2], empty[2], s[2], m1, x, m2, d, u, uo, m3, o, out, qs;
     uint32_t tmem;
     int dead;                       // a bounded wait ran out: nothing waits any more, the loops run off
 };
@@ -217,30 +217,39 @@ __device__ __forceinline__ void put_terms(const float* x, const uint32_t (&to)[T
     }
 }
 
-// Channels i .. i + 31 of a thread's half column of the state as the next product's operand; a third
-// term lies in the columns of beta X, which is written after that product.
-template <int TERMS, int H>
-__device__ __forceinline__ void put_state_terms(const float* s, uint32_t tl, int wg, int i) {
-    uint32_t to[TERMS];
-    to[0] = tl + TM_S + wg * H + i / 2;
-    to[1] = to[0] + H / 2;
-    if constexpr (TERMS == 3) to[TERMS - 1] = tl + TM_X + wg * (H / 2) + i / 2;
-    put_terms<TERMS>(s, to);
-}
-
-// s <- whole s + the H update columns at `from`, N at a time (as registers allow).
-template <int H, int N>
-__device__ __forceinline__ void add_update(float (&s)[H], float whole, uint32_t from) {
+// A thread's half column of the state: s <- whole s + the update's columns (kFirst: as it is), and, where
+// another chunk follows, s as the next product's operand. 32 channels at a time, each with a
+// barrier of its own, so that the product over the first runs while the second are split; N
+// columns at a time as registers allow. A third term lies in the columns of beta X, which is
+// written after that product.
+template <int TERMS, int H, int N>
+__device__ __forceinline__ void next_state(float (&s)[H], float whole, bool first, bool more, uint32_t tl, int wg, ChainBars& bars) {
 #pragma unroll
-    for (int k = 0; k < H; k += N) {
-        float d[N];
-        tc::tmem_ld32<N>(from + k, d);
-        tc::tmem_ld_wait();
+    for (int i = 0; i < H; i += 32) {
+        const uint32_t at = tl + TM_S + wg * H + i;
+        if (!first) {
 #pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            fma2(d[i], d[i + 1], s[k + i], s[k + i + 1], whole, whole);
-            s[k + i] = d[i];
-            s[k + i + 1] = d[i + 1];
+            for (int k = 0; k < 32; k += N) {
+                float d[N];
+                tc::tmem_ld32<N>(at + k, d);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < N; e += 2) {
+                    fma2(d[e], d[e + 1], s[i + k + e], s[i + k + e + 1], whole, whole);
+                    s[i + k + e] = d[e];
+                    s[i + k + e + 1] = d[e + 1];
+                }
+            }
+        }
+        if (more) {
+            uint32_t to[TERMS];
+            to[0] = at;
+            to[1] = at + 16;
+            if constexpr (TERMS == 3) to[TERMS - 1] = tl + TM_X + wg * (H / 2) + i / 2;
+            put_terms<TERMS>(s + i, to);
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            tc::mbar_arrive(&bars.s[i / 32]);
         }
     }
 }
@@ -293,7 +302,7 @@ __device__ __forceinline__ void chain_begin(ChainBars& b, unsigned char* stages,
             tc::mbar_init(&b.full[i], 32 * kLoadWarps + 1);
             tc::mbar_init(&b.empty[i], 1 + kEpiWarps + out_warps);
         }
-        for (uint64_t* e : {&b.s, &b.x, &b.u, &b.uo}) tc::mbar_init(e, 32 * kEpiWarps);
+        for (uint64_t* e : {&b.s[0], &b.s[1], &b.x, &b.u, &b.uo}) tc::mbar_init(e, 32 * kEpiWarps);
         for (uint64_t* e : {&b.d, &b.out, &b.qs}) tc::mbar_init(e, 32 * kOutWarps);
         for (uint64_t* e : {&b.m1, &b.m2, &b.m3, &b.o}) tc::mbar_init(e, 1);
         b.dead = 0;
@@ -396,18 +405,19 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t st = fresh(base + (c & 1) * L::BYTES), ph = c & 1;
                 if (c > 0 && !maps) chain_wait(bars, &bars.qs, (c - 1) & 1);    // Q S of the chunk before is read
-                chain_wait(bars, &bars.s, ph);
-                tc::tc_fence_after();
-                if (elected()) {
 #pragma unroll
-                    for (int term = 0; term < 2; ++term)               // [K S | Q S]
+                for (int b = 0; b < H / 32; ++b) {                     // [K S | Q S], 32 channels of either half at a time
+                    chain_wait(bars, &bars.s[b], ph);
+                    tc::tc_fence_after();
+                    if (elected()) {
 #pragma unroll
-                        for (int j = 0; j < DK / 16; ++j) {
-                            const int half = j / (H / 16), jj = j % (H / 16);
-                            tc::mma_ts(tm + TM_ACC, tm + TM_S + half * H + term * (H / 2) + jj * 8,
-                                       tc::sdesc(st + L::KQ + (j / 4) * 16384 + (j % 4) * 32, 16, 1024), i128, (term | j) != 0);
+                        for (int e = 0; e < 8; ++e) {                  // term, half, 16 channels
+                            const int term = e / 4, half = (e / 2) % 2, ch = half * H + 32 * b + 16 * (e % 2);
+                            tc::mma_ts(tm + TM_ACC, tm + TM_S + half * H + 32 * b + 16 * term + 8 * (e % 2),
+                                       tc::sdesc(st + L::KQ + (ch / 64) * 16384 + (ch % 64) * 2, 16, 1024), i128, (b | e) != 0);
                         }
-                    tc::mma_commit(&bars.m1);
+                        if (b == H / 32 - 1) tc::mma_commit(&bars.m1);
+                    }
                 }
                 if (c > 0 && !maps) output(c - 1);
                 chain_wait(bars, &bars.x, ph);
@@ -523,16 +533,11 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 const float whole = reinterpret_cast<const float*>(sm + ((c - 1) & 1) * L::BYTES + L::VECS)[VEC_EG + 63];
                 chain_wait(bars, &bars.m3, (c - 1) & 1);
                 tc::tc_fence_after();
-                add_update<H, 32>(s, whole, tl + TM_S + wg * H);
+                next_state<2, H, 32>(s, whole, false, c < chunks, tl, wg, bars);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bars.empty[(c - 1) & 1]);
-            }
-            if (c < chunks) {
-#pragma unroll
-                for (int i = 0; i < H; i += 32) put_state_terms<2, H>(s + i, tl, wg, i);
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
-                tc::mbar_arrive(&bars.s);
+            } else {
+                next_state<2, H, 32>(s, 1.f, true, c < chunks, tl, wg, bars);
             }
             if constexpr (kBack) {             // the entering (at the end: the final) state for the backward kernels
                 if (live) {
@@ -751,19 +756,20 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                             tc::mma_ss(tm + TM_PU, tc::sdesc(st + L::DO + j * 2048, 8192, 1024),
                                        tc::sdesc(st + L::P + term * 8192 + j * 2048, 8192, 1024), iE, term == 0 || j != 0);
                 }
-                chain_wait(bars, &bars.s, ph);
-                tc::tc_fence_after();
-                if (elected()) {
 #pragma unroll
-                    for (int term = 0; term < 3; ++term)               // K dS
+                for (int b = 0; b < H / 32; ++b) {                     // K dS, 32 channels of either half at a time
+                    chain_wait(bars, &bars.s[b], ph);
+                    tc::tc_fence_after();
+                    if (elected()) {
 #pragma unroll
-                        for (int j = 0; j < DK / 16; ++j) {
-                            const int half = j / (H / 16), jj = j % (H / 16);
-                            const uint32_t a = term < 2 ? TM_S + half * H + term * (H / 2) : TM_X + half * (H / 2);
-                            tc::mma_ts(tm + TM_ACC, tm + a + jj * 8, tc::sdesc(st + L::KQ + (j / 4) * 16384 + (j % 4) * 32, 16, 1024),
-                                       iK, (term | j) != 0);
+                        for (int e = 0; e < 12; ++e) {                 // term, half, 16 channels
+                            const int term = e / 4, half = (e / 2) % 2, ch = half * H + 32 * b + 16 * (e % 2);
+                            const uint32_t a = term < 2 ? TM_S + half * H + 32 * b + 16 * term : TM_X + half * (H / 2) + 16 * b;
+                            tc::mma_ts(tm + TM_ACC, tm + a + 8 * (e % 2), tc::sdesc(st + L::KQ + (ch / 64) * 16384 + (ch % 64) * 2, 16, 1024),
+                                       iK, (b | e) != 0);
                         }
-                    tc::mma_commit(&bars.m1);
+                        if (b == H / 32 - 1) tc::mma_commit(&bars.m1);
+                    }
                 }
                 if (it > 0) chain_wait(bars, &bars.out, (it - 1) & 1);   // y of the chunk before is read
                 chain_wait(bars, &bars.x, ph);
@@ -900,16 +906,11 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 const float whole = reinterpret_cast<const float*>(sm + ((it - 1) & 1) * L::BYTES + L::VECS)[VEC_EG + 63];
                 chain_wait(bars, &bars.m3, (it - 1) & 1);
                 tc::tc_fence_after();
-                add_update<H, 16>(s, whole, tl + TM_S + wg * H);
+                next_state<3, H, 16>(s, whole, false, it < chunks, tl, wg, bars);
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&bars.empty[(it - 1) & 1]);
-            }
-            if (it < chunks) {
-#pragma unroll
-                for (int i = 0; i < H; i += 32) put_state_terms<3, H>(s + i, tl, wg, i);
-                tc::tmem_st_wait();
-                tc::tc_fence_before();
-                tc::mbar_arrive(&bars.s);
+            } else {
+                next_state<3, H, 16>(s, 1.f, true, it < chunks, tl, wg, bars);
             }
             // <S', dS>, and dS itself for the gradients of k
             if (quarter < strips && chunks > 0) {
