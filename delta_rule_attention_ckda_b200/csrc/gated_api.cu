@@ -175,7 +175,7 @@ bool chunked_fits(const Shape& s) { return s.Hk <= 65535 && (long long)Seqs::slo
 // one after the other: whole sequences take the average sequence's (its longest is not known on the
 // host); segments take two passes of maps and one run, in as many waves as the SMs need. Segments
 // pay from about 0.7 of the whole time (B200, one sequence of 65536 tokens, 16 heads of 128: 4.2 ms
-// whole, 1.9 ms in 9 segments; of 2048 tokens: 0.17 and 0.16 ms).
+// whole, 1.6 ms in 6 segments; of 2048 tokens: 0.17 and 0.16 ms).
 int segment_chunks(const Shape& s) {
     const long long rows = (long long)s.N * s.Hv, chunks = ((long long)s.total + (long long)s.N * C - 1) / ((long long)s.N * C), sms = sm_count();
     if (s.N == 0 || chunks < 32 || rows * 4 > sms) return 0;
@@ -581,9 +581,10 @@ ckda_status_t prep_launch(const PrepArgs& a, ckda_dtype_t dt, int* blocks_out, c
         size_t smem = (size_t)8 * a.rotary * sizeof(float);
         if (kBack) smem = std::max(smem, (size_t)8 * gp * a.d * sizeof(float));
         *blocks_out = blocks;
-        if (G == 8) prep_vec_kernel<TIn, 8, UR, kBack><<<blocks, 256, smem, st>>>(a, wpt);
-        else if (G == 16) prep_vec_kernel<TIn, 16, UR, kBack><<<blocks, 256, smem, st>>>(a, wpt);
-        else prep_vec_kernel<TIn, 32, UR, kBack><<<blocks, 256, smem, st>>>(a, wpt);
+        auto go = [&](auto kernel) { kernel<<<blocks, 256, smem, st>>>(a, wpt); };
+        if (G == 8) a.interleaved ? go(prep_vec_kernel<TIn, 8, UR, kBack, true>) : go(prep_vec_kernel<TIn, 8, UR, kBack, false>);
+        else if (G == 16) a.interleaved ? go(prep_vec_kernel<TIn, 16, UR, kBack, true>) : go(prep_vec_kernel<TIn, 16, UR, kBack, false>);
+        else a.interleaved ? go(prep_vec_kernel<TIn, 32, UR, kBack, true>) : go(prep_vec_kernel<TIn, 32, UR, kBack, false>);
     } else {
         *blocks_out = kBack ? prep_blocks(a.tokens) : std::min(a.tokens, 148 * 8);
         prep_row_kernel<TIn, kBack><<<*blocks_out, 256, 0, st>>>(a);

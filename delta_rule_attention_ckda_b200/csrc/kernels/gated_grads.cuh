@@ -17,10 +17,15 @@
 // over (chunk, key head) pairs; every tile of the next pair is asked for as soon as the products
 // that read its place are done, so about 100 KB are always on their way. The tiles come by bulk
 // and tensor copies: the same loop on cp.async, 16 bytes a thread, spent 40% of its time issuing
-// them. A chunk that ends inside comes row by row, with zeros behind its end. Dw and Da are formed by four warps each and pass through
-// shared memory, where they serve as left operands straight and transposed; then a warp owns 16
-// tokens and half of the channels. Value heads that share a key head are summed in the
-// accumulators, in head order.
+// them. A chunk that ends inside comes row by row, with zeros behind its end. Dw and Da are
+// formed by four warps each and pass through shared memory, where they serve as left operands
+// straight and transposed; then a warp owns 16 tokens and half of the channels. Value heads
+// that share a key head are summed in the accumulators, in head order.
+//
+// Measured, 8192 chunks of 128 x 128 (1.3 GB): 499 us, 40% of the copy bandwidth; 714 before the bulk
+// copies. What bounds it now is the warps' own products and fragment loads between barriers (issue
+// 24%, tensor pipe 34%, shared memory 35%) with one CTA an SM by shared memory; sixteen warps
+// spill and are slower.
 #pragma once
 #include "gated_chain.cuh"
 

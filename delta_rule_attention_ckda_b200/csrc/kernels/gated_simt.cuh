@@ -15,6 +15,9 @@
 // One CTA per (sequence, head): column phases (thread = column) and row phases (thread =
 // row) over dS and R in padded shared memory. The forward states come from checkpoints every
 // KB tokens, recomputed KB at a time into a scratch of the workspace.
+//
+// What bounds it is the chain of tokens (one step after the other, a few block barriers each going
+// backward); it serves the types and sizes that the tensor-core kernels do not take.
 #pragma once
 #include "gated_common.cuh"
 

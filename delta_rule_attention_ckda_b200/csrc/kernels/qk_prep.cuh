@@ -15,14 +15,18 @@
 //
 // Vector path: a warp takes a token (several warps where tokens are few), G lanes a head row, 16
 // bytes each, UR rows in work and UR more on their way. Blocks stay for all their tokens, so
-// loads also run under the next token's angles. 32768 tokens of 16 + 16 heads of 128: 107 us,
-// 77% of the measured copy bandwidth (without the rows on their way 8% slower; 4 blocks an SM
-// instead of 3 spill, 18% slower). Backward, 16383 tokens of 16 + 8 heads: 77 us and 4 for the
-// weights' sums, 57%: 8 loads of 16 bytes a lane in flight fill the registers. What a lane does to a channel is the same for every head of
-// the token, out = r (x A + x' B) with x' the pair's other channel (from a lane R/16 away, or the
-// neighbour in the same register), so weight, cosine, sine and scale are folded into A and B once
-// per token. Warps share nothing and meet at no barrier. Rows of other sizes or alignments take
-// the scalar path, one warp per row through a row buffer.
+// loads also run under the next token's angles. What a lane does to a channel is the same for
+// every head of the token, out = r (x A + x' B) with x' the pair's other channel (from a lane
+// R/16 away, or the neighbour in the same register), so weight, cosine, sine and scale are folded
+// into A and B once per token. Warps share nothing and meet at no barrier. Rows of other sizes or
+// alignments take the scalar path, one warp per row through a row buffer.
+//
+// Measured: 32768 tokens of 16 + 16 heads of 128, 537 MB: 100 us, 82% of the copy bandwidth (without
+// the rows on their way 8% slower; with 4 blocks an SM, which spill, 18%; the pair layout chosen
+// in the kernel instead of by instance 10%: the issue slots are 70% busy). Backward, 16383 tokens
+// of 16 + 8 heads, 302 MB: 76 us and 4 for the weights' sums, 61%; two row loads of 16 bytes a
+// lane for each of x and dy in work and as many on their way fill the registers of two blocks an
+// SM (with three or with four rows they spill: 33% and 8% slower).
 #pragma once
 #include "gated_mma.cuh"
 
@@ -150,17 +154,17 @@ __device__ __forceinline__ float group_sum(float x) {
 
 // Vector path: d a multiple of 8, rows 16-byte aligned, R a multiple of 16 (half) or 8 (interleaved).
 // `wpt` warps share a token's heads.
-template <typename TIn, int G, int UR, bool kBack>
+template <typename TIn, int G, int UR, bool kBack, bool kInter>
 __global__ void __launch_bounds__(256, kBack ? 2 : 3)
 prep_vec_kernel(const PrepArgs a, int wpt) {
     extern __shared__ __align__(16) float smf[];
     constexpr int GP = 32 / G;                                  // rows a warp takes at once
     const int half = a.rotary / 2, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % G, e0 = 8 * l;
     float2* cs = reinterpret_cast<float2*>(smf) + warp * half;
-    const bool live = e0 < a.d, in = e0 < a.rotary, first = a.interleaved || e0 < half;
-    const int other = in && !a.interleaved ? (first ? lane + half / 8 : lane - half / 8) : lane;
-    const int eo = in && !a.interleaved ? (first ? e0 + half : e0 - half) : e0;      // the partners' channels
-    const int p0 = a.interleaved ? e0 / 2 : (first ? e0 : e0 - half);
+    const bool live = e0 < a.d, in = e0 < a.rotary, first = kInter || e0 < half;
+    const int other = in && !kInter ? (first ? lane + half / 8 : lane - half / 8) : lane;
+    const int eo = in && !kInter ? (first ? e0 + half : e0 - half) : e0;      // the partners' channels
+    const int p0 = kInter ? e0 / 2 : (first ? e0 : e0 - half);
     float acc[2][8];
     if constexpr (kBack) {
 #pragma unroll
@@ -172,17 +176,16 @@ prep_vec_kernel(const PrepArgs a, int wpt) {
         Raw8<TIn> x[UR], d[kBack ? UR : 1];
     };
     auto fetch = [&](Batch& b, long long t, int which, int hb) {
-        const TIn* xp = static_cast<const TIn*>(a.x[which]) + t * a.stride[which] + e0;
-        const TIn* dp = kBack ? static_cast<const TIn*>(a.dy[which]) + t * a.heads[which] * a.d + e0 : nullptr;
+        const int h = hb + lane / G, hop = wpt * GP * a.d, left = live && t < a.tokens ? a.heads[which] - h : 0;
+        const TIn* xp = static_cast<const TIn*>(a.x[which]) + t * a.stride[which] + (long long)h * a.d + e0;
+        const TIn* dp = kBack ? static_cast<const TIn*>(a.dy[which]) + (t * a.heads[which] + h) * a.d + e0 : nullptr;
 #pragma unroll
         for (int j = 0; j < UR; ++j) {
-            const int h = hb + j * wpt * GP + lane / G;
-            const bool on = live && t < a.tokens && h < a.heads[which];
             b.x[j].zero();
-            if (on) b.x[j].load(xp + (long long)h * a.d);
+            if (j * wpt * GP < left) b.x[j].load(xp + j * hop);
             if constexpr (kBack) {
                 b.d[j].zero();
-                if (on) b.d[j].load(dp + (long long)h * a.d);
+                if (j * wpt * GP < left) b.d[j].load(dp + j * hop);
             }
         }
     };
@@ -207,14 +210,14 @@ prep_vec_kernel(const PrepArgs a, int wpt) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float we = w && live ? __ldg(w + e0 + i) : 1.f;
-                const float wo = kBack ? 1.f : (w && live ? __ldg(w + (a.interleaved ? (e0 + i) ^ 1 : eo + i) % a.d) : 1.f);
+                const float wo = kBack ? 1.f : (w && live ? __ldg(w + (kInter ? (e0 + i) ^ 1 : eo + i)) : 1.f);
                 const float own = kBack ? scale : we * scale;
                 A[i] = own;
                 B[i] = 0.f;
                 if constexpr (kBack) wt[i] = we;
                 if (in) {
-                    const float2 c = cs[a.interleaved ? p0 + i / 2 : p0 + i];
-                    const bool plus = a.interleaved ? (i & 1) : !first;              // the sine's sign, turned back in reverse
+                    const float2 c = cs[kInter ? p0 + i / 2 : p0 + i];
+                    const bool plus = kInter ? (i & 1) : !first;              // the sine's sign, turned back in reverse
                     A[i] = own * c.x;
                     B[i] = wo * scale * (plus != kBack ? c.y : -c.y);
                 }
@@ -236,8 +239,8 @@ prep_vec_kernel(const PrepArgs a, int wpt) {
                     float coef;
                     const float f = norm_factor(a, group_sum<G>(s0 + s1), coef);
                     const Raw8<TIn>& turned = kBack ? now.d[kBack ? j : 0] : now.x[j];
-                    (a.interleaved ? turned.swapped() : turned.from_lane(other, in)).unpack(y);
-                    if (a.interleaved && !in) {
+                    (kInter ? turned.swapped() : turned.from_lane(other, in)).unpack(y);
+                    if (kInter && !in) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) y[i] = 0.f;
                     }
