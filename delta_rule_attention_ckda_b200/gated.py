@@ -181,6 +181,15 @@ def _workspace(which: str, dev, sizes, workspace, stream, used):
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _given(grads, names) -> dict:
+    """The outputs given for a backward call, by name."""
+    got = dict(grads or {})
+    for name in got:
+        if name not in names:
+            raise ValueError(f"grads has no {name!r}, only {', '.join(names)}")
+    return got
+
+
 def _call_device(t, name: str = "q"):
     dev = _device(t, name)
     return dev if dev.index is not None else torch.device("cuda", torch.cuda.current_device())
@@ -271,13 +280,14 @@ def gated_bwd(q, k, v, g, beta, grad_o, S0=None, grad_S_T=None, *, cu_seqlens=No
               workspace=None, stream=None):
     """ckda_gated_bwd: gradients of L = <grad_o, o> + <grad_S_T, S_T> for gated_chunk_fwd. Returns a
     dict with dq, dk, dv (in q's type), dg, dbeta, dS0 (fp32; dS0 None unless want_dS0). Output
-    tensors may be passed in `grads` (same keys); dS0 may be grad_S_T itself."""
+    tensors may be passed in `grads` (same keys); dS0 may be grad_S_T itself. Rows behind the last
+    packed sequence are not written."""
     p = _Problem(q, k, v, g, beta, S0, cu_seqlens)
     dev = p.dev
     _check(grad_o, "grad_o", p.o_shape, v.dtype, dev)
     if grad_S_T is not None:
         _check(grad_S_T, "grad_S_T", p.state_shape, F32, dev)
-    got = dict(grads or {})
+    got = _given(grads, ("dq", "dk", "dv", "dg", "dbeta", "dS0"))
     shapes = {"dq": (q.shape, q.dtype), "dk": (q.shape, q.dtype), "dv": (p.o_shape, q.dtype), "dg": (p.g_shape, F32),
               "dbeta": (p.g_shape, F32), "dS0": (p.state_shape, F32)}
     given = []
@@ -435,7 +445,7 @@ def qk_norm_rope_bwd(q, k, grad_q, grad_k=None, *, positions=None, inv_freq=None
         raise ValueError("k and grad_k come together")
     if k is not None:
         _check(grad_k, "grad_k", p.tokens_shape + (p.Hk, p.d), q.dtype, p.dev)
-    got = dict(grads or {})
+    got = _given(grads, ("dq", "dk", "dq_weight", "dk_weight"))
     spans = p.spans + [("grad_q", grad_q), ("grad_k", grad_k)]
     got["dq"] = p.out(got.get("dq"), "dq", p.Hq, q.dtype, spans, stream)
     spans.append(("dq", got["dq"]))

@@ -142,6 +142,8 @@ def test_binding_checks():
     grads = {"dq": fake(1, 4, 1, 16), "dv": fake(1, 4, 2, 16), "dg": fake(1, 4, 2, **f32), "dbeta": fake(1, 4, 2, **f32),
              "dS0": fake(1, 2, 16, 16, **f32)}
     grads["dk"] = grads["dq"]
+    with pytest.raises(ValueError, match="no 'dS_0'"):
+        ck.gated_bwd(q, k, v, g, b, fake(1, 4, 2, 16), grads={"dS_0": grads["dS0"]})
     with pytest.raises(ValueError, match="dk overlaps dq"):
         ck.gated_bwd(q, k, v, g, b, fake(1, 4, 2, 16), grads=grads)
     S = fake(3, 2, 16, 16, **f32)
