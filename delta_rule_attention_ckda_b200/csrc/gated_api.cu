@@ -171,18 +171,24 @@ bool rows_aligned(const Shape& s, long long qs, long long ks, long long vs) {
 // Whether grids and row numbers of the chunked kernels hold the call.
 bool chunked_fits(const Shape& s) { return s.Hk <= 65535 && (long long)Seqs::slots(s.N, s.total) * s.Hv * C <= 0x7fffffffLL; }
 
-// Chunks in a segment (0: whole sequences run), for a call's sizes alone. Time is counted in chunks
-// one after the other: whole sequences take the average sequence's (its longest is not known on the
-// host); segments take two passes of maps and one run, in as many waves as the SMs need. Segments
-// pay from about 0.7 of the whole time (B200, one sequence of 65536 tokens, 16 heads of 128: 4.2 ms
-// whole, 1.6 ms in 6 segments; of 2048 tokens: 0.17 and 0.16 ms).
-int segment_chunks(const Shape& s) {
-    const long long rows = (long long)s.N * s.Hv, chunks = ((long long)s.total + (long long)s.N * C - 1) / ((long long)s.N * C), sms = sm_count();
-    if (s.N == 0 || chunks < 32 || rows * 4 > sms) return 0;
-    long long best = 0, time = chunks * 7 / 10;
-    for (long long n = 3; n <= 32 && n * 4 <= chunks; ++n) {
-        const long long cps = (chunks + n - 1) / n;
-        const long long t = (((2 * n - 3) * rows + sms - 1) / sms + (n * rows + sms - 1) / sms) * cps + 8;
+// Chunks in a segment (0: whole sequences run), for a call's sizes alone. Time is counted in chunks of the
+// forward chain one after the other (4 us): a pass takes its waves of CTAs times a segment's chunks
+// and 5 or 6 more for its start, a scan a quarter per segment; going back, the chain that keeps its
+// states counts 7/4, the adjoint's two passes 6/4 and 8/4. The longest sequence is not known
+// on the host: the average is taken, back, where segments pay sooner, a quarter more. Segments have
+// to gain an eighth. B200, us, whole and in segments: one sequence of 2048 tokens and 16 heads of 128,
+// forward 140 and 112, backward 521 and 306; of 65536, forward 4200 and 1570; 2 of 4096, forward 290
+// and 245, backward 1086 and 740; 1 of 1024, forward 83 and 89 (not taken), backward 257 and 208.
+int segment_chunks(const Shape& s, bool back) {
+    if (s.N == 0) return 0;
+    const long long rows = (long long)s.N * s.Hv, sms = sm_count(), each = (long long)s.N * C, start = back ? 5 : 6;
+    const long long average = (s.total + each - 1) / each, longest = back ? (5 * average + 3) / 4 : average;
+    auto waves = [&](long long per) { return (std::max(per, 1LL) * rows + sms - 1) / sms; };
+    long long best = 0, time = waves(1) * (longest + start) * (back ? 15 : 4) * 7 / 8;      // quarters of a chunk
+    for (long long n = 3; n <= 32 && n * 2 <= longest; ++n) {
+        const long long cps = (longest + n - 1) / n, per = (average + cps - 1) / cps;
+        const long long maps = waves(2 * per - 3), run = waves(per), adjoint = waves(per - 1);
+        const long long t = back ? (4 * maps + 15 * run + 6 * adjoint) * (cps + start) + 2 * n : 4 * (maps + run) * (cps + start) + n;
         if (t < time) {
             time = t;
             best = cps;
@@ -192,7 +198,7 @@ int segment_chunks(const Shape& s) {
 }
 
 struct ChunkLayout {
-    size_t zhi, zlo, phi, plo, vec, shi, slo, dshi, u, w, parts, states, maps, total;
+    size_t zhi, zlo, phi, plo, vec, shi, slo, dshi, u, w, parts, states, maps, dstates, total;
     int cps;
 };
 ChunkLayout chunk_layout(const Shape& s, bool back) {
@@ -217,12 +223,13 @@ ChunkLayout chunk_layout(const Shape& s, bool back) {
         l.w = take((size_t)s.dv * 64 * 4);
         l.parts = take(strips * PARTS * 4);
     }
-    l.cps = back ? 0 : segment_chunks(s);
+    l.cps = segment_chunks(s, back);
     if (l.cps > 0) {
         const size_t places = SegArgs::places(s.N, s.total, l.cps) * s.Hv;
         l.states = at;
         l.maps = l.states + up256(places * s.dk * s.dv * 4);
-        at = l.maps + up256(places * s.dk * s.dk * 4);
+        l.dstates = l.maps + up256(places * s.dk * s.dk * 4);
+        at = l.dstates + (back ? up256(places * s.dk * s.dv * 4) : 0);
     }
     l.total = at;
     return l;
@@ -232,6 +239,12 @@ ChunkWs chunk_ws(const ChunkLayout& l, void* base) {
     auto H = [&](size_t at) { return reinterpret_cast<bf16*>(b + at); };
     auto F = [&](size_t at) { return reinterpret_cast<float*>(b + at); };
     return ChunkWs{H(l.zhi), H(l.zlo), H(l.phi), H(l.plo), F(l.vec), H(l.shi), H(l.slo), H(l.dshi), H(l.u), F(l.w), F(l.parts)};
+}
+
+SegArgs segments(const ChunkLayout& l, void* base) {
+    char* b = static_cast<char*>(base);
+    auto F = [&](size_t at) { return reinterpret_cast<float*>(b + at); };
+    return SegArgs{kSegWhole, l.cps, 0, F(l.states), F(l.maps), F(l.dstates)};
 }
 
 struct Call {
@@ -274,6 +287,15 @@ cudaError_t run_intra(const Call& c, const Maps& m, const ChainIn& in) {
     return cudaPeekAtLastError();
 }
 
+template <bool kSuffix>
+cudaError_t run_scan(const Call& c, const SegArgs& sg) {
+    cudaError_t e = kernel_ready(segment_scan_kernel<kSuffix>, kScanSmem);
+    if (e != cudaSuccess) return e;
+    segment_scan_kernel<kSuffix><<<dim3((unsigned)(c.s.N * c.s.Hv), (unsigned)((c.s.dv + 15) / 16)), 256, kScanSmem, c.st>>>(
+        sg, c.seqs, c.s.Hv, c.s.dk, c.s.dv);
+    return cudaPeekAtLastError();
+}
+
 template <int DK, bool kBack>
 cudaError_t run_chain_fwd(const Call& c, const Maps& m, const ChainIn& in) {
     constexpr size_t smem = ChainStage<DK, kBack>::SMEM;
@@ -281,24 +303,28 @@ cudaError_t run_chain_fwd(const Call& c, const Maps& m, const ChainIn& in) {
     cudaError_t e = kernel_ready(chain_fwd_kernel<DK, kBack>, smem, kRegLaunch);
     if (e != cudaSuccess) return e;
     SegArgs sg = c.seg;
-    auto go = [&](dim3 grid) {
-        chain_fwd_kernel<DK, kBack><<<grid, kChainThreads, smem, c.st>>>(m.q, m.k, m.v, m.o, in, c.S0, c.o, c.ST, c.ws, c.seqs, sg,
-                                                                        c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
+    const unsigned seqs = (unsigned)(c.s.N * c.s.Hv);
+    auto run = [&](unsigned grid) {
+        chain_fwd_kernel<DK, kBack><<<grid, kChainThreads, smem, c.st>>>(m.q, m.k, m.v, m.o, in, c.S0, c.o, c.ST, c.ws, c.seqs, sg, c.s.Hk,
+                                                                        c.s.Hv, c.s.dk, c.s.dv);
         return cudaPeekAtLastError();
     };
-    if (kBack || sg.cps == 0) return go(dim3((unsigned)(c.s.N * c.s.Hv)));
-    const size_t places = SegArgs::places(c.s.N, c.s.total, sg.cps) * c.s.Hv;
-    sg.mode = kSegMaps;
-    e = go(dim3((unsigned)places, 2));
+    if (sg.cps == 0) return run(seqs);
+    const unsigned places = (unsigned)(SegArgs::places(c.s.N, c.s.total, sg.cps) * c.s.Hv);
+    constexpr size_t maps_smem = ChainStage<DK, false>::SMEM;
+    e = kernel_ready(chain_fwd_kernel<DK, false>, maps_smem, kRegLaunch);
     if (e != cudaSuccess) return e;
-    segment_prefix_kernel<<<dim3((unsigned)(c.s.N * c.s.Hv), (unsigned)((c.s.dv + 31) / 32)), 256, 0, c.st>>>(sg, c.seqs, c.s.Hv, c.s.dk, c.s.dv);
+    sg.mode = kSegMaps;
+    chain_fwd_kernel<DK, false><<<dim3(places, 2), kChainThreads, maps_smem, c.st>>>(
+        m.q, m.k, m.v, m.o, in, c.S0, c.o, c.ST, c.ws, c.seqs, sg, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
     e = cudaPeekAtLastError();
+    if (e == cudaSuccess) e = run_scan<false>(c, sg);
     if (e != cudaSuccess) return e;
     sg.mode = kSegRun;
     sg.apart = c.ST != nullptr && c.ST == c.S0;
-    e = go(dim3((unsigned)places));
+    e = run(places);
     if (e != cudaSuccess || !sg.apart) return e;
-    segment_final_kernel<<<(unsigned)(c.s.N * c.s.Hv), 256, 0, c.st>>>(sg, c.seqs, c.ST, c.s.Hv, c.s.dk * c.s.dv);
+    segment_result_kernel<<<seqs, 256, 0, c.st>>>(sg, c.seqs, sg.states, false, c.ST, c.s.Hv, c.s.dk * c.s.dv);
     return cudaPeekAtLastError();
 }
 template <int DK>
@@ -306,8 +332,25 @@ cudaError_t run_chain_bwd(const Call& c, const Maps& m, const ChainIn& in) {
     constexpr size_t smem = ChainStage<DK, true>::SMEM;
     cudaError_t e = kernel_ready(chain_bwd_kernel<DK>, smem, kRegLaunch);
     if (e != cudaSuccess) return e;
-    chain_bwd_kernel<DK><<<(unsigned)(c.s.N * c.s.Hv), kChainThreads, smem, c.st>>>(
-        m.q, m.k, m.v, m.o, in, c.dST, c.gv, c.gS0, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
+    SegArgs sg = c.seg;
+    const unsigned seqs = (unsigned)(c.s.N * c.s.Hv);
+    auto run = [&](unsigned grid) {
+        chain_bwd_kernel<DK><<<grid, kChainThreads, smem, c.st>>>(m.q, m.k, m.v, m.o, in, c.dST, c.gv, c.gS0, c.ws, c.seqs, sg, c.s.Hk, c.s.Hv,
+                                                                  c.s.dk, c.s.dv);
+        return cudaPeekAtLastError();
+    };
+    if (sg.cps == 0) return run(seqs);
+    const unsigned places = (unsigned)(SegArgs::places(c.s.N, c.s.total, sg.cps) * c.s.Hv);
+    sg.mode = kSegMaps;
+    e = run(places);
+    if (e != cudaSuccess) return e;
+    e = run_scan<true>(c, sg);
+    if (e != cudaSuccess) return e;
+    sg.mode = kSegRun;
+    sg.apart = c.gS0 != nullptr && c.gS0 == c.dST;
+    e = run(places);
+    if (e != cudaSuccess || !sg.apart) return e;
+    segment_result_kernel<<<seqs, 256, 0, c.st>>>(sg, c.seqs, sg.dstates, true, c.gS0, c.s.Hv, c.s.dk * c.s.dv);
     return cudaPeekAtLastError();
 }
 template <int DK, int DV>
@@ -370,7 +413,7 @@ size_t ckda_gated_fwd_workspace_bytes(int N, int total, int Hk, int Hv, int dk, 
 int ckda_gated_fwd_segment_tokens(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt) {
     const Shape s{N, 0, total, Hk, Hv, dk, dv, dt};
     if (check_shape(s, true) != CKDA_OK || N == 0 || total == 0 || !chunked(s)) return 0;
-    return segment_chunks(s) * C;
+    return segment_chunks(s, false) * C;
 }
 
 ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -404,8 +447,7 @@ ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const 
         a.qs = q_stride; a.ks = k_stride; a.vs = v_stride;
         const ChunkLayout l = chunk_layout(s, false);
         a.ws = chunk_ws(l, workspace);
-        a.seg = SegArgs{kSegWhole, l.cps, 0, reinterpret_cast<float*>(static_cast<char*>(workspace) + l.states),
-                        reinterpret_cast<float*>(static_cast<char*>(workspace) + l.maps)};
+        a.seg = segments(l, workspace);
         a.st = st;
         const cudaError_t e = dk <= 64 ? run_chunked<64, false>(a) : run_chunked<128, false>(a);
         return e == cudaSuccess ? launch_status() : (cudaGetLastError(), CKDA_ERR_CUDA);
@@ -456,7 +498,9 @@ ckda_status_t ckda_gated_bwd(const void* q, const void* k, const void* v, const 
         a.gq = static_cast<bf16*>(grad_q); a.gk = static_cast<bf16*>(grad_k); a.gv = static_cast<bf16*>(grad_v);
         a.gg = grad_g; a.gb = grad_beta; a.gS0 = grad_S0;
         a.qs = q_stride; a.ks = k_stride; a.vs = v_stride;
-        a.ws = chunk_ws(chunk_layout(s, true), ws);
+        const ChunkLayout l = chunk_layout(s, true);
+        a.ws = chunk_ws(l, ws);
+        a.seg = segments(l, ws);
         a.st = st;
         const cudaError_t e = dk <= 64 ? run_chunked<64, true>(a) : run_chunked<128, true>(a);
         return e == cudaSuccess ? launch_status() : (cudaGetLastError(), CKDA_ERR_CUDA);

@@ -109,16 +109,19 @@ __device__ __forceinline__ bool elected() {
 
 // Long sequences on few heads run as segments of `cps` chunks side by side. A segment acts on the
 // state entering it as S -> M S + N; pass kSegMaps builds every segment's N (from zero, the first
-// from S0) and M (from the identity, with v = 0) at once, segment_prefix_kernel chains them into the
-// state behind every segment, and pass kSegRun runs the segments again from those. Segment j of
+// from S0) and M (from the identity, with v = 0) at once, segment_scan_kernel chains them into the
+// state behind every segment, and pass kSegRun runs the segments again from those. The adjoint acts
+// as dS -> M^T dS + N' on the same maps: its pass kSegMaps builds every N' (the last from dS_T),
+// segment_scan_kernel chains them, and its pass kSegRun runs. Segment j of
 // sequence n has place start / (cps C) + n + j of its own, as chunks have. 65536 tokens of 16
 // heads: maps 0.60 ms, prefix 0.02, run 0.69, against 4.2 whole.
 enum { kSegWhole = 0, kSegMaps = 1, kSegRun = 2 };
 struct SegArgs {
     int mode, cps;
-    int apart;                      // the final states go to the last segments' places: S_T is S0, which others still read
+    int apart;                      // results go to segments' places: S_T is S0 (or dS_0 is dS_T), which others still read
     float* states;                  // [place][Hv][dk][dv] fp32: N, then the state behind the segment
     float* maps;                    // [place][Hv][dk][dk] fp32: M, transposed
+    float* dstates;                 // backward: [place][Hv][dk][dv] fp32: the cotangent entering a segment from zero, then of the state before it
     __host__ __device__ static size_t places(int N, int total, int cps) { return (size_t)total / ((size_t)cps * C) + (size_t)N; }
     __device__ __forceinline__ int first_place(int n, int start) const { return start / (cps * C) + n; }
     __device__ __forceinline__ int find(const Seqs& seqs, int place) const {
@@ -344,7 +347,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ ChainBars bars;
     const int h = blockIdx.x % Hv, hk = h / (Hv / Hk), place = blockIdx.x / Hv;
-    const int n = !kBack && sg.mode ? sg.find(seqs, place) : place;
+    const int n = sg.mode ? sg.find(seqs, place) : place;
     const bool maps = !kBack && sg.mode == kSegMaps, transition = maps && blockIdx.y == 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int start, len;
@@ -356,10 +359,11 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     const size_t mat = (size_t)dk * dv, sbase = ((size_t)n * Hv + h) * mat;
     const float* from = S0 == nullptr ? nullptr : S0 + sbase;          // the entering state
     float* to = ST == nullptr ? nullptr : ST + sbase;                  // where the leaving state goes
-    if (!kBack && sg.mode) {                   // this segment's chunks, as a sequence of their own
+    bool last = true;
+    if (sg.mode) {                             // this segment's chunks, as a sequence of their own
         const int j = place - sg.first_place(n, start), skip = j * sg.cps;
         if (j < 0 || (j > 0 && (long long)skip * C >= len)) return;
-        const bool last = (long long)(skip + sg.cps) * C >= len;
+        last = (long long)(skip + sg.cps) * C >= len;
         if (maps && (last || (transition && j == 0))) return;
         const size_t own = (size_t)place * Hv + h;
         if (maps) {
@@ -548,8 +552,8 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             } else {
                 next_state<2, H, 32>(s, 1.f, true, c < chunks, tl, wg, bars);
             }
-            if constexpr (kBack) {             // the entering (at the end: the final) state for the backward kernels
-                if (live) {
+            if constexpr (kBack) {             // the entering (behind the last chunk: the final) state for the backward kernels
+                if (live && (c < chunks || last)) {
                     const size_t to = ((size_t)(slot0 + c) * Hv + h) * mat + ((size_t)(wg * H / 8) * dv + row) * 8;
                     put_state<H>(s, ws.shi + to, ws.slo + to, (size_t)dv * 8, dk - wg * H);
                 }
@@ -654,52 +658,89 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     chain_end(bars);
 }
 
-// The state behind every segment, in place of its N: S_j = M_j S_{j-1} + N_j, fp32, in order. A CTA of
-// 256 threads takes 32 columns of one (sequence, head); a thread one row and 16 columns.
+// The states between segments from their maps, fp32, one segment after the other.
+// Prefix: the state behind every segment but the last, S_j = M_j S_{j-1} + N_j, in place of N_j.
+// Suffix: the cotangent of the state before every segment but the first, D_j = M_j^T D_{j+1} + N'_j, in
+// place of N'_j. A CTA of 256 threads takes 16 columns of one (sequence, head), a thread one row and
+// 8 columns; the next map comes while one is multiplied (2 us a segment; read in the loop it was 10).
+constexpr int kScanLd = 132;                   // floats in a row of a map: 16-byte reads of 8 rows side by side meet no bank twice
+constexpr size_t kScanSmem = (2 * 128 * kScanLd + 128 * 16) * sizeof(float);
+template <bool kSuffix>
 __global__ void __launch_bounds__(256)
-segment_prefix_kernel(SegArgs sg, Seqs seqs, int Hv, int dk, int dv) {
-    __shared__ float S[128][33];
-    const int n = blockIdx.x / Hv, h = blockIdx.x % Hv, i = threadIdx.x & 127, j0 = (threadIdx.x >> 7) * 16, c0 = blockIdx.y * 32;
+segment_scan_kernel(SegArgs sg, Seqs seqs, int Hv, int dk, int dv) {
+    extern __shared__ __align__(16) float scan[];
+    float* S = scan + 2 * 128 * kScanLd;       // [128][16]
+    const int n = blockIdx.x / Hv, h = blockIdx.x % Hv, i = threadIdx.x & 127, j0 = (threadIdx.x >> 7) * 8, c0 = blockIdx.y * 16 + j0;
     int start, len;
     bool ok;
     seqs.get(n, start, len, ok);
-    const int first = sg.first_place(n, start), count = (len + sg.cps * C - 1) / (sg.cps * C) - 1;   // the last needs none
+    const int first = sg.first_place(n, start), count = (len + sg.cps * C - 1) / (sg.cps * C);
     const size_t mat = (size_t)dk * dv;
-    for (int seg = 0; seg < count; ++seg) {
-        const size_t own = (size_t)(first + seg) * Hv + h;
-        float* st = sg.states + own * mat;
-        float acc[16];
+    float* places = kSuffix ? sg.dstates : sg.states;
+    auto own = [&](int step) { return (size_t)(first + (kSuffix ? count - 1 - step : step)) * Hv + h; };
+    auto fetch = [&](int step) {
+        const float* from = sg.maps + own(step) * dk * dk;
+        const uint32_t to = s32(scan + (step & 1) * 128 * kScanLd);
+        for (int e = threadIdx.x; e < dk * (dk / 4); e += 256) {
+            const int r = e / (dk / 4), x = e % (dk / 4);
+            cp16(to + (r * kScanLd + 4 * x) * 4, from + (size_t)r * dk + 4 * x, true);
+        }
+    };
+    for (int step = 0; step < count - 1; ++step) {
+        float* st = places + own(step) * mat + (size_t)i * dv + c0;
+        const bool live = i < dk && c0 < dv;   // dv is a multiple of 8
+        float4 add[2];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) acc[j] = i < dk && c0 + j0 + j < dv ? st[(size_t)i * dv + c0 + j0 + j] : 0.f;
-        if (seg > 0 && i < dk) {
-            const float* M = sg.maps + own * dk * dk + i;
-#pragma unroll 8
-            for (int d = 0; d < dk; ++d) {
-                const float m = M[(size_t)d * dk];
+        for (int j = 0; j < 2; ++j) add[j] = live ? reinterpret_cast<const float4*>(st)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
+        if (step + 1 < count - 1) fetch(step + 1);
+        cp_commit();
+        float acc[8] = {};
+        if (step > 0) {                        // the first has its state already
+            cp_wait<1>();
+            __syncthreads();
+            const float* M = scan + (step & 1) * 128 * kScanLd;
+#pragma unroll 4
+            for (int d = 0; d < dk; d += 4) {
+                float m[4];
+                if constexpr (kSuffix) {
+                    const float4 x = *reinterpret_cast<const float4*>(M + i * kScanLd + d);
+                    m[0] = x.x; m[1] = x.y; m[2] = x.z; m[3] = x.w;
+                } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) acc[j] = fmaf(m, S[d][j0 + j], acc[j]);
+                    for (int e = 0; e < 4; ++e) m[e] = M[(d + e) * kScanLd + i];
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int j = 0; j < 8; j += 4) {
+                        const float4 x = *reinterpret_cast<const float4*>(S + (d + e) * 16 + j0 + j);
+                        fma2(acc[j], acc[j + 1], m[e], m[e], x.x, x.y);
+                        fma2(acc[j + 2], acc[j + 3], m[e], m[e], x.z, x.w);
+                    }
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            if (i < dk) S[i][j0 + j] = acc[j];
-            if (seg > 0 && i < dk && c0 + j0 + j < dv) st[(size_t)i * dv + c0 + j0 + j] = acc[j];
+        for (int j = 0; j < 2; ++j) {
+            const float4 x = make_float4(acc[4 * j] + add[j].x, acc[4 * j + 1] + add[j].y, acc[4 * j + 2] + add[j].z, acc[4 * j + 3] + add[j].w);
+            *reinterpret_cast<float4*>(S + i * 16 + j0 + 4 * j) = x;
+            if (step > 0 && live) reinterpret_cast<float4*>(st)[j] = x;
         }
         __syncthreads();
     }
+    cp_wait<0>();
 }
 
-// The final states from the last segments' places to S_T.
+// Results from the last (or first) segments' places to where they belong.
 __global__ void __launch_bounds__(256)
-segment_final_kernel(SegArgs sg, Seqs seqs, float* __restrict__ ST, int Hv, int mat) {
+segment_result_kernel(SegArgs sg, Seqs seqs, const float* __restrict__ places, bool first, float* __restrict__ result, int Hv, int mat) {
     const int n = blockIdx.x / Hv, h = blockIdx.x % Hv;
     int start, len;
     bool ok;
     seqs.get(n, start, len, ok);
-    const int last = sg.first_place(n, start) + max((len + sg.cps * C - 1) / (sg.cps * C) - 1, 0);
-    const float4* from = reinterpret_cast<const float4*>(sg.states + ((size_t)last * Hv + h) * mat);
-    float4* to = reinterpret_cast<float4*>(ST + (size_t)blockIdx.x * mat);
+    const int place = sg.first_place(n, start) + (first ? 0 : max((len + sg.cps * C - 1) / (sg.cps * C) - 1, 0));
+    const float4* from = reinterpret_cast<const float4*>(places + ((size_t)place * Hv + h) * mat);
+    float4* to = reinterpret_cast<float4*>(result + (size_t)blockIdx.x * mat);
     for (int i = threadIdx.x; i < mat / 4; i += 256) to[i] = from[i];
 }
 
@@ -716,19 +757,36 @@ template <int DK>
 __global__ void __launch_bounds__(kChainThreads, 1)
 chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                  const __grid_constant__ CUtensorMap mo, const ChainIn in, const float* dST, __nv_bfloat16* __restrict__ grad_v,
-                 float* grad_S0, ChunkWs ws, Seqs seqs, int Hk, int Hv, int dk, int dv) {
+                 float* grad_S0, ChunkWs ws, Seqs seqs, SegArgs sg, int Hk, int Hv, int dk, int dv) {
     using L = ChainStage<DK, true>;
     constexpr int H = DK / 2;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ ChainBars bars;
-    const int n = blockIdx.x / Hv, h = blockIdx.x % Hv, hk = h / (Hv / Hk);
+    const int h = blockIdx.x % Hv, hk = h / (Hv / Hk), place = blockIdx.x / Hv, n = sg.mode ? sg.find(seqs, place) : place;
+    const bool maps = sg.mode == kSegMaps;     // the cotangent alone
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int start, len;
     bool ok;
     seqs.get(n, start, len, ok);
-    const int chunks = (len + C - 1) / C, slot0 = seqs.first_slot(n, start), strips = (dv + 31) / 32;
+    int slot0 = seqs.first_slot(n, start);
+    const int strips = (dv + 31) / 32;
     const size_t mat = (size_t)dk * dv, sbase = ((size_t)n * Hv + h) * mat;
+    const float* from = dST == nullptr ? nullptr : dST + sbase;        // the cotangent of the leaving state
+    float* to = grad_S0 == nullptr ? nullptr : grad_S0 + sbase;        // where that of the entering state goes
+    if (sg.mode) {                             // this segment's chunks, as a sequence of their own
+        const int j = place - sg.first_place(n, start), skip = j * sg.cps;
+        if (j < 0 || (j > 0 && (long long)skip * C >= len) || (maps && j == 0)) return;
+        const bool last = (long long)(skip + sg.cps) * C >= len;
+        const size_t own = (size_t)place * Hv + h;
+        if (!last) from = maps ? nullptr : sg.dstates + (own + Hv) * mat;
+        if (maps || (j == 0 && sg.apart)) to = sg.dstates + own * mat;
+        else if (j > 0) to = nullptr;
+        slot0 += skip;
+        start += skip * C;
+        len = last ? len - skip * C : sg.cps * C;
+    }
+    const int chunks = (len + C - 1) / C;
     chain_begin(bars, sm, 2 * L::BYTES, kOutWarps);
     const uint32_t tm = bars.tmem, base = s32(sm);
 
@@ -739,7 +797,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll 1
             for (int it = 0; it < chunks; ++it) {
                 const int c = chunks - 1 - it;
-                if (x == 32) {                 // what the epilogues read straight from memory, into L2
+                if (x == 32 && !maps) {        // what the epilogues read straight from memory, into L2
                     const size_t wh = (size_t)(slot0 + c) * Hv + h;
                     tc::prefetch_l2_bulk(ws.shi + (wh + (it ? 0 : Hv)) * mat, (uint32_t)(mat * 2));
                     tc::prefetch_l2_bulk(ws.slo + (wh + (it ? 0 : Hv)) * mat, (uint32_t)(mat * 2));
@@ -848,6 +906,13 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             tc::tmem_st_wait();
             tc::tc_fence_before();
             tc::mbar_arrive(&bars.d);
+            if (maps) {                                            // nobody reads y
+                chain_wait(bars, &bars.u, it & 1);
+                tc::mbar_arrive(&bars.out);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars.empty[it & 1]);
+                continue;
+            }
             float w[32];
             const float4* wp = reinterpret_cast<const float4*>(ws.w + wh * 64 * dv) + (live ? row : 0);
             auto load_w = [&](int half) {
@@ -898,7 +963,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll
         for (int i = 0; i < H; ++i) {
             const int d = wg * H + i;
-            s[i] = (dST != nullptr && live && d < dk) ? dST[sbase + (size_t)d * dv + row] : 0.f;
+            s[i] = (from != nullptr && live && d < dk) ? from[(size_t)d * dv + row] : 0.f;
         }
 #pragma unroll 1
         for (int it = 0; it <= chunks; ++it) {
@@ -909,7 +974,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             const size_t next = ((size_t)(slot0 + c + 1) * Hv + h) * mat + ((size_t)(wg * H / 8) * dv + row) * 8;
 #pragma unroll
             for (int i = 0; i < H / 8; ++i) {
-                const bool in = live && chunks > 0 && wg * H + 8 * i < dk;
+                const bool in = live && chunks > 0 && !maps && wg * H + 8 * i < dk;
                 sh[i] = in ? *reinterpret_cast<const uint4*>(ws.shi + next + (size_t)i * dv * 8) : make_uint4(0, 0, 0, 0);
                 sl[i] = in ? *reinterpret_cast<const uint4*>(ws.slo + next + (size_t)i * dv * 8) : make_uint4(0, 0, 0, 0);
             }
@@ -924,7 +989,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 next_state<3, H, 16>(s, 1.f, true, it < chunks, tl, wg, bars);
             }
             // <S', dS>, and dS itself for the gradients of k
-            if (quarter < strips && chunks > 0) {
+            if (quarter < strips && chunks > 0 && !maps) {
                 float dot0 = 0.f, dot1 = 0.f;
 #pragma unroll
                 for (int i = 0; i < H / 8; ++i) {
@@ -1004,11 +1069,11 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             tc::tc_fence_before();
             tc::mbar_arrive(&bars.u);
         }
-        if (grad_S0 != nullptr && live) {
+        if (to != nullptr && live) {
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 const int d = wg * H + i;
-                if (d < dk) grad_S0[sbase + (size_t)d * dv + row] = s[i];
+                if (d < dk) to[(size_t)d * dv + row] = s[i];
             }
         }
     }

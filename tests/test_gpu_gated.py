@@ -169,6 +169,30 @@ def test_backward_packed(ck, case):
     near_grads(got, q, k, v, g, b, do, S0, dST, cu)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("case", SEGMENTED, ids=str)
+def test_backward_in_segments(ck, case, in_place):
+    lens, Hk, Hv, dk, dv = case
+    if isinstance(lens, tuple):
+        cu, lead, N, total = None, lens, lens[0], lens[0] * lens[1]
+    else:
+        cu, total = packed(lens, 3)
+        lead, N = (total,), len(lens)
+    assert ck.gated_segment_tokens(N, total, Hk, Hv, dk, dv) > 0
+    q, k, v, g, b, S0, do, dST = make(lead, Hk, Hv, dk, dv, BF, total, N, gate=-5.0)
+    x = dev(q, k, v, g, b, do, S0, dST)
+    got = ck.gated_bwd(*x, cu_seqlens=None if cu is None else cu.cuda(), grads={"dS0": x[7]} if in_place else None)
+    again = ck.gated_bwd(*x[:7], dST.cuda(), cu_seqlens=None if cu is None else cu.cuda())
+    fine(ck)
+    n = total if cu is None else sum(lens)
+    for name in ("dq", "dk", "dv", "dg", "dbeta"):
+        if cu is not None:
+            got[name][n:], again[name][n:] = 0.0, 0.0
+        assert torch.equal(got[name], again[name]), name
+    assert torch.equal(got["dS0"], again["dS0"])
+    near_grads(got, q, k, v, g, b, do, S0, dST, cu)
+
+
 def test_backward_by_differences(ck):
     """The fp32 gradients against central differences of the forward (fp32, steps of 2^-6: the
     rule is at most cubic in one input's entries here, differences are off by the third
