@@ -241,10 +241,11 @@ ChunkWs chunk_ws(const ChunkLayout& l, void* base) {
     return ChunkWs{H(l.zhi), H(l.zlo), H(l.phi), H(l.plo), F(l.vec), H(l.shi), H(l.slo), H(l.dshi), H(l.u), F(l.w), F(l.parts)};
 }
 
-SegArgs segments(const ChunkLayout& l, void* base) {
+SegArgs segments(const ChunkLayout& l, void* base, const Shape& s, bool packed) {
     char* b = static_cast<char*>(base);
     auto F = [&](size_t at) { return reinterpret_cast<float*>(b + at); };
-    return SegArgs{kSegWhole, l.cps, 0, F(l.states), F(l.maps), F(l.dstates)};
+    const int ranked = packed && l.cps == 0 && s.N <= kMaxRanked && (long long)s.N * s.Hv > sm_count();
+    return SegArgs{kSegWhole, l.cps, ranked, 0, F(l.states), F(l.maps), F(l.dstates)};
 }
 
 struct Call {
@@ -447,7 +448,7 @@ ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const 
         a.qs = q_stride; a.ks = k_stride; a.vs = v_stride;
         const ChunkLayout l = chunk_layout(s, false);
         a.ws = chunk_ws(l, workspace);
-        a.seg = segments(l, workspace);
+        a.seg = segments(l, workspace, s, cu_seqlens != nullptr);
         a.st = st;
         const cudaError_t e = dk <= 64 ? run_chunked<64, false>(a) : run_chunked<128, false>(a);
         return e == cudaSuccess ? launch_status() : (cudaGetLastError(), CKDA_ERR_CUDA);
@@ -500,7 +501,7 @@ ckda_status_t ckda_gated_bwd(const void* q, const void* k, const void* v, const 
         a.qs = q_stride; a.ks = k_stride; a.vs = v_stride;
         const ChunkLayout l = chunk_layout(s, true);
         a.ws = chunk_ws(l, ws);
-        a.seg = segments(l, ws);
+        a.seg = segments(l, ws, s, cu_seqlens != nullptr);
         a.st = st;
         const cudaError_t e = dk <= 64 ? run_chunked<64, true>(a) : run_chunked<128, true>(a);
         return e == cudaSuccess ? launch_status() : (cudaGetLastError(), CKDA_ERR_CUDA);

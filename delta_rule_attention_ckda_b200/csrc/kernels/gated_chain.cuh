@@ -118,6 +118,7 @@ __device__ __forceinline__ bool elected() {
 enum { kSegWhole = 0, kSegMaps = 1, kSegRun = 2 };
 struct SegArgs {
     int mode, cps;
+    int longest_first;              // whole sequences of several lengths in more CTAs than SMs: see by_length
     int apart;                      // results go to segments' places: S_T is S0 (or dS_0 is dS_T), which others still read
     float* states;                  // [place][Hv][dk][dv] fp32: N, then the state behind the segment
     float* maps;                    // [place][Hv][dk][dk] fp32: M, transposed
@@ -134,6 +135,28 @@ struct SegArgs {
         return lo;
     }
 };
+
+// The sequence of rank `place` by length, longest first (equal ones in order): started last, a long one
+// runs on alone (13 sequences of 234 to 1536 tokens, 16 heads: 138 us in order, 107 so). The block together;
+// `lens`: memory for N <= kMaxRanked lengths.
+constexpr int kMaxRanked = 256;
+__device__ __forceinline__ int by_length(const Seqs& seqs, int place, int* lens) {
+    __shared__ int found;
+    for (int m = threadIdx.x; m < seqs.N; m += blockDim.x) {
+        int start;
+        bool ok;
+        seqs.get(m, start, lens[m], ok);
+    }
+    __syncthreads();
+    if (threadIdx.x < seqs.N) {
+        const int mine = lens[threadIdx.x];
+        int rank = 0;
+        for (int m = 0; m < seqs.N; ++m) rank += lens[m] > mine || (lens[m] == mine && m < (int)threadIdx.x);
+        if (rank == place) found = threadIdx.x;
+    }
+    __syncthreads();
+    return found;
+}
 
 // The loading warps' share (thread x) of a chunk into stage `st`, completing on `full`: k, q, v, dO
 // by tensor copies where the chunk is whole, else by rows with zeros behind the sequence's end;
@@ -347,7 +370,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ ChainBars bars;
     const int h = blockIdx.x % Hv, hk = h / (Hv / Hk), place = blockIdx.x / Hv;
-    const int n = sg.mode ? sg.find(seqs, place) : place;
+    const int n = sg.mode ? sg.find(seqs, place) : (sg.longest_first ? by_length(seqs, place, reinterpret_cast<int*>(sm)) : place);
     const bool maps = !kBack && sg.mode == kSegMaps, transition = maps && blockIdx.y == 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int start, len;
@@ -763,7 +786,8 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ ChainBars bars;
-    const int h = blockIdx.x % Hv, hk = h / (Hv / Hk), place = blockIdx.x / Hv, n = sg.mode ? sg.find(seqs, place) : place;
+    const int h = blockIdx.x % Hv, hk = h / (Hv / Hk), place = blockIdx.x / Hv;
+    const int n = sg.mode ? sg.find(seqs, place) : (sg.longest_first ? by_length(seqs, place, reinterpret_cast<int*>(sm)) : place);
     const bool maps = sg.mode == kSegMaps;     // the cotangent alone
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int start, len;

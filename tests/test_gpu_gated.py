@@ -60,6 +60,9 @@ def test_forward_dense(ck, case):
 PACKED = [  # lengths, rows behind the last sequence, Hk, Hv, dk, dv, dtype
     ([5], 0, 1, 1, 64, 64, BF), ([1, 64, 0, 65, 130], 7, 2, 4, 128, 128, BF), ([0, 0, 3], 1, 1, 2, 64, 128, BF),
     ([63, 1, 1, 128, 2], 0, 1, 1, 128, 64, BF), ([9, 0, 17], 3, 1, 2, 20, 36, F32), ([200], 56, 1, 1, 40, 24, BF),
+    # more sequences than SMs: up to 256 of them start longest first
+    ([7 * i * i % 83 for i in range(40)], 5, 2, 4, 64, 64, BF), ([i % 3 for i in range(300)], 2, 1, 1, 64, 64, BF),
+    ([1 + 90 * (i == 200) for i in range(256)], 0, 1, 1, 8, 128, BF),
 ]
 
 
@@ -68,7 +71,11 @@ def packed(lens, tail):
     return cu, sum(lens) + tail
 
 
-@pytest.mark.parametrize("case", PACKED, ids=str)
+def named(case):
+    return str(case) if len(case[0]) < 10 else f"{len(case[0])} sequences, {case[2:]}"
+
+
+@pytest.mark.parametrize("case", PACKED, ids=named)
 def test_forward_packed(ck, case):
     lens, tail, Hk, Hv, dk, dv, dt = case
     cu, total = packed(lens, tail)
@@ -152,7 +159,7 @@ def test_backward_dense(ck, case):
     near_grads(got, q, k, v, g, b, do, S0, dST)
 
 
-@pytest.mark.parametrize("case", PACKED, ids=str)
+@pytest.mark.parametrize("case", PACKED, ids=named)
 def test_backward_packed(ck, case):
     lens, tail, Hk, Hv, dk, dv, dt = case
     cu, total = packed(lens, tail)
