@@ -66,12 +66,11 @@ struct ChainStage {
     static constexpr uint32_t BYTES = VECS + 1024;
     static constexpr uint32_t OUT = 2 * BYTES;                     // [64][128] rows on their way out
     static constexpr size_t SMEM = OUT + 16384 + 1024;
-    static constexpr uint32_t kTileBytes = (DK / 64) * 16384 + 16384 + (kDO ? 16384 : 0);
 };
 static_assert(ChainStage<128, true>::SMEM <= 232448, "more shared memory than an SM has");
 
 struct ChainBars {
-    uint64_t full[2], empty[2], s[2], m1, x, m2, d, u, uo, m3, o, out, qs;
+    uint64_t full[2], empty[2], do_full[2], do_empty[2], s[2], m1, x, m2, d, u, uo, m3, o, out, qs;
     uint32_t tmem;
     int dead;                       // a bounded wait ran out: nothing waits any more, the loops run off
 };
@@ -158,19 +157,18 @@ __device__ __forceinline__ int by_length(const Seqs& seqs, int place, int* lens)
     return found;
 }
 
-// The loading warps' share (thread x) of a chunk into stage `st`, completing on `full`: k, q, v, dO
+// The loading warps' share (thread x) of a chunk into stage `st`, completing on `full`: k, q, v (kDO: dO too)
 // by tensor copies where the chunk is whole, else by rows with zeros behind the sequence's end;
 // the lower blocks of Z and P (those above the block diagonal stay the zeros the kernel starts
 // with); the vectors.
-template <int DK, bool kDO>
+template <typename L, int DK, bool kDO>
 __device__ __forceinline__ void chain_load(uint32_t st, uint64_t* full, int x, const ChainIn& in, const CUtensorMap* mq, const CUtensorMap* mk,
                                            const CUtensorMap* mv, const CUtensorMap* mo, const ChunkWs& ws, size_t wh, int tok, int nt,
                                            int h, int hk, int Hv, int dk, int dv) {
-    using L = ChainStage<DK, kDO>;
     constexpr int NT = 32 * kLoadWarps, PK = DK / 8;
     const bool tiles = in.maps && nt == C;
     if (x == 0) {
-        tc::mbar_arrive_expect_tx(full, tiles ? L::kTileBytes : 0);
+        tc::mbar_arrive_expect_tx(full, tiles ? (DK / 64) * 16384 + 16384 + (kDO ? 16384 : 0) : 0);
         if (tiles) {
 #pragma unroll
             for (int b = 0; b < DK / 64; ++b) {
@@ -221,6 +219,28 @@ __device__ __forceinline__ void chain_load(uint32_t st, uint64_t* full, int x, c
     cp_commit();
     cp_wait<0>();
     tc::fence_proxy_async_smem();
+    tc::mbar_arrive(full);
+}
+
+// The tile of dO alone, completing on `full`: the forward chain's out warps read it last, and nothing
+// else should wait for them.
+template <typename L>
+__device__ __forceinline__ void chain_load_do(uint32_t st, uint64_t* full, int x, const ChainIn& in, const CUtensorMap* mo, int tok, int nt,
+                                              int h, int Hv, int dv) {
+    const bool tiles = in.maps && nt == C;
+    if (x == 0) {
+        tc::mbar_arrive_expect_tx(full, tiles ? 16384 : 0);
+        if (tiles) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) tma_rows(st + L::DO + b * 8192, mo, full, 64 * b, h, tok);
+        }
+    }
+    if (!tiles) {
+        tile_rows<32 * kLoadWarps>(st + L::DO, in.dO + ((size_t)tok * Hv + h) * dv, (long long)Hv * dv, nt, dv, 128, x);
+        cp_commit();
+        cp_wait<0>();
+        tc::fence_proxy_async_smem();
+    }
     tc::mbar_arrive(full);
 }
 
@@ -336,6 +356,8 @@ __device__ __forceinline__ void chain_begin(ChainBars& b, unsigned char* stages,
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&b.full[i], 32 * kLoadWarps + 1);
             tc::mbar_init(&b.empty[i], 1 + kEpiWarps + out_warps);
+            tc::mbar_init(&b.do_full[i], 32 * kLoadWarps + 1);
+            tc::mbar_init(&b.do_empty[i], kOutWarps);
         }
         for (uint64_t* e : {&b.s[0], &b.s[1], &b.x, &b.u, &b.uo}) tc::mbar_init(e, 32 * kEpiWarps);
         for (uint64_t* e : {&b.d, &b.out, &b.qs}) tc::mbar_init(e, 32 * kOutWarps);
@@ -412,8 +434,12 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 if (c >= 2) chain_wait(bars, &bars.empty[c & 1], ((c >> 1) - 1) & 1);
-                chain_load<DK, kBack>(base + (c & 1) * L::BYTES, &bars.full[c & 1], x, in, &mq, &mk, &mv, &mo, ws,
-                                      (size_t)(slot0 + c) * Hv + h, start + c * C, min(C, len - c * C), h, hk, Hv, dk, dv);
+                chain_load<L, DK, false>(base + (c & 1) * L::BYTES, &bars.full[c & 1], x, in, &mq, &mk, &mv, &mo, ws,
+                                         (size_t)(slot0 + c) * Hv + h, start + c * C, min(C, len - c * C), h, hk, Hv, dk, dv);
+                if constexpr (kBack) {
+                    if (c >= 2) chain_wait(bars, &bars.do_empty[c & 1], ((c >> 1) - 1) & 1);
+                    chain_load_do<L>(base + (c & 1) * L::BYTES, &bars.do_full[c & 1], x, in, &mo, start + c * C, min(C, len - c * C), h, Hv, dv);
+                }
             }
         } else {                               // ------------------------------------------ products
             constexpr uint32_t i128 = tc::idesc_bf16(128, 128, 0, 0), i64 = tc::idesc_bf16(128, 64, 0, 0),
@@ -516,6 +542,8 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 const float4 e = *reinterpret_cast<const float4*>(eg + i);
                 r[i] *= e.x; r[i + 1] *= e.y; r[i + 2] *= e.z; r[i + 3] *= e.w;
             }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars.empty[c & 1]);        // of the stage only dO is read from here on
             chain_wait(bars, &bars.o, c & 1);
             tc::tc_fence_after();
 #pragma unroll
@@ -528,6 +556,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             }
             tc::tc_fence_before();
             tc::mbar_arrive(&bars.out);
+            if constexpr (kBack) chain_wait(bars, &bars.do_full[c & 1], (c >> 1) & 1);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 if constexpr (kBack) {
@@ -543,9 +572,10 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                         *reinterpret_cast<__nv_bfloat16*>(tile + (32 * half + i) * 256 + 2 * row) = __float2bfloat16_rn(r[32 * half + i]);
                 }
             }
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&bars.empty[c & 1]);
-            if constexpr (!kBack) {
+            if constexpr (kBack) {
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bars.do_empty[c & 1]);
+            } else {
                 out_sync();
                 rows_out(tile, x, o + ((size_t)tok * Hv + h) * dv, (long long)Hv * dv, nt, dv);
                 out_sync();
@@ -828,7 +858,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     tc::prefetch_l2_bulk(ws.w + wh * 64 * dv, (uint32_t)(64 * dv * 4));
                 }
                 if (it >= 2) chain_wait(bars, &bars.empty[it & 1], ((it >> 1) - 1) & 1);
-                chain_load<DK, true>(base + (it & 1) * L::BYTES, &bars.full[it & 1], x, in, &mq, &mk, &mv, &mo, ws,
+                chain_load<L, DK, true>(base + (it & 1) * L::BYTES, &bars.full[it & 1], x, in, &mq, &mk, &mv, &mo, ws,
                                      (size_t)(slot0 + c) * Hv + h, start + c * C, min(C, len - c * C), h, hk, Hv, dk, dv);
             }
         } else {                               // ------------------------------------------ products
