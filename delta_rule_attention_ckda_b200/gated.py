@@ -63,10 +63,11 @@ def _rows(t, name: str, lead: int, dtype, dev) -> int:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {lead + 2} dimensions")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    heads, d = t.shape[-2:]
+    shape = t.shape
+    heads, d = shape[-2], shape[-1]
     inner = heads * d
     if t.is_contiguous() or t.numel() == 0:
-        return max(inner, 1)
+        return inner or 1
     st = t.stride()
     if (d > 1 and st[-1] != 1) or (heads > 1 and st[-2] != d):
         raise ValueError(f"{name} must have contiguous heads and channels, has strides {st}")
@@ -157,23 +158,23 @@ def _bytes(which: str, device_index: int, sizes) -> int:
         return int(getattr(load(), which)(*sizes))
 
 
-def _empty(shape, dev, dtype, stream):
-    """New memory for a call on `stream`: of that stream, so that torch hands it out again only behind
-    the call, whatever the current stream is."""
+def _empty(like, shape, stream, dtype=None):
+    """New memory on like's device and (unless given) of its type, for a call on `stream`: of that
+    stream, so that torch hands it out again only behind the call, whatever the current stream is."""
     if stream is None:
-        return torch.empty(shape, device=dev, dtype=dtype)
-    if stream.device != dev:
-        raise ValueError(f"stream is on {stream.device}, the call's tensors are on {dev}")
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+    if stream.device != like.device:
+        raise ValueError(f"stream is on {stream.device}, the call's tensors are on {like.device}")
     with torch.cuda.stream(stream):
-        return torch.empty(shape, device=dev, dtype=dtype)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _workspace(which: str, dev, sizes, workspace, stream, used):
+def _workspace(which: str, dev, sizes, workspace, stream, like, used):
     need = _bytes(which, dev.index, sizes)
     if workspace is None:
         if need == 0:
             return None, 0
-        return _empty(need, dev, torch.uint8, stream), need
+        return _empty(like, need, stream, torch.uint8), need
     _on(workspace, "workspace", dev)
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
@@ -254,7 +255,7 @@ def gated_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, o=None, S_T=N
     dev = p.dev
     spans = p.spans
     if o is None:
-        o = _empty(p.o_shape, dev, v.dtype, stream)
+        o = _empty(v, p.o_shape, stream)
     else:
         _check(o, "o", p.o_shape, v.dtype, dev)
         _apart(o, "o", spans + [("S0", S0)])
@@ -263,8 +264,8 @@ def gated_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, o=None, S_T=N
         same = S0 is not None and S_T.data_ptr() == S0.data_ptr()
         _apart(S_T, "S_T", spans + [("o", o)] + ([] if same else [("S0", S0)]))
     elif want_state:
-        S_T = _empty(p.state_shape, dev, F32, stream)
-    workspace, wbytes = _workspace("ckda_gated_fwd_workspace_bytes", dev, p.ws_sizes, workspace, stream,
+        S_T = _empty(g, p.state_shape, stream)
+    workspace, wbytes = _workspace("ckda_gated_fwd_workspace_bytes", dev, p.ws_sizes, workspace, stream, g,
                                    spans + [("S0", S0), ("o", o), ("S_T", S_T)])
     _launch(dev, stream, load().ckda_gated_fwd, "ckda_gated_fwd",
             (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(o), _ptr(S_T), _ptr(cu_seqlens), *p.sizes,
@@ -295,7 +296,7 @@ def gated_bwd(q, k, v, g, beta, grad_o, S0=None, grad_S_T=None, *, cu_seqlens=No
         if name == "dS0" and not want_dS0:
             got[name] = None
         elif got.get(name) is None:
-            got[name] = _empty(shape, dev, dtype, stream)
+            got[name] = _empty(q if dtype is q.dtype else g, shape, stream)
         else:
             _check(got[name], name, shape, dtype, dev)
             given.append(name)
@@ -304,7 +305,7 @@ def gated_bwd(q, k, v, g, beta, grad_o, S0=None, grad_S_T=None, *, cu_seqlens=No
         if not (name == "dS0" and grad_S_T is not None and got[name].data_ptr() == grad_S_T.data_ptr()):
             others.append(("grad_S_T", grad_S_T))
         _apart(got[name], name, others)
-    workspace, wbytes = _workspace("ckda_gated_bwd_workspace_bytes", dev, p.ws_sizes, workspace, stream,
+    workspace, wbytes = _workspace("ckda_gated_bwd_workspace_bytes", dev, p.ws_sizes, workspace, stream, g,
                                    p.spans + [("S0", S0), ("grad_o", grad_o), ("grad_S_T", grad_S_T), *got.items()])
     _launch(dev, stream, load().ckda_gated_bwd, "ckda_gated_bwd",
             (_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S0), _ptr(grad_o), _ptr(grad_S_T), _ptr(got["dq"]),
@@ -321,11 +322,12 @@ def gated_decode_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None) -
     qs = _rows(q, "q", 1, None, dev)
     dt = q.dtype
     ks, vs = _rows(k, "k", 1, dt, dev), _rows(v, "v", 1, dt, dev)
-    N, Hk, dk = q.shape
-    Hv, dv = v.shape[1:]
-    if k.shape != q.shape:
-        raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(q.shape)}")
-    if v.shape[0] != N:
+    shape = q.shape
+    N, Hk, dk = shape
+    rows, Hv, dv = v.shape
+    if k.shape != shape:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(shape)}")
+    if rows != N:
         raise ValueError(f"v has shape {tuple(v.shape)}, expected {(N, Hv, dv)}")
     if Hk < 1 or Hv < 1 or Hv % Hk != 0:
         raise ValueError(f"v has {Hv} heads, not a multiple of the {Hk} of q and k")
@@ -342,7 +344,7 @@ def gated_decode_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None) -
     spans = [("q", q), ("k", k), ("v", v), ("g", g), ("beta", beta), ("slots", slots)]
     _apart(S, "S", spans)
     if o is None:
-        o = _empty((N, Hv, dv), dev, dt, stream)
+        o = _empty(v, (N, Hv, dv), stream)
     else:
         _check(o, "o", (N, Hv, dv), dt, dev)
         _apart(o, "o", spans + [("S", S)])
@@ -362,14 +364,15 @@ class _Prep:
         lead = q.dim() - 2
         self.qs = _rows(q, "q", lead, None, dev)
         self.dt = _dt(q)
-        self.tokens_shape = tuple(q.shape[:-2])
-        self.Hq, self.d = q.shape[-2:]
+        shape = q.shape
+        self.tokens_shape = shape[:-2]
+        self.Hq, self.d = shape[-2], shape[-1]
         self.Hk, self.ks = 0, 0
         if k is not None:
             self.ks = _rows(k, "k", lead, q.dtype, dev)
-            if tuple(k.shape[:-2]) != self.tokens_shape or k.shape[-1] != self.d:
-                raise ValueError(f"k has shape {tuple(k.shape)}, expected {self.tokens_shape + (k.shape[-2], self.d)}")
             self.Hk = k.shape[-2]
+            if k.shape != self.tokens_shape + (self.Hk, self.d):
+                raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(self.tokens_shape) + (self.Hk, self.d)}")
         tokens = prod(self.tokens_shape)
         if tokens > 0x7fffffff:
             raise ValueError("more than 2**31 - 1 tokens")
@@ -401,12 +404,11 @@ class _Prep:
         self.sizes = (tokens, max(1, self.tokens_shape[-1]), self.Hq, self.Hk, self.d, rotary, self.qs, self.ks, self.dt,
                       NORMS[norm], LAYOUTS[layout], float(eps), float(q_scale), float(rope_scale))
 
-    def out(self, t, name, heads, dtype, others, stream):
-        """An output of `heads` heads, allocated or checked."""
-        shape = self.tokens_shape + (heads, self.d)
+    def out(self, t, name, like, others, stream):
+        """An output of like's shape and type, allocated or checked to share memory with none of `others`."""
         if t is None:
-            return _empty(shape, self.dev, dtype, stream)
-        _check(t, name, shape, dtype, self.dev)
+            return torch.empty_like(like) if stream is None and like.is_contiguous() else _empty(like, like.shape, stream)
+        _check(t, name, like.shape, like.dtype, self.dev)
         _apart(t, name, others)
         return t
 
@@ -420,15 +422,18 @@ def qk_norm_rope(q, k=None, *, positions=None, inv_freq=None, norm="l2", layout=
     tokens' shape, None: the index along the last token dimension. Returns (q_out, k_out), which may
     be q and k themselves where those are contiguous (k_out None without k)."""
     p = _Prep(q, k, positions, inv_freq, norm, layout, q_weight, k_weight, eps, q_scale, rope_scale)
+
     def others(t, src, own):
-        same = t is not None and src.is_contiguous() and t.data_ptr() == src.data_ptr()
+        if t is None:
+            return ()
+        same = src.is_contiguous() and t.data_ptr() == src.data_ptr()
         return [x for x in p.spans if not (same and x[0] == own)]
 
-    q_out = p.out(q_out, "q_out", p.Hq, q.dtype, others(q_out, q, "q"), stream)
+    q_out = p.out(q_out, "q_out", q, others(q_out, q, "q"), stream)
     if k is None:
         k_out = None
     else:
-        k_out = p.out(k_out, "k_out", p.Hk, k.dtype, others(k_out, k, "k") + [("q_out", q_out)], stream)
+        k_out = p.out(k_out, "k_out", k, [*others(k_out, k, "k"), ("q_out", q_out)], stream)
     _launch(p.dev, stream, load().ckda_qk_prep, "ckda_qk_prep",
             (_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), *p.ptrs, *p.sizes))
     return q_out, k_out
@@ -447,9 +452,9 @@ def qk_norm_rope_bwd(q, k, grad_q, grad_k=None, *, positions=None, inv_freq=None
         _check(grad_k, "grad_k", p.tokens_shape + (p.Hk, p.d), q.dtype, p.dev)
     got = _given(grads, ("dq", "dk", "dq_weight", "dk_weight"))
     spans = p.spans + [("grad_q", grad_q), ("grad_k", grad_k)]
-    got["dq"] = p.out(got.get("dq"), "dq", p.Hq, q.dtype, spans, stream)
+    got["dq"] = p.out(got.get("dq"), "dq", q, spans, stream)
     spans.append(("dq", got["dq"]))
-    got["dk"] = p.out(got.get("dk"), "dk", p.Hk, k.dtype, spans, stream) if k is not None else None
+    got["dk"] = p.out(got.get("dk"), "dk", k, spans, stream) if k is not None else None
     spans.append(("dk", got["dk"]))
     weights = False
     for name, w in (("dq_weight", q_weight), ("dk_weight", k_weight)):
@@ -458,14 +463,14 @@ def qk_norm_rope_bwd(q, k, grad_q, grad_k=None, *, positions=None, inv_freq=None
             continue
         weights = True
         if got.get(name) is None:
-            got[name] = _empty(p.d, p.dev, F32, stream)
+            got[name] = _empty(w, (p.d,), stream)
         else:
             _check(got[name], name, (p.d,), F32, p.dev)
             _apart(got[name], name, spans)
         spans.append((name, got[name]))
     wbytes = 0
     if weights or workspace is not None:
-        workspace, wbytes = _workspace("ckda_qk_prep_bwd_workspace_bytes", p.dev, (p.d,), workspace, stream, spans)
+        workspace, wbytes = _workspace("ckda_qk_prep_bwd_workspace_bytes", p.dev, (p.d,), workspace, stream, q, spans)
     _launch(p.dev, stream, load().ckda_qk_prep_bwd, "ckda_qk_prep_bwd",
             (_ptr(q), _ptr(k), _ptr(grad_q), _ptr(grad_k), _ptr(got["dq"]), _ptr(got["dk"]), _ptr(got["dq_weight"]),
              _ptr(got["dk_weight"]), *p.ptrs, *p.sizes, _ptr(workspace), wbytes))
