@@ -19,7 +19,7 @@
 //
 // Measured, 8 x 16 sequences of 4096 tokens: 284 us, 4.4 us a chunk (7500 cycles) of which the
 // products are 2000, the tensor pipe 28% busy; with the states, W and U for the backward pass
-// 480 us. A chunk's tiles brought to L2 ahead gain 1%: memory is not what it waits for.
+// 376 us (480 while the out warps, which sum <dO, o>, held the whole stage). A chunk's tiles brought to L2 ahead gain 1%: memory is not what it waits for.
 //
 // What hides what: the output's products (P U), its epilogue and its store run under the next
 // chunk's state split; loads run a chunk ahead. A product of N = 64 takes as long as one of
@@ -113,7 +113,7 @@ __device__ __forceinline__ bool elected() {
 // as dS -> M^T dS + N' on the same maps: its pass kSegMaps builds every N' (the last from dS_T),
 // segment_scan_kernel chains them, and its pass kSegRun runs. Segment j of
 // sequence n has place start / (cps C) + n + j of its own, as chunks have. 65536 tokens of 16
-// heads: maps 0.60 ms, prefix 0.02, run 0.69, against 4.2 whole.
+// heads: maps 0.60 ms, scan 0.01, run 0.69, against 4.2 whole.
 enum { kSegWhole = 0, kSegMaps = 1, kSegRun = 2 };
 struct SegArgs {
     int mode, cps;
@@ -804,8 +804,8 @@ segment_result_kernel(SegArgs sg, Seqs seqs, const float* __restrict__ places, b
 // chunk. The layout and roles of the forward chain; the out warps prepare the operand e^G dO and
 // take y from TMEM for dV and the sums. The products that do not wait for dS (P^T dO, Q^T dO)
 // run under the epilogues; the operands of the update carry three terms. Measured as the forward
-// chain: 557 us; the same chain of latencies, with a third term in two operands, and 1.9 GB of
-// states and sums to move (47% of the bandwidth).
+// chain: 565 us; the out warps' operand, rows and sums over lanes take all of a chunk's 16000
+// cycles, and 1.9 GB of states and sums are moved (47% of the bandwidth).
 template <int DK>
 __global__ void __launch_bounds__(kChainThreads, 1)
 chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
