@@ -81,6 +81,23 @@ cudaError_t kernel_ready(K kernel, size_t bytes, int regs = 0) {
     return e;
 }
 
+// A launch; `close`: it may begin before the kernel ahead of it in the stream has ended (see
+// previous_done).
+template <typename... P, typename... A>
+cudaError_t launch_kernel(bool close, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, A&&... a) {
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t how{};
+    how.gridDim = grid;
+    how.blockDim = dim3(threads);
+    how.dynamicSmemBytes = smem;
+    how.stream = st;
+    how.attrs = &early;
+    how.numAttrs = close ? 1 : 0;
+    return cudaLaunchKernelEx(&how, kernel, static_cast<P>(a)...);
+}
+
 struct Shape {
     int N, T, total, Hk, Hv, dk, dv;
     ckda_dtype_t dt;
@@ -288,13 +305,17 @@ cudaError_t run_intra(const Call& c, const Maps& m, const ChainIn& in) {
     return cudaPeekAtLastError();
 }
 
+// Short calls, whose kernels are about as long as the gaps between them, are launched closely: up to two
+// chunks an SM. 2777 tokens of 4 heads back 169 us apart and 154 so, 512 of 4 forward 50 and 46; 1024
+// of 16 as long; 8 x 4096 of 16 436 and 448, the chains' blocks lying where others ended first.
+bool close(const Shape& s) { return (long long)Seqs::slots(s.N, s.total) * s.Hv <= 2LL * sm_count(); }
+
 template <bool kSuffix>
 cudaError_t run_scan(const Call& c, const SegArgs& sg) {
     cudaError_t e = kernel_ready(segment_scan_kernel<kSuffix>, kScanSmem);
     if (e != cudaSuccess) return e;
-    segment_scan_kernel<kSuffix><<<dim3((unsigned)(c.s.N * c.s.Hv), (unsigned)((c.s.dv + 15) / 16)), 256, kScanSmem, c.st>>>(
-        sg, c.seqs, c.s.Hv, c.s.dk, c.s.dv);
-    return cudaPeekAtLastError();
+    return launch_kernel(close(c.s), segment_scan_kernel<kSuffix>, dim3((unsigned)(c.s.N * c.s.Hv), (unsigned)((c.s.dv + 15) / 16)), 256, kScanSmem, c.st,
+                        sg, c.seqs, c.s.Hv, c.s.dk, c.s.dv);
 }
 
 template <int DK, bool kBack>
@@ -306,9 +327,8 @@ cudaError_t run_chain_fwd(const Call& c, const Maps& m, const ChainIn& in) {
     SegArgs sg = c.seg;
     const unsigned seqs = (unsigned)(c.s.N * c.s.Hv);
     auto run = [&](unsigned grid) {
-        chain_fwd_kernel<DK, kBack><<<grid, kChainThreads, smem, c.st>>>(m.q, m.k, m.v, m.o, in, c.S0, c.o, c.ST, c.ws, c.seqs, sg, c.s.Hk,
-                                                                        c.s.Hv, c.s.dk, c.s.dv);
-        return cudaPeekAtLastError();
+        return launch_kernel(close(c.s), chain_fwd_kernel<DK, kBack>, grid, kChainThreads, smem, c.st, m.q, m.k, m.v, m.o, in, c.S0, c.o, c.ST, c.ws,
+                            c.seqs, sg, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
     };
     if (sg.cps == 0) return run(seqs);
     const unsigned places = (unsigned)(SegArgs::places(c.s.N, c.s.total, sg.cps) * c.s.Hv);
@@ -316,17 +336,15 @@ cudaError_t run_chain_fwd(const Call& c, const Maps& m, const ChainIn& in) {
     e = kernel_ready(chain_fwd_kernel<DK, false>, maps_smem, kRegLaunch);
     if (e != cudaSuccess) return e;
     sg.mode = kSegMaps;
-    chain_fwd_kernel<DK, false><<<dim3(places, 2), kChainThreads, maps_smem, c.st>>>(
-        m.q, m.k, m.v, m.o, in, c.S0, c.o, c.ST, c.ws, c.seqs, sg, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
-    e = cudaPeekAtLastError();
+    e = launch_kernel(close(c.s), chain_fwd_kernel<DK, false>, dim3(places, 2), kChainThreads, maps_smem, c.st, m.q, m.k, m.v, m.o, in, c.S0, c.o, c.ST,
+                     c.ws, c.seqs, sg, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
     if (e == cudaSuccess) e = run_scan<false>(c, sg);
     if (e != cudaSuccess) return e;
     sg.mode = kSegRun;
     sg.apart = c.ST != nullptr && c.ST == c.S0;
     e = run(places);
     if (e != cudaSuccess || !sg.apart) return e;
-    segment_result_kernel<<<seqs, 256, 0, c.st>>>(sg, c.seqs, sg.states, false, c.ST, c.s.Hv, c.s.dk * c.s.dv);
-    return cudaPeekAtLastError();
+    return launch_kernel(close(c.s), segment_result_kernel, seqs, 256, 0, c.st, sg, c.seqs, sg.states, false, c.ST, c.s.Hv, c.s.dk * c.s.dv);
 }
 template <int DK>
 cudaError_t run_chain_bwd(const Call& c, const Maps& m, const ChainIn& in) {
@@ -336,9 +354,8 @@ cudaError_t run_chain_bwd(const Call& c, const Maps& m, const ChainIn& in) {
     SegArgs sg = c.seg;
     const unsigned seqs = (unsigned)(c.s.N * c.s.Hv);
     auto run = [&](unsigned grid) {
-        chain_bwd_kernel<DK><<<grid, kChainThreads, smem, c.st>>>(m.q, m.k, m.v, m.o, in, c.dST, c.gv, c.gS0, c.ws, c.seqs, sg, c.s.Hk, c.s.Hv,
-                                                                  c.s.dk, c.s.dv);
-        return cudaPeekAtLastError();
+        return launch_kernel(close(c.s), chain_bwd_kernel<DK>, grid, kChainThreads, smem, c.st, m.q, m.k, m.v, m.o, in, c.dST, c.gv, c.gS0, c.ws, c.seqs,
+                            sg, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
     };
     if (sg.cps == 0) return run(seqs);
     const unsigned places = (unsigned)(SegArgs::places(c.s.N, c.s.total, sg.cps) * c.s.Hv);
@@ -351,8 +368,7 @@ cudaError_t run_chain_bwd(const Call& c, const Maps& m, const ChainIn& in) {
     sg.apart = c.gS0 != nullptr && c.gS0 == c.dST;
     e = run(places);
     if (e != cudaSuccess || !sg.apart) return e;
-    segment_result_kernel<<<seqs, 256, 0, c.st>>>(sg, c.seqs, sg.dstates, true, c.gS0, c.s.Hv, c.s.dk * c.s.dv);
-    return cudaPeekAtLastError();
+    return launch_kernel(close(c.s), segment_result_kernel, seqs, 256, 0, c.st, sg, c.seqs, sg.dstates, true, c.gS0, c.s.Hv, c.s.dk * c.s.dv);
 }
 template <int DK, int DV>
 cudaError_t run_grads(const Call& c, const Maps& m, const ChainIn& in) {
@@ -364,9 +380,8 @@ cudaError_t run_grads(const Call& c, const Maps& m, const ChainIn& in) {
     if (in.maps && !(rows_map(&gv, c.gv, c.s.total, c.s.Hv, c.s.dv, (long long)c.s.Hv * c.s.dv) &&
                      rows_map(&u, c.ws.u, slots * c.s.Hv * C, 1, c.s.dv, c.s.dv)))
         return cudaErrorInvalidValue;
-    grad_kernel<DK, DV><<<(unsigned)std::min<long long>(items, sm_count()), 256, smem, c.st>>>(
-        m.q, m.k, m.o, gv, u, in, c.gv, c.gq, c.gk, c.gg, c.gb, c.ws, c.seqs, (int)slots, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
-    return cudaPeekAtLastError();
+    return launch_kernel(close(c.s), grad_kernel<DK, DV>, (unsigned)std::min<long long>(items, sm_count()), 256, smem, c.st, m.q, m.k, m.o, gv, u, in, c.gv,
+                        c.gq, c.gk, c.gg, c.gb, c.ws, c.seqs, (int)slots, c.s.Hk, c.s.Hv, c.s.dk, c.s.dv);
 }
 
 template <int DK, bool kBack>

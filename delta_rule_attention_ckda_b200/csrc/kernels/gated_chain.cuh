@@ -370,6 +370,7 @@ __device__ __forceinline__ void chain_begin(ChainBars& b, unsigned char* stages,
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
+    previous_done();
 }
 __device__ __forceinline__ void chain_end(ChainBars& b) {
     tc::tc_fence_before();
@@ -388,6 +389,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                  ChunkWs ws, Seqs seqs, SegArgs sg, int Hk, int Hv, int dk, int dv) {
     using L = ChainStage<DK, kBack>;
     constexpr int H = DK / 2;                  // channels of an epilogue thread
+    next_may_start();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ ChainBars bars;
@@ -407,9 +409,8 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     bool last = true;
     if (sg.mode) {                             // this segment's chunks, as a sequence of their own
         const int j = place - sg.first_place(n, start), skip = j * sg.cps;
-        if (j < 0 || (j > 0 && (long long)skip * C >= len)) return;
         last = (long long)(skip + sg.cps) * C >= len;
-        if (maps && (last || (transition && j == 0))) return;
+        if (j < 0 || (j > 0 && (long long)skip * C >= len) || (maps && (last || (transition && j == 0)))) return previous_done();
         const size_t own = (size_t)place * Hv + h;
         if (maps) {
             if (j > 0) from = nullptr;
@@ -730,6 +731,8 @@ segment_scan_kernel(SegArgs sg, Seqs seqs, int Hv, int dk, int dv) {
     const int first = sg.first_place(n, start), count = (len + sg.cps * C - 1) / (sg.cps * C);
     const size_t mat = (size_t)dk * dv;
     float* places = kSuffix ? sg.dstates : sg.states;
+    next_may_start();
+    previous_done();
     auto own = [&](int step) { return (size_t)(first + (kSuffix ? count - 1 - step : step)) * Hv + h; };
     auto fetch = [&](int step) {
         const float* from = sg.maps + own(step) * dk * dk;
@@ -792,6 +795,7 @@ segment_result_kernel(SegArgs sg, Seqs seqs, const float* __restrict__ places, b
     bool ok;
     seqs.get(n, start, len, ok);
     const int place = sg.first_place(n, start) + (first ? 0 : max((len + sg.cps * C - 1) / (sg.cps * C) - 1, 0));
+    previous_done();
     const float4* from = reinterpret_cast<const float4*>(places + ((size_t)place * Hv + h) * mat);
     float4* to = reinterpret_cast<float4*>(result + (size_t)blockIdx.x * mat);
     for (int i = threadIdx.x; i < mat / 4; i += 256) to[i] = from[i];
@@ -813,6 +817,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                  float* grad_S0, ChunkWs ws, Seqs seqs, SegArgs sg, int Hk, int Hv, int dk, int dv) {
     using L = ChainStage<DK, true>;
     constexpr int H = DK / 2;
+    next_may_start();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ ChainBars bars;
@@ -830,7 +835,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     float* to = grad_S0 == nullptr ? nullptr : grad_S0 + sbase;        // where that of the entering state goes
     if (sg.mode) {                             // this segment's chunks, as a sequence of their own
         const int j = place - sg.first_place(n, start), skip = j * sg.cps;
-        if (j < 0 || (j > 0 && (long long)skip * C >= len) || (maps && j == 0)) return;
+        if (j < 0 || (j > 0 && (long long)skip * C >= len) || (maps && j == 0)) return previous_done();
         const bool last = (long long)(skip + sg.cps) * C >= len;
         const size_t own = (size_t)place * Hv + h;
         if (!last) from = maps ? nullptr : sg.dstates + (own + Hv) * mat;

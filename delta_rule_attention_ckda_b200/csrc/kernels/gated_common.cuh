@@ -29,6 +29,13 @@ template <typename T> __device__ __forceinline__ T from_f32(float x);
 template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// Kernels of one short call follow one another closely: each lets the next begin once all its own blocks
+// run (what the next sets up then runs beside the last of them), and waits for the one before
+// it, complete and visible, ahead of anything that one wrote. Every block waits, also one without
+// work: a kernel has ended only when the one before it has.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void previous_done() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The sequences of a call. Dense (cu == nullptr): N sequences of T tokens, one after the
 // other. Packed: sequence n is tokens cu[n] .. cu[n+1] - 1 of `total`.
 struct Seqs {

@@ -163,6 +163,7 @@ grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
     }
     for (int i = tid; i < (L::BYTES - 1024) / 16; i += 256) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
+    previous_done();
     const uint32_t ln = swz_lane(true), lk = swz_lane(false);           // as ofs_n / ofs_at, as ofs_k / ofs_a
     // rows of a state tile as the right operand's k: this lane's row and group of channels
     const uint32_t ls = (uint32_t)(((lane & 7) + ((lane >> 3) & 1) * 8) * 16 + ((lane >> 4) & 1) * dv * 16);

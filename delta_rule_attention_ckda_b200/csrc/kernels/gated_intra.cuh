@@ -73,6 +73,7 @@ intra_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full;
+    next_may_start();
     const int slot = blockIdx.x, hk = blockIdx.y, rep = Hv / Hk, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int n = seqs.find(slot);
     int start, len;
