@@ -400,7 +400,6 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
     int start, len;
     bool ok;
     seqs.get(n, start, len, ok);
-    if (!ok && h == 0 && threadIdx.x == 0) report_index_error();
     int slot0 = seqs.first_slot(n, start);
     const int strips = (dv + 31) / 32;
     const size_t mat = (size_t)dk * dv, sbase = ((size_t)n * Hv + h) * mat;

@@ -78,6 +78,11 @@ intra_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
     const int n = seqs.find(slot);
     int start, len;
     bool ok;
+    if (slot == 0 && hk == 0 && seqs.cu != nullptr)                    // every sequence's offsets: out of order, find() may not meet them all
+        for (int m = tid; m < seqs.N; m += 128) {
+            seqs.get(m, start, len, ok);
+            if (!ok) report_index_error();
+        }
     seqs.get(n, start, len, ok);
     const int c = slot - seqs.first_slot(n, start);
     if (c < 0 || (long long)c * C >= len) return;

@@ -255,6 +255,23 @@ def test_bad_offsets_are_reported(ck):
     fine(ck)
 
 
+@pytest.mark.parametrize("total,offsets", [
+    (6000, [0, 3000, 7000]), (6000, [0, 6000, 0, 6000]), (6000, [5999, -1, 6001, 0]),                    # in segments
+    (500, [(37 * i) % 620 - 60 for i in range(161)]),                                                    # more than SMs: ranked
+], ids=["beyond", "again", "backwards", "ranked"])
+def test_bad_offsets_of_long_and_many(ck, total, offsets):
+    N = len(offsets) - 1
+    q, k, v, g, b, S0, do, dST = dev(*make((total,), 1, 1, 64, 64, BF, 2, N))
+    cu = torch.tensor(offsets, dtype=torch.int32).cuda()
+    o = torch.full((total + 64, 1, 64), 7.0, dtype=BF, device="cuda")
+    ck.gated_chunk_fwd(q, k, v, g, b, S0, cu_seqlens=cu, o=o[:total])
+    assert ck.get_device_error() == 7
+    assert (o[total:] == 7.0).all()
+    ck.gated_bwd(q, k, v, g, b, do, S0, dST, cu_seqlens=cu)
+    assert ck.get_device_error() == 7
+    fine(ck)
+
+
 # ------------------------------------------------------------------- single tokens
 
 @pytest.mark.parametrize("case", [(1, 1, 1, 1, 128, 128, BF), (3, 7, 2, 4, 128, 128, BF), (40, 40, 4, 8, 64, 64, BF),
