@@ -215,7 +215,7 @@ int segment_chunks(const Shape& s, bool back) {
 }
 
 struct ChunkLayout {
-    size_t zhi, zlo, phi, plo, vec, shi, slo, dshi, u, w, parts, states, maps, dstates, total;
+    size_t zhi, zlo, phi, plo, vec, shi, slo, dshi, u, d, parts, states, maps, dstates, total;
     int cps;
 };
 ChunkLayout chunk_layout(const Shape& s, bool back) {
@@ -237,7 +237,7 @@ ChunkLayout chunk_layout(const Shape& s, bool back) {
         l.slo = take((size_t)s.dk * s.dv * 2);
         l.dshi = take((size_t)s.dk * s.dv * 2);
         l.u = take((size_t)64 * s.dv * 2);
-        l.w = take((size_t)s.dv * 64 * 4);
+        l.d = take((size_t)s.dv * 64 * 4);
         l.parts = take(strips * PARTS * 4);
     }
     l.cps = segment_chunks(s, back);
@@ -255,7 +255,7 @@ ChunkWs chunk_ws(const ChunkLayout& l, void* base) {
     char* b = static_cast<char*>(base);
     auto H = [&](size_t at) { return reinterpret_cast<bf16*>(b + at); };
     auto F = [&](size_t at) { return reinterpret_cast<float*>(b + at); };
-    return ChunkWs{H(l.zhi), H(l.zlo), H(l.phi), H(l.plo), F(l.vec), H(l.shi), H(l.slo), H(l.dshi), H(l.u), F(l.w), F(l.parts)};
+    return ChunkWs{H(l.zhi), H(l.zlo), H(l.phi), H(l.plo), F(l.vec), H(l.shi), H(l.slo), H(l.dshi), H(l.u), F(l.d), F(l.parts)};
 }
 
 SegArgs segments(const ChunkLayout& l, void* base, const Shape& s, bool packed) {
@@ -295,13 +295,13 @@ struct Maps {
     CUtensorMap q, k, v, o;
 };
 
-template <int DK>
+template <int DK, bool kBack>
 cudaError_t run_intra(const Call& c, const Maps& m, const ChainIn& in) {
     constexpr size_t smem = intra_smem(DK);
     cudaError_t e = kernel_ready(intra_kernel<DK>, smem);
     if (e != cudaSuccess) return e;
     intra_kernel<DK><<<dim3((unsigned)Seqs::slots(c.s.N, c.s.total), (unsigned)c.s.Hk), 128, smem, c.st>>>(
-        m.q, m.k, in, c.g, c.beta, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk);
+        m.q, m.k, in, c.g, c.beta, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, kBack);
     return cudaPeekAtLastError();
 }
 
@@ -394,7 +394,7 @@ cudaError_t run_chunked(const Call& c) {
                         (!kBack || rows_map(&m.o, c.grad_o, c.s.total, c.s.Hv, c.s.dv, (long long)c.s.Hv * c.s.dv));
         if (!ok) return cudaErrorInvalidValue;
     }
-    cudaError_t e = run_intra<DK>(c, m, in);
+    cudaError_t e = run_intra<DK, kBack>(c, m, in);
     if (e == cudaSuccess) e = run_chain_fwd<DK, kBack>(c, m, in);
     if constexpr (kBack) {
         if (e == cudaSuccess) e = run_chain_bwd<DK>(c, m, in);

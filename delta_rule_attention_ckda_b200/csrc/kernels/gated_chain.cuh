@@ -195,7 +195,7 @@ __device__ __forceinline__ void chain_load(uint32_t st, uint64_t* full, int x, c
             cp16(to + L::P, ws.phi + from, true);
             cp16(to + L::P + 8192, ws.plo + from, true);
         }
-    if (x < 48) cp16(st + L::VECS + x * 16, ws.vec + wh * VEC + x * 4, true);
+    if (x < (kDO ? 64 : 48)) cp16(st + L::VECS + x * 16, ws.vec + wh * VEC + x * 4, true);
     if (!tiles) {
         const __nv_bfloat16 *q = in.q + tok * in.qs + (size_t)hk * dk, *k = in.k + tok * in.ks + (size_t)hk * dk,
                             *v = in.v + tok * in.vs + (size_t)h * dv, *dO = kDO ? in.dO + ((size_t)tok * Hv + h) * dv : nullptr;
@@ -565,7 +565,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     for (int i = 0; i < 32; ++i) t[i] = r[32 * half + i] * tile_value(st + L::DO, 32 * half + i, row);
                     const float sum = lane_sums(t);
                     if (quarter < strips)
-                        ws.parts[(((size_t)(slot0 + c) * Hv + h) * strips + quarter) * PARTS + PART_DOO + 32 * half + lane] = sum;
+                        ws.parts[(((size_t)(slot0 + c) * Hv + h) * strips + quarter) * PARTS + PART_PAST + 32 * half + lane] = sum;
                 } else {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -612,7 +612,7 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 }
             }
             if (c == chunks) break;
-            // X = V - e^G K S, and beta X as an operand
+            // X = V - e^G K S, and beta X as an operand; x holds X, with kBack e^G K S
             const unsigned char* st = sm + (c & 1) * L::BYTES;
             const float* vec = reinterpret_cast<const float*>(st + L::VECS) + 32 * wg;
             float x[32], y[32];
@@ -632,7 +632,12 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 const float4 eg = *reinterpret_cast<const float4*>(vec + VEC_EG + i), bt = *reinterpret_cast<const float4*>(vec + VEC_BETA + i);
                 fma2(y[i], y[i + 1], x[i], x[i + 1], -eg.x, -eg.y);
                 fma2(y[i + 2], y[i + 3], x[i + 2], x[i + 3], -eg.z, -eg.w);
-                x[i] = y[i]; x[i + 1] = y[i + 1]; x[i + 2] = y[i + 2]; x[i + 3] = y[i + 3];
+                if constexpr (kBack) {
+                    mul2(x[i], x[i + 1], eg.x, eg.y);
+                    mul2(x[i + 2], x[i + 3], eg.z, eg.w);
+                } else {
+                    x[i] = y[i]; x[i + 1] = y[i + 1]; x[i + 2] = y[i + 2]; x[i + 3] = y[i + 3];
+                }
                 mul2(y[i], y[i + 1], bt.x, bt.y);
                 mul2(y[i + 2], y[i + 3], bt.z, bt.w);
             }
@@ -643,25 +648,33 @@ chain_fwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             tc::tmem_st_wait();
             tc::tc_fence_before();
             tc::mbar_arrive(&bars.x);
-            // W, U; the operands U' = e^{G_C - G} U and U
+            // W, U; the operands U' = e^{G_C - G} U and U. For the backward pass d = V - W is formed first, from
+            // what it consists of: it falls with the decay, and a difference of V and W would keep V's rounding.
             chain_wait(bars, &bars.m2, c & 1);
             tc::tc_fence_after();
-            {
-                tc::tmem_ld32<32>(tl + TM_UZ + 32 * wg, y);
+#pragma unroll
+            for (int k = 0; k < 128; k += 64) {
+                tc::tmem_ld32<32>(tl + TM_UZ + k + 32 * wg, y);
                 tc::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) add2(x[i], x[i + 1], y[i], y[i + 1]);
-                tc::tmem_ld32<32>(tl + TM_UZ + 64 + 32 * wg, y);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) add2(x[i], x[i + 1], y[i], y[i + 1]);
+                for (int i = 0; i < 32; i += 2) {
+                    if constexpr (kBack) fma2(x[i], x[i + 1], y[i], y[i + 1], -1.f, -1.f);
+                    else add2(x[i], x[i + 1], y[i], y[i + 1]);
+                }
             }
             const size_t wh = (size_t)(slot0 + c) * Hv + h;
             if constexpr (kBack) {
                 if (live) {
-                    float4* wp = reinterpret_cast<float4*>(ws.w + wh * 64 * dv) + (size_t)(8 * wg) * dv + row;
+                    float4* dp = reinterpret_cast<float4*>(ws.d + wh * 64 * dv) + (size_t)(8 * wg) * dv + row;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) wp[i * dv] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    for (int i = 0; i < 8; ++i) dp[i * dv] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    float w0 = tile_value(st + L::V, 32 * wg + i, row), w1 = tile_value(st + L::V, 32 * wg + i + 1, row);
+                    fma2(w0, w1, x[i], x[i + 1], -1.f, -1.f);
+                    x[i] = w0;
+                    x[i + 1] = w1;
                 }
             }
 #pragma unroll
@@ -803,8 +816,9 @@ segment_result_kernel(SegArgs sg, Seqs seqs, const float* __restrict__ places, b
 // The adjoint chain, chunks last to first, dS the cotangent of the state leaving a chunk:
 //   dU = P^T dO + e^{G_C - G} (.) K dS,   y = dU + Z^T (beta dU),   dV = beta y
 //   dS <- e^{G_C} dS + Q^T (e^G (.) dO) - K^T (e^G (.) dV)
-// and the sums that the gradients of beta and g need: w.y and dV.v per token, <S', dS> per
-// chunk. The layout and roles of the forward chain; the out warps prepare the operand e^G dO and
+// and the sums that the gradients of beta and g need (see gated_grads.cuh): w.y and what a token's
+// future takes from it, <S', dS> per chunk. P comes without its diagonal, whose part of dU and y,
+// q_i.k_i dO_i, is added where the whole is needed. The layout and roles of the forward chain; the out warps prepare the operand e^G dO and
 // take y from TMEM for dV and the sums. The products that do not wait for dS (P^T dO, Q^T dO)
 // run under the epilogues; the operands of the update carry three terms. Measured as the forward
 // chain: 565 us; the out warps' operand, rows and sums over lanes take all of a chunk's 16000
@@ -859,7 +873,7 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     const size_t wh = (size_t)(slot0 + c) * Hv + h;
                     tc::prefetch_l2_bulk(ws.shi + (wh + (it ? 0 : Hv)) * mat, (uint32_t)(mat * 2));
                     tc::prefetch_l2_bulk(ws.slo + (wh + (it ? 0 : Hv)) * mat, (uint32_t)(mat * 2));
-                    tc::prefetch_l2_bulk(ws.w + wh * 64 * dv, (uint32_t)(64 * dv * 4));
+                    tc::prefetch_l2_bulk(ws.d + wh * 64 * dv, (uint32_t)(64 * dv * 4));
                 }
                 if (it >= 2) chain_wait(bars, &bars.empty[it & 1], ((it >> 1) - 1) & 1);
                 chain_load<L, DK, true>(base + (it & 1) * L::BYTES, &bars.full[it & 1], x, in, &mq, &mk, &mv, &mo, ws,
@@ -957,7 +971,13 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             for (int half = 0; half < 2; ++half) {
                 float e[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) e[i] = vec[VEC_EG + 32 * half + i] * tile_value(st + L::DO, 32 * half + i, row);
+                for (int i = 0; i < 32; i += 4) {
+                    const float4 eg = *reinterpret_cast<const float4*>(vec + VEC_EG + 32 * half + i);
+                    e[i] = eg.x * tile_value(st + L::DO, 32 * half + i, row);
+                    e[i + 1] = eg.y * tile_value(st + L::DO, 32 * half + i + 1, row);
+                    e[i + 2] = eg.z * tile_value(st + L::DO, 32 * half + i + 2, row);
+                    e[i + 3] = eg.w * tile_value(st + L::DO, 32 * half + i + 3, row);
+                }
                 const uint32_t to[3] = {tl + TM_ACC + 32 * half, tl + TM_ACC + 32 * half + 16, tl + TM_PU + 32 * half};
                 put_terms<3>(e, to);
             }
@@ -971,16 +991,16 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                 if (lane == 0) tc::mbar_arrive(&bars.empty[it & 1]);
                 continue;
             }
-            float w[32];
-            const float4* wp = reinterpret_cast<const float4*>(ws.w + wh * 64 * dv) + (live ? row : 0);
-            auto load_w = [&](int half) {
+            float d[32];
+            const float4* dp = reinterpret_cast<const float4*>(ws.d + wh * 64 * dv) + (live ? row : 0);
+            auto load_d = [&](int half) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float4 a = live ? wp[(size_t)(8 * half + i) * dv] : make_float4(0.f, 0.f, 0.f, 0.f);
-                    w[4 * i] = a.x; w[4 * i + 1] = a.y; w[4 * i + 2] = a.z; w[4 * i + 3] = a.w;
+                    const float4 a = live ? dp[(size_t)(8 * half + i) * dv] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    d[4 * i] = a.x; d[4 * i + 1] = a.y; d[4 * i + 2] = a.z; d[4 * i + 3] = a.w;
                 }
             };
-            load_w(0);
+            load_d(0);
             chain_wait(bars, &bars.u, it & 1);
             tc::tc_fence_after();
 #pragma unroll 1
@@ -992,19 +1012,27 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     tc::tc_fence_before();
                     tc::mbar_arrive(&bars.out);
                 }
+                // y arrives without the token's own dO; w = V - d
 #pragma unroll
-                for (int i = 0; i < 32; i += 2) mul2(w[i], w[i + 1], y[i], y[i + 1]);
-                const float db = lane_sums(w);
-                if (quarter < strips) part[PART_DB + 32 * half + lane] = db;
-                if (half == 0) load_w(1);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    y[i] *= vec[VEC_BETA + 32 * half + i];
-                    *reinterpret_cast<__nv_bfloat16*>(tile + (32 * half + i) * 256 + 2 * row) = __float2bfloat16_rn(y[i]);
-                    y[i] *= tile_value(st + L::V, 32 * half + i, row);
+                for (int i = 0; i < 32; i += 2) {
+                    const int t = 32 * half + i;
+                    const float2 b = *reinterpret_cast<const float2*>(vec + VEC_BETA + t), p = *reinterpret_cast<const float2*>(vec + VEC_PD + t);
+                    float w0 = tile_value(st + L::V, t, row), w1 = tile_value(st + L::V, t + 1, row), a0 = y[i], a1 = y[i + 1];
+                    fma2(w0, w1, d[i], d[i + 1], -1.f, -1.f);
+                    fma2(a0, a1, p.x, p.y, tile_value(st + L::DO, t, row), tile_value(st + L::DO, t + 1, row));
+                    *reinterpret_cast<__nv_bfloat16*>(tile + t * 256 + 2 * row) = __float2bfloat16_rn(b.x * a0);
+                    *reinterpret_cast<__nv_bfloat16*>(tile + (t + 1) * 256 + 2 * row) = __float2bfloat16_rn(b.y * a1);
+                    mul2(y[i], y[i + 1], w0, w1);
+                    fma2(y[i], y[i + 1], a0, a1, d[i], d[i + 1]);
+                    mul2(a0, a1, w0, w1);
+                    d[i] = a0;
+                    d[i + 1] = a1;
                 }
-                const float dvv = lane_sums(y);
-                if (quarter < strips) part[PART_DVV + 32 * half + lane] = dvv;
+                const float db = lane_sums(d);
+                if (quarter < strips) part[PART_DB + 32 * half + lane] = db;
+                if (half == 0) load_d(1);
+                const float future = vec[VEC_BETA + 32 * half + lane] * lane_sums(y);
+                if (quarter < strips) part[PART_FUTURE + 32 * half + lane] = future;
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars.empty[it & 1]);
@@ -1067,10 +1095,14 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
                     ws.parts[((((size_t)slot0 + max(c, 0)) * Hv + h) * strips + quarter) * PARTS + (it < chunks ? PART_SDS : PART_SDS0) + wg] = dot;
             }
             if (it == chunks) break;
-            // dU, and beta dU as an operand
+            // dU without the token's own dO (P here has no diagonal) in x, and beta dU as an operand
             const unsigned char* st = sm + (it & 1) * L::BYTES;
             const float* vec = reinterpret_cast<const float*>(st + L::VECS) + 32 * wg;
             float x[32], y[32];
+            auto add_own = [&](const unsigned char* stage, int i, float& z0, float& z1) {      // tokens i and i + 1
+                const float2 p = *reinterpret_cast<const float2*>(stage + L::VECS + 4 * (32 * wg + VEC_PD + i));
+                fma2(z0, z1, p.x, p.y, tile_value(stage + L::DO, 32 * wg + i, row), tile_value(stage + L::DO, 32 * wg + i + 1, row));
+            };
             chain_wait(bars, &bars.full[it & 1], (it >> 1) & 1);
             chain_wait(bars, &bars.m1, it & 1);
             tc::tc_fence_after();
@@ -1080,11 +1112,13 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
                 const float4 dc = *reinterpret_cast<const float4*>(vec + VEC_DEC + i), bt = *reinterpret_cast<const float4*>(vec + VEC_BETA + i);
-                x[i] = fmaf(dc.x, x[i], y[i]);
-                x[i + 1] = fmaf(dc.y, x[i + 1], y[i + 1]);
-                x[i + 2] = fmaf(dc.z, x[i + 2], y[i + 2]);
-                x[i + 3] = fmaf(dc.w, x[i + 3], y[i + 3]);
-                y[i] = bt.x * x[i]; y[i + 1] = bt.y * x[i + 1]; y[i + 2] = bt.z * x[i + 2]; y[i + 3] = bt.w * x[i + 3];
+                fma2(y[i], y[i + 1], dc.x, dc.y, x[i], x[i + 1]);
+                fma2(y[i + 2], y[i + 3], dc.z, dc.w, x[i + 2], x[i + 3]);
+                x[i] = y[i]; x[i + 1] = y[i + 1]; x[i + 2] = y[i + 2]; x[i + 3] = y[i + 3];
+                add_own(st, i, y[i], y[i + 1]);
+                add_own(st, i + 2, y[i + 2], y[i + 3]);
+                mul2(y[i], y[i + 1], bt.x, bt.y);
+                mul2(y[i + 2], y[i + 3], bt.z, bt.w);
             }
             {
                 const uint32_t to[2] = {tl + TM_X + 32 * wg, tl + TM_X + 32 * wg + 16};
@@ -1093,31 +1127,31 @@ chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__
             tc::tmem_st_wait();
             tc::tc_fence_before();
             tc::mbar_arrive(&bars.x);
-            // y (to TMEM for the out warps), and - e^G dV as an operand
+            // y without the token's own dO (to TMEM for the out warps), and - e^G dV as an operand
             chain_wait(bars, &bars.m2, it & 1);
             tc::tc_fence_after();
-            tc::tmem_ld32<32>(tl + TM_UZ + 32 * wg, y);
-            tc::tmem_ld_wait();
+            st = sm + fresh((it & 1) * L::BYTES);  // the own parts are read again: kept from above they would spill
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] += y[i];
-            tc::tmem_ld32<32>(tl + TM_UZ + 64 + 32 * wg, y);
-            tc::tmem_ld_wait();
-            {
-                uint32_t r[16];
+            for (int k = 0; k < 32; k += 8) {
+                float e[8], z[8];
+                uint32_t r[8];
+                tc::tmem_ld32<8>(tl + TM_UZ + 32 * wg + k, e);
+                tc::tmem_ld32<8>(tl + TM_UZ + 64 + 32 * wg + k, z);
+                tc::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; i += 16) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        x[i + j] += y[i + j];
-                        r[j] = __float_as_uint(x[i + j]);
-                    }
-                    tc::tmem_st32<16>(tl + TM_ACC + 64 + 32 * wg + i, r);
+                for (int i = 0; i < 8; ++i) {
+                    x[k + i] += e[i] + z[i];
+                    r[i] = __float_as_uint(x[k + i]);
                 }
-            }
+                tc::tmem_st32<8>(tl + TM_ACC + 64 + 32 * wg + k, r);
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-                const float4 bt = *reinterpret_cast<const float4*>(vec + VEC_BETA + i), eg = *reinterpret_cast<const float4*>(vec + VEC_EG + i);
-                x[i] *= -eg.x * bt.x; x[i + 1] *= -eg.y * bt.y; x[i + 2] *= -eg.z * bt.z; x[i + 3] *= -eg.w * bt.w;
+                for (int i = k; i < k + 8; i += 4) {
+                    const float4 bt = *reinterpret_cast<const float4*>(vec + VEC_BETA + i), eg = *reinterpret_cast<const float4*>(vec + VEC_EG + i);
+                    add_own(st, i, x[i], x[i + 1]);
+                    add_own(st, i + 2, x[i + 2], x[i + 3]);
+                    mul2(x[i], x[i + 1], -eg.x * bt.x, -eg.y * bt.y);
+                    mul2(x[i + 2], x[i + 3], -eg.z * bt.z, -eg.w * bt.w);
+                }
             }
             {
                 const uint32_t to[3] = {tl + TM_UZ + 32 * wg, tl + TM_UZ + 32 * wg + 16, tl + TM_UZ + 64 + 32 * wg};

@@ -7,9 +7,16 @@
 //   dbeta_t = <w_t, y_t>,   dg_t = sum_{i >= t} e_i + <S_C, dS_C>,   e_i = <dO_i, o_i> - <dV_i, v_i>
 // dg: scaling the state of one moment scales what every later term takes of it, so the later
 // terms' own products with their cotangents sum to the derivative by the log gate. The same
-// number counted from the chunk's start is <S_0, dS_0> - sum_{i < t} e_i; each e_i is off by its
-// products' rounding, so the two are weighted by the other's number of terms, (n - t) and t of n,
-// which cuts the error of the sum to a half of the one-sided one (1.04e-5 to 6e-6 of dg's norm).
+// number counted from the chunk's start is <S_0, dS_0> - sum_{i < t} e_i; each term is off by its
+// products' rounding, a like part of it, so the two are weighted by the squares of the other's terms. Where
+// terms are alike that cuts the error to a half of the one-sided one; a sequence's dS_T, which no gate has
+// damped yet, then has no say in gates that damp it.
+// In e_i a token's own update meets its own output, p_i dO_i.u_i with p_i = q_i.k_i, on both sides
+// and cancels: o_i = o'_i + p_i u_i, y_i = y'_i + p_i dO_i, v_i = w_i + d_i give
+//   e_i = <dO_i, o'_i> - beta_i (<y_i, d_i> + <w_i, y'_i>),
+// in which o' and d (what the past gives) and y' (what the future asks for) fall with the decay as dg
+// does. So the chains form those three without the own part, never as differences, and dg keeps its digits
+// under strong gates.
 //
 // dQ and dK are rounded to bf16 at the end, so their operands go in one bf16 term; dg and
 // dbeta come from the chains' fp32 sums. Memory-bound: per chunk and head 157 KB are read (states
@@ -195,7 +202,7 @@ grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
         // warp 0: the sums that dg and dbeta come from, in flight (two tokens a lane; lanes 0 .. 7 the
         // parts of <S, dS> at the chunk's end, 8 .. 15 those at its start: the end of the chunk before,
         // or SDS0)
-        float2 doo[4], dvv[4], wy[4];
+        float2 past[4], fut[4], wy[4];
         float edge = 0.f;
         if (warp == 0) {
             const float* part = ws.parts + u.wh * strips * PARTS;
@@ -204,8 +211,8 @@ grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             for (int i = 0; i < 4; ++i) {
                 const float2* p = reinterpret_cast<const float2*>(part + (size_t)i * PARTS) + lane;
                 const bool in = i < strips;
-                doo[i] = in ? p[PART_DOO / 2] : make_float2(0.f, 0.f);
-                dvv[i] = in ? p[PART_DVV / 2] : make_float2(0.f, 0.f);
+                past[i] = in ? p[PART_PAST / 2] : make_float2(0.f, 0.f);
+                fut[i] = in ? p[PART_FUTURE / 2] : make_float2(0.f, 0.f);
                 wy[i] = in ? p[PART_DB / 2] : make_float2(0.f, 0.f);
             }
             const int i = (lane & 7) / 2;
@@ -260,26 +267,32 @@ grad_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUte
             float a[2] = {0.f, 0.f}, e[2] = {0.f, 0.f}, db[2] = {0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                a[0] += doo[i].x; a[1] += doo[i].y;
-                e[0] += dvv[i].x; e[1] += dvv[i].y;
+                a[0] += past[i].x; a[1] += past[i].y;
+                e[0] += fut[i].x; e[1] += fut[i].y;
                 db[0] += wy[i].x; db[1] += wy[i].y;
             }
 #pragma unroll
             for (int off = 4; off > 0; off >>= 1) edge += __shfl_xor_sync(0xffffffffu, edge, off);
             const double end = __shfl_sync(0xffffffffu, edge, 0), begin = __shfl_sync(0xffffffffu, edge, 8);
             const double x[2] = {(double)a[0] - (double)e[0], (double)a[1] - (double)e[1]};
-            double sum = x[0] + x[1];          // of this lane's tokens and all later ones
+            const double s[2] = {(double)a[0] * a[0] + (double)e[0] * e[0], (double)a[1] * a[1] + (double)e[1] * e[1]};
+            double sum = x[0] + x[1], squares = s[0] + s[1];       // of this lane's tokens and all later ones
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const double y = __shfl_down_sync(0xffffffffu, sum, off);
-                if (lane + off < 32) sum += y;
+                const double y = __shfl_down_sync(0xffffffffu, sum, off), z = __shfl_down_sync(0xffffffffu, squares, off);
+                if (lane + off < 32) {
+                    sum += y;
+                    squares += z;
+                }
             }
             const double all = __shfl_sync(0xffffffffu, sum, 0), from[2] = {sum, sum - x[0]};
+            const double every = __shfl_sync(0xffffffffu, squares, 0), later[2] = {squares, squares - s[0]};
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = 2 * lane + i;
                 if (t < u.nt) {
-                    const double f = (double)t / u.nt;
+                    const double earlier = begin * begin + (every - later[i]), both = begin * begin + every + end * end;
+                    const double f = both > 0.0 ? earlier / both : 0.0;
                     grad_g[(u.tok + t) * Hv + h] = (float)(f * (from[i] + end) + (1.0 - f) * (begin - (all - from[i])));
                     grad_beta[(u.tok + t) * Hv + h] = db[i];
                 }

@@ -156,8 +156,9 @@ __device__ __forceinline__ uint32_t frag(uint32_t lane, int r0, int c0) {
 
 // ---------------------------------------------------------------- workspace of the chunked kernels
 
-// Per chunk and value head, floats: e^G, e^{G_C - G}, beta, then G in two parts (G = hi + lo).
-enum { VEC_EG = 0, VEC_DEC = 64, VEC_BETA = 128, VEC_GHI = 192, VEC_GLO = 256, VEC = 320 };
+// Per chunk and value head, floats: e^G, e^{G_C - G}, beta, P's diagonal q_i.k_i (backward only), then G in
+// two parts (G = hi + lo).
+enum { VEC_EG = 0, VEC_DEC = 64, VEC_BETA = 128, VEC_PD = 192, VEC_GHI = 256, VEC_GLO = 320, VEC = 384 };
 
 // Per chunk slot and value head (each pointer is that of slot 0, head 0). What a thread per state
 // column reads and writes lies with its columns side by side, 16 bytes each: states as
@@ -168,12 +169,12 @@ struct ChunkWs {
     __nv_bfloat16 *shi, *slo;                  // backward: entering state, [dk / 8][dv][8] (see put_state)
     __nv_bfloat16* dshi;                       // backward: cotangent of the leaving state, [dk / 8][dv][8]
     __nv_bfloat16* u;                          // backward: updates [64][dv]
-    float* w;                                  // backward: w, [16][dv][4]
+    float* d;                                  // backward: v - w, [16][dv][4]
     float* parts;                              // backward: [dv / 32][PARTS] sums over 32 columns (SDS: two halves)
 };
-// DOO <dO, o>, DVV <dV, v>, DB <w, y> per token; SDS <S', dS> of the leaving state, SDS0 (a
-// sequence's first chunk) of the entering one
-enum { PART_DOO = 0, PART_DVV = 64, PART_DB = 128, PART_SDS = 192, PART_SDS0 = 194, PARTS = 208 };
+// PAST <dO, o> without a token's own update, FUTURE what is taken from it (see gated_grads.cuh), DB <w, y> per
+// token; SDS <S', dS> of the leaving state, SDS0 (a sequence's first chunk) of the entering one
+enum { PART_PAST = 0, PART_FUTURE = 64, PART_DB = 128, PART_SDS = 192, PART_SDS0 = 194, PARTS = 208 };
 
 }  // namespace gated
 }  // namespace ckda

@@ -635,3 +635,29 @@ def test_empty(ck):
     e = torch.empty(0, dtype=torch.int32).cuda()
     assert ck.state_copy(S0, e, e) is S0
     fine(ck)
+
+
+# ------------------------------------------------------------------- gates that forget
+
+@pytest.mark.parametrize("dt,d", [(BF, 64), (BF, 128), (F32, 32)])
+@pytest.mark.parametrize("gate", [-0.5, -2.0, -5.0, -8.0, -12.0, -20.0, -40.0])
+def test_strong_gates(ck, gate, dt, d):
+    """Gates that all forget within a token or two: dg falls with e^g, and its digits have to stay.
+    fp32 and every other gradient: as everywhere. dg in chunks is a weighted sum of e_i, what token i
+    takes of its past minus what its future takes of it: a pair of tokens on one side of t cancels there, its
+    errors do not. The weights' squares sum to (64 - t) (t / 64)^2 + t (1 - t / 64)^2, 64 / 6 in the mean
+    over a chunk, 3.3 as a root; each e_i is of dg's own size and three products with two rounded operands each,
+    off by 2.7e-6 at RMS: 3.3 * 6^0.5 * 2.7e-6 = 2.2e-5 of the norm, and twice that is allowed."""
+    T = 300
+    q, k, v, g, b, S0, do, dST = make((1, T), 1, 2, d, d, dt, 5, 1)
+    g = gate * (0.5 + torch.rand(g.shape, generator=torch.Generator().manual_seed(9)))
+    got = ck.gated_bwd(*dev(q, k, v, g, b, do, S0, dST))
+    fine(ck)
+    want = ref.gated_bwd(q, k, v, g, b, do, S0, dST)
+    squares = dict(zip(("dq", "dk"), ref.grad_squares(q, k, v, g, b, do, S0, dST)))
+    for name in want:
+        if dt == BF and name == "dg":
+            err = float((got[name].double().cpu() - want[name]).norm())
+            assert err <= 4.4e-5 * float(want[name].norm()), (gate, err / float(want[name].norm()))
+        else:
+            near(name, got[name], want[name], squares.get(name))
