@@ -661,3 +661,16 @@ def test_strong_gates(ck, gate, dt, d):
             assert err <= 4.4e-5 * float(want[name].norm()), (gate, err / float(want[name].norm()))
         else:
             near(name, got[name], want[name], squares.get(name))
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("lens", [[1], [1, 1, 1, 1, 1], [1, 0, 64, 1, 65]], ids=str)
+def test_first_gate_without_a_state_has_no_gradient(ck, dt, lens):
+    """A sequence's first gate scales a state of zeros: its gradient is 0, not the rounding of sums that cancel."""
+    cu, total = packed(lens, 0)
+    q, k, v, g, b, _, do, _ = make((total,), 1, 2, 64, 128, dt, 7, len(lens), s0=False)
+    got = ck.gated_bwd(*dev(q, k, v, g, b, do), cu_seqlens=cu.cuda())
+    fine(ck)
+    first = [a for a, e in ref.bounds(cu) if e > a]
+    assert (got["dg"][first] == 0).all()
+    near_grads(got, q, k, v, g, b, do, cu=cu)
