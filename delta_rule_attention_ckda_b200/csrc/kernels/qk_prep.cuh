@@ -237,7 +237,10 @@ prep_vec_kernel(const PrepArgs a, int wpt) {
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) fma2(s0, s1, x[i], x[i + 1], x[i], x[i + 1]);
                     float coef;
-                    const float f = norm_factor(a, group_sum<G>(s0 + s1), coef);
+                    float f = norm_factor(a, group_sum<G>(s0 + s1), coef);
+                    // lanes behind the last head hold zeros, whose RMS factor without eps is infinite: their 0 f
+                    // would be a NaN in the weights' sums
+                    if (kBack && h >= a.heads[which]) f = 0.f;
                     const Raw8<TIn>& turned = kBack ? now.d[kBack ? j : 0] : now.x[j];
                     (kInter ? turned.swapped() : turned.from_lane(other, in)).unpack(y);
                     if (kInter && !in) {

@@ -404,6 +404,24 @@ def test_prep_backward(ck, case):
             assert got["d" + n + "_weight"] is None
 
 
+@pytest.mark.parametrize("Hq,Hk,d,dt", [(3, 1, 64, BF), (3, 2, 64, F32), (1, 3, 128, BF), (5, 4, 96, F32), (3, 1, 256, BF), (3, 1, 37, F32)],
+                         ids=str)
+def test_prep_backward_without_eps(ck, Hq, Hk, d, dt):
+    """RMS norms with eps = 0 (no row is zero): heads that do not fill the rows a warp takes at once. Tolerances: as
+    test_prep_backward and near."""
+    gen = torch.Generator().manual_seed(d)
+    q, k, dq, dk = (torch.randn(50, h, d, generator=gen).to(dt) for h in (Hq, Hk, Hq, Hk))
+    w = torch.rand(d, generator=gen) + 0.5
+    got = ck.qk_norm_rope_bwd(*dev(q, k, dq, dk), norm="rms", eps=0.0, q_weight=w.cuda(), k_weight=w.cuda())
+    fine(ck)
+    for n, x, g in (("q", q, dq), ("k", k, dk)):
+        x64, w64 = x.double().requires_grad_(), w.double().requires_grad_()
+        dx, dw = torch.autograd.grad(ref.prep(x64, norm="rms", weight=w64, eps=0.0), [x64, w64], g.double())
+        big = (g.double() * w * x.double().square().mean(-1, keepdim=True).rsqrt()).abs().amax(-1, keepdim=True)
+        assert ((got["d" + n].double().cpu() - dx).abs() <= torch.finfo(dt).eps / 2 * dx.abs() + 2.0 ** -18 * big).all()
+        near("d" + n + "_weight", got["d" + n + "_weight"], dw)
+
+
 def test_prep_strided_in_place_and_default_positions(ck):
     B, T, Hq, Hk, d = 2, 50, 4, 2, 64
     gen = torch.Generator().manual_seed(0)
