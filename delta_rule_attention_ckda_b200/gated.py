@@ -86,6 +86,12 @@ def _rows(t, name: str, lead: int, dtype, dev) -> int:
     return row
 
 
+def _count(n: int, what: str) -> None:
+    """The library counts in 32 bits; ctypes would cut a larger number to its lower half."""
+    if n > 0x7fffffff:
+        raise ValueError(f"more than 2**31 - 1 {what}")
+
+
 def _indexes(t, name: str, n: Optional[int], dev) -> None:
     _on(t, name, dev)
     if t.dim() != 1 or (n is not None and t.shape[0] != n):
@@ -226,6 +232,7 @@ class _Problem:
         else:
             N, T = tokens
             total = N * T
+        _count(max(total, N, T), "tokens")
         self.o_shape = tokens + (Hv, dv)
         self.g_shape = tokens + (Hv,)
         self.state_shape = (N, Hv, dk, dv)
@@ -336,6 +343,7 @@ def gated_decode_step(q, k, v, g, beta, S, *, slots=None, o=None, stream=None) -
     if not isinstance(S, torch.Tensor) or S.dim() != 4:
         raise ValueError("S must be a [pool, Hv, dk, dv] tensor")
     pool = S.shape[0]
+    _count(max(N, pool), "rows or states")
     _check(S, "S", (pool, Hv, dk, dv), F32, dev)
     if slots is not None:
         _indexes(slots, "slots", N, dev)
@@ -374,8 +382,7 @@ class _Prep:
             if k.shape != self.tokens_shape + (self.Hk, self.d):
                 raise ValueError(f"k has shape {tuple(k.shape)}, expected {tuple(self.tokens_shape) + (self.Hk, self.d)}")
         tokens = prod(self.tokens_shape)
-        if tokens > 0x7fffffff:
-            raise ValueError("more than 2**31 - 1 tokens")
+        _count(tokens, "tokens")
         if norm not in NORMS:
             raise ValueError(f"norm must be one of {sorted(NORMS)}, got {norm!r}")
         if layout not in LAYOUTS:
@@ -530,6 +537,7 @@ def state_copy(S, src, dst, *, pool_dim=0, stream=None) -> torch.Tensor:
     layers, slots = S.shape[0] if pool_dim else 1, S.shape[pool_dim]
     if slots == 0:
         raise ValueError("S holds no states")
+    _count(max(layers, slots), "layers or states")
     _launch(dev, stream, load().ckda_state_copy, "ckda_state_copy",
             (_ptr(S), _ptr(src), _ptr(dst), src.shape[0], layers, slots, prod(S.shape[pool_dim + 1:])))
     return S

@@ -169,6 +169,33 @@ def test_binding_checks():
         ck.state_copy(S, fake(2, dtype=torch.int32), fake(2, dtype=torch.int32), pool_dim=2)
 
 
+def test_binding_counts():
+    """Counts beyond 32 bits are refused: cut to their lower half, 2**32 tokens would be none. (Tensors without memory.)"""
+    import delta_rule_attention_ckda_b200 as ck
+
+    def big(*shape, dtype=torch.float32):
+        return torch.empty(*shape, dtype=dtype, device="meta").as_subclass(_Fake)
+
+    n, bf, i32 = 1 << 32, torch.bfloat16, torch.int32
+    for lead in ((1, n), (n, 1), (1 << 20, 1 << 12), (1, 1 << 31)):
+        x, g = big(*lead, 1, 1, dtype=bf), big(*lead, 1)
+        with pytest.raises(ValueError, match="2[*][*]31"):
+            ck.gated_chunk_fwd(x, x, x, g, g)
+        with pytest.raises(ValueError, match="2[*][*]31"):
+            ck.gated_bwd(x, x, x, g, g, x)
+    x, g = big(n + 4, 1, 1, dtype=bf), big(n + 4, 1)
+    with pytest.raises(ValueError, match="2[*][*]31"):
+        ck.gated_chunk_fwd(x, x, x, g, g, cu_seqlens=big(2, dtype=i32))
+    with pytest.raises(ValueError, match="2[*][*]31"):
+        ck.gated_decode_step(x, x, x, g, g, big(n + 4, 1, 1, 1))
+    x, g = big(4, 1, 1, dtype=bf), big(4, 1)
+    with pytest.raises(ValueError, match="2[*][*]31"):
+        ck.gated_decode_step(x, x, x, g, g, big(n + 5, 1, 1, 1), slots=big(4, dtype=i32))
+    for shape in ((1, n + 8, 4), (n + 8, 1, 4)):
+        with pytest.raises(ValueError, match="2[*][*]31"):
+            ck.state_copy(big(*shape), big(1, dtype=i32), big(1, dtype=i32), pool_dim=1)
+
+
 def test_rows_of_wider_tensors():
     """The distance between tokens of slices, over one and two leading dimensions."""
     from delta_rule_attention_ckda_b200.gated import _rows
