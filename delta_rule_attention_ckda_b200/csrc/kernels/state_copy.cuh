@@ -36,7 +36,7 @@ state_copy_kernel(uint4* __restrict__ S, const int* __restrict__ src, const int*
     int* from = last + table;                                  // [pairs] source slot, -1 clear, -2 not copied
     int* to = from + pairs;
     const int tid = threadIdx.x;
-    uint4* base = S + (size_t)blockIdx.y * slots * pieces;     // one layer's pool
+    uint4* base = S + (long long)blockIdx.y * slots * pieces;  // one layer's pool
     const long long p0 = (long long)blockIdx.x * width;
     const int w = (int)min((long long)width, pieces - p0);
     for (int i = tid; i < table; i += kCopyThreads) {

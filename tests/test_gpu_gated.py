@@ -479,6 +479,25 @@ def test_state_copy_swap_and_bad_pairs(ck):
     fine(ck)
 
 
+def test_state_copy_in_the_last_of_many_layers(ck):
+    """Layers times slots beyond 2^32: the last layer's states move, and no other's. (Memory is taken, not filled.)"""
+    layers, slots = 65535, 65540
+    if torch.cuda.mem_get_info()[0] < layers * slots * 16 + (4 << 30):
+        pytest.skip("needs 73 GB")
+    S = torch.empty(layers, slots, 4, device="cuda")
+    some = torch.tensor([0, 1, 2, layers // 2, layers - 1]).cuda()
+    fill = torch.arange(5 * slots * 4, device="cuda", dtype=F32).view(5, slots, 4)
+    S[some] = fill
+    src, dst = torch.tensor([5, -1, slots - 1], dtype=torch.int32).cuda(), torch.tensor([7, slots - 2, 9], dtype=torch.int32).cuda()
+    ck.state_copy(S, src, dst, pool_dim=1)
+    fine(ck)
+    want = fill.clone()
+    want[:, 7], want[:, slots - 2], want[:, 9] = fill[:, 5], 0.0, fill[:, slots - 1]
+    assert torch.equal(S[some], want)
+    del S
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------- together
 
 def test_layer_run_together(ck):
