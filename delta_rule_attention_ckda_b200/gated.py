@@ -494,7 +494,8 @@ def rope_frequencies(rotary: int, base: float = 10000.0, *, factor: float = 1.0,
                  divides the slowest by factor;
       "by_parts": pairs that turn more than `fast` times in the trained length are left alone,
                  those that turn less than `slow` times are divided by factor, between them a ramp
-                 in the pair index; rope_scale is then 0.1 ln(factor) + 1."""
+                 in the pair index (which goes past the last pair where that still turns more than
+                 `slow` times); rope_scale is then 0.1 ln(factor) + 1."""
     import math
     if rotary < 2 or rotary % 2 != 0:
         raise ValueError(f"rotary must be even and at least 2, got {rotary}")
@@ -513,8 +514,10 @@ def rope_frequencies(rotary: int, base: float = 10000.0, *, factor: float = 1.0,
     elif scaling == "by_parts":
         def index(turns):                         # the (real) pair index that turns this often in `trained` tokens
             return rotary * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))
-        lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rotary // 2 - 1)
+        lo, hi = max(math.floor(index(fast)), 0), math.ceil(index(slow))
         ramp = ((torch.arange(rotary // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+        if hi <= 0:                               # even the first pair turns less than `slow` times
+            ramp.fill_(1)
         f = base ** -p * (1 - ramp + ramp / factor)
         scale = 0.1 * math.log(factor) + 1.0
     else:

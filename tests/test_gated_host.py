@@ -229,6 +229,25 @@ def test_frequencies():
             ck.rope_frequencies(bad.pop("rotary"), **bad)
 
 
+@pytest.mark.parametrize("rotary,base,trained", [(64, 10000.0, 131072), (128, 10000.0, 32768), (64, 10000.0, 4096), (16, 500.0, 8192),
+                                                 (128, 500000.0, 8192), (64, 10000.0, 6), (2, 10000.0, 4096)])
+def test_frequencies_by_parts(rotary, base, trained):
+    """What the three parts promise, also where no pair turns as little as `slow` times, or every pair does."""
+    import delta_rule_attention_ckda_b200 as ck
+    f, _ = ck.rope_frequencies(rotary, base)
+    part, _ = ck.rope_frequencies(rotary, base, factor=8.0, scaling="by_parts", trained=trained)
+    index = lambda turns: rotary * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+    share = (1 - part / f) / (1 - 1 / 8)                                  # 0: left alone, 1: divided by factor
+    for p in range(rotary // 2):
+        if p <= math.floor(index(32.0)):
+            assert abs(share[p]) < 1e-12, p
+        elif p >= index(1.0):
+            assert p < math.ceil(index(1.0)) or abs(share[p] - 1) < 1e-12, p
+        else:                                                             # between: strictly, in steps of one size
+            lo, hi = max(math.floor(index(32.0)), 0), math.ceil(index(1.0))
+            assert abs(share[p] - (p - lo) / (hi - lo)) < 1e-12, p
+
+
 def test_oracle_rule_is_the_per_channel_rule():
     """The scalar-gate definition against the library's per-channel oracle with the gate repeated."""
     import numpy as np
