@@ -25,7 +25,7 @@ from ._lib import (BF16, BWD_CHUNK_TC, BWD_RECURRENT, F32, PATH_CHUNK_TC, PATH_R
                    cp_prefix, decode_step, get_device_error, load, maps_workspace_bytes, noalloc_scratch_bytes,
                    recurrent_fwd,
                    workspace_bytes, LIB_PATH)
-from .gated import (gated_bwd, gated_bwd_workspace_bytes, gated_chunk_fwd, gated_decode_step,
+from .gated import (gated_bwd, gated_bwd_segment_tokens, gated_bwd_workspace_bytes, gated_chunk_fwd, gated_decode_step,
                     gated_fwd_workspace_bytes, gated_segment_tokens, qk_norm_rope, qk_norm_rope_bwd, rope_frequencies,
                     state_copy)
 from . import context_parallel
@@ -35,5 +35,5 @@ __all__ = ["bwd", "bwd_path", "BWD_CHUNK_TC", "BWD_RECURRENT", "bwd_workspace_by
            "workspace_bytes", "chunk_path", "chunk_segments", "get_device_error", "load", "CkdaError", "LIB_PATH", "F32", "BF16",
            "PATH_RECURRENT", "PATH_CHUNK_TC", "gated_chunk_fwd", "gated_fwd_workspace_bytes", "gated_segment_tokens",
            "gated_bwd",
-           "gated_bwd_workspace_bytes", "gated_decode_step", "qk_norm_rope", "qk_norm_rope_bwd", "rope_frequencies",
+           "gated_bwd_segment_tokens", "gated_bwd_workspace_bytes", "gated_decode_step", "qk_norm_rope", "qk_norm_rope_bwd", "rope_frequencies",
            "state_copy"]

@@ -84,8 +84,9 @@ def load(path: Optional[str] = None) -> ctypes.CDLL:
     ll, f = ctypes.c_longlong, ctypes.c_float
     lib.ckda_gated_fwd_workspace_bytes.argtypes = [i] * 7
     lib.ckda_gated_fwd_workspace_bytes.restype = sz
-    lib.ckda_gated_fwd_segment_tokens.argtypes = [i] * 7
-    lib.ckda_gated_fwd_segment_tokens.restype = i
+    for plan in (lib.ckda_gated_fwd_segment_tokens, lib.ckda_gated_bwd_segment_tokens):
+        plan.argtypes = [i] * 7
+        plan.restype = i
     lib.ckda_gated_fwd.argtypes = [vp] * 9 + [i] * 7 + [ll] * 3 + [i, vp, sz, vp]
     lib.ckda_gated_fwd.restype = i
     lib.ckda_gated_bwd_workspace_bytes.argtypes = [i] * 7

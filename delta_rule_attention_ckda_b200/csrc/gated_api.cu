@@ -478,6 +478,12 @@ size_t ckda_gated_bwd_workspace_bytes(int N, int total, int Hk, int Hv, int dk, 
     return chunked(s) ? chunk_layout(s, true).total : simt_bwd_layout(s).total;
 }
 
+int ckda_gated_bwd_segment_tokens(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt) {
+    const Shape s{N, 0, total, Hk, Hv, dk, dv, dt};
+    if (check_shape(s, true) != CKDA_OK || N == 0 || total == 0 || !chunked(s)) return 0;
+    return segment_chunks(s, true) * C;
+}
+
 ckda_status_t ckda_gated_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
                              const float* S0, const void* grad_o, const float* grad_S_T, void* grad_q, void* grad_k,
                              void* grad_v, float* grad_g, float* grad_beta, float* grad_S0, const int* cu_seqlens, int N,

@@ -253,6 +253,11 @@ def gated_segment_tokens(N, total, Hk, Hv, dk, dv, dtype=torch.bfloat16) -> int:
     return int(load().ckda_gated_fwd_segment_tokens(N, total, Hk, Hv, dk, dv, _dt(torch.empty(0, dtype=dtype))))
 
 
+def gated_bwd_segment_tokens(N, total, Hk, Hv, dk, dv, dtype=torch.bfloat16) -> int:
+    """As gated_segment_tokens, of gated_bwd's own plan."""
+    return int(load().ckda_gated_bwd_segment_tokens(N, total, Hk, Hv, dk, dv, _dt(torch.empty(0, dtype=dtype))))
+
+
 def gated_chunk_fwd(q, k, v, g, beta, S0=None, *, cu_seqlens=None, o=None, S_T=None, want_state=True, workspace=None,
                     stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """ckda_gated_fwd. Returns (o, S_T): o in v's type and shape (rows behind the last packed

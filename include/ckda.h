@@ -388,6 +388,7 @@ CKDA_API size_t ckda_gated_fwd_workspace_bytes(int N, int total, int Hk, int Hv,
  * the current device (a scheduling choice, as ckda_chunk_fwd_segments); 0 where it runs them
  * whole (for tests and reporting). ckda_gated_bwd has a plan of its own, from the same sizes. */
 CKDA_API int ckda_gated_fwd_segment_tokens(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt);
+CKDA_API int ckda_gated_bwd_segment_tokens(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt);
 CKDA_API ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
                                       const float* S0, void* o, float* S_T, const int* cu_seqlens, int N, int T,
                                       int total, int Hk, int Hv, int dk, int dv, long long q_stride,

@@ -99,6 +99,18 @@ def test_workspace_and_segments(lib):
     assert back(1, 10, 1, 1, 8, 8, F32) > 0 and back(1, 0, 1, 1, 8, 8, F32) == 0
 
 
+def test_backward_plan(lib):
+    """The backward pass has a plan of its own: its workspace holds what that plan takes."""
+    fwd_plan, plan, need = lib.ckda_gated_fwd_segment_tokens, lib.ckda_gated_bwd_segment_tokens, lib.ckda_gated_bwd_workspace_bytes
+    n = plan(1, 65536, 16, 16, 128, 128, BF)
+    assert n % 64 == 0 and 1024 <= n < 65536 and n != fwd_plan(1, 65536, 16, 16, 128, 128, BF)
+    assert plan(8, 32768, 16, 16, 128, 128, BF) == 0 and plan(1, 65536, 16, 16, 128, 128, F32) == 0 and plan(0, 0, 1, 1, 64, 64, BF) == 0
+    assert plan(1, 2777, 2, 4, 64, 128, BF) > 0 and plan(1, 2777, 2, 4, 0, 128, BF) == 0
+    whole = 65536 // 64 * 16 * (4 * 8192 + 3 * 128 * 128 * 2 + 64 * 128 * 6)        # what every chunk keeps, vectors and sums apart
+    places = 65536 // n * 16 * 3 * 128 * 128 * 4                                     # states, maps and cotangents of segments
+    assert need(1, 65536, 16, 16, 128, 128, BF) >= whole + places
+
+
 def test_device_error_name(lib):
     assert lib.ckda_status_string(7) not in (b"unknown status", b"ok")
 

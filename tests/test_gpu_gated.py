@@ -200,6 +200,51 @@ def test_backward_in_segments(ck, case, in_place):
     near_grads(got, q, k, v, g, b, do, S0, dST, cu)
 
 
+def longest(lens):
+    return lens[1] if isinstance(lens, tuple) else max(lens)
+
+
+def sizes(lens):
+    """N and the number of tokens, as the segment tests make them."""
+    return (lens[0], lens[0] * lens[1]) if isinstance(lens, tuple) else (len(lens), sum(lens) + 3)
+
+
+# Long enough for segments on more chunks than two an SM: launched one after the other, not closely.
+SEGMENTED_WIDE = [((1, 3000), 2, 8, 64, 64), ([2900, 40, 3100], 1, 8, 64, 64)]
+
+
+@pytest.mark.parametrize("case", SEGMENTED + SEGMENTED_WIDE, ids=str)
+def test_segments_are_planned(ck, case):
+    """Both passes of the cases above have a plan that cuts their longest sequence."""
+    lens, Hk, Hv, dk, dv = case
+    for plan in (ck.gated_segment_tokens, ck.gated_bwd_segment_tokens):
+        n = plan(*sizes(lens), Hk, Hv, dk, dv)
+        assert 0 < n < longest(lens) and n % 64 == 0
+    N, total = sizes(lens)
+    if case in SEGMENTED_WIDE:
+        assert (total // 64 + N) * Hv > 2 * torch.cuda.get_device_properties(0).multi_processor_count
+
+
+@pytest.mark.parametrize("case", SEGMENTED_WIDE, ids=str)
+def test_segments_on_many_heads(ck, case):
+    lens, Hk, Hv, dk, dv = case
+    N, total = sizes(lens)
+    cu, lead = (None, lens) if isinstance(lens, tuple) else (packed(lens, 3)[0], (total,))
+    q, k, v, g, b, S0, do, dST = make(lead, Hk, Hv, dk, dv, BF, total, N, gate=-5.0)
+    x = dev(q, k, v, g, b, do, S0, dST)
+    on = None if cu is None else cu.cuda()
+    o, ST = ck.gated_chunk_fwd(*x[:5], x[6], cu_seqlens=on)
+    got = ck.gated_bwd(*x, cu_seqlens=on)
+    fine(ck)
+    if cu is not None:
+        for t in (o, *(got[n] for n in ("dq", "dk", "dv", "dg", "dbeta"))):
+            t[total - 3:] = 0.0
+    o_ref, S_ref = ref.gated_fwd(q, k, v, g, b, S0, cu)
+    near("o", o, o_ref)
+    near("S_T", ST, S_ref)
+    near_grads(got, q, k, v, g, b, do, S0, dST, cu)
+
+
 def test_backward_by_differences(ck):
     """The fp32 gradients against central differences of the forward (fp32, steps of 2^-6: the
     rule is at most cubic in one input's entries here, differences are off by the third
