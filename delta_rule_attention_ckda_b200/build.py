@@ -15,7 +15,10 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = [*ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "--expt-relaxed-constexpr",
-         "-Xptxas", "-warn-spills"]
+         "-Xptxas", "-warn-spills", "-Xptxas", "-v"]
+# Kernels that move registers between their warps, by part of their name: the file and constant that
+# say how many a thread is compiled to. Such a split adds up against no other number.
+SPLITS = {"chain_fwd_kernel": ("kernels/gated_chain.cuh", "kRegLaunch"), "chain_bwd_kernel": ("kernels/gated_chain.cuh", "kRegLaunch")}
 
 
 TARGETS = {LIB: ["ckda_api.cu", "gated_api.cu"], SELFTEST_LIB: ["selftest.cu"]}
@@ -36,6 +39,23 @@ def _inputs(src: str):
                     todo.append(os.path.normpath(os.path.join(d, name)))
                     break
     return seen | {os.path.abspath(__file__)}
+
+
+def _check_registers(log: str) -> None:
+    """The compiler's report (-Xptxas -v) against SPLITS."""
+    entry = None
+    for line in log.splitlines():
+        m = re.search(r"Compiling entry function '(\S+)'", line)
+        if m:
+            entry = m.group(1)
+        m = re.search(r"Used (\d+) registers", line)
+        if m and entry:
+            for part, (file, name) in SPLITS.items():
+                if part in entry:
+                    want = int(re.search(rf"\b{name} = (\d+)", open(os.path.join(CSRC, file)).read()).group(1))
+                    if int(m.group(1)) != want:
+                        raise RuntimeError(f"{entry} was compiled to {m.group(1)} registers a thread; its split between warps needs {want}")
+            entry = None
 
 
 def _newer(out: str, files) -> bool:
@@ -64,13 +84,25 @@ def _build_one(lib: str, sources, force: bool, verbose: bool, extra) -> None:
                os.path.join(CSRC, src), "-o", tmp]
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
-        procs.append((subprocess.Popen(cmd), tmp, obj, cmd))
+        log = open(tmp + ".log", "w+")
+        procs.append((subprocess.Popen(cmd, stderr=log), log, tmp, obj, cmd))
     failed = None
-    for p, tmp, obj, cmd in procs:
-        if p.wait() != 0:
-            failed = subprocess.CalledProcessError(p.returncode, cmd)
-        else:
+    for p, log, tmp, obj, cmd in procs:
+        p.wait()
+        with log:
+            log.seek(0)
+            said = log.read()
+        os.remove(log.name)
+        for line in said.splitlines():
+            if verbose or not re.search(r"^ptxas info|bytes stack frame|^$", line):
+                print(line, file=sys.stderr)
+        try:
+            if p.returncode != 0:
+                raise subprocess.CalledProcessError(p.returncode, cmd)
+            _check_registers(said)
             os.replace(tmp, obj)
+        except (subprocess.CalledProcessError, RuntimeError) as e:
+            failed = e
     if failed:
         raise failed
     tmp = lib + f".tmp{os.getpid()}"
@@ -86,5 +118,4 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
 
 
 if __name__ == "__main__":
-    build(force="--force" in sys.argv, verbose=True,
-          extra=(["-Xptxas", "-v"] if "--ptxas-v" in sys.argv else []))
+    build(force="--force" in sys.argv, verbose=True)

@@ -115,6 +115,21 @@ def test_device_error_name(lib):
     assert lib.ckda_status_string(7) not in (b"unknown status", b"ok")
 
 
+def test_build_checks_register_splits():
+    """A chain compiled to another number of registers than its split adds up to fails the build, not the calls."""
+    from delta_rule_attention_ckda_b200 import build
+    said = ("ptxas info    : Compiling entry function '_ZN4ckda5gated16chain_bwd_kernelILi64EEEvv' for 'sm_100a'\n"
+            "ptxas info    : Function properties for _ZN4ckda5gated16chain_bwd_kernelILi64EEEvv\n"
+            "    104 bytes stack frame, 104 bytes spill stores, 108 bytes spill loads\n"
+            "ptxas info    : Used {} registers, used 2 barriers, 104 bytes cumulative stack size\n"
+            "ptxas info    : Compiling entry function '_ZN4ckda5gated12intra_kernelILi64EEEvv' for 'sm_100a'\n"
+            "ptxas info    : Used 90 registers, used 1 barriers\n")
+    build._check_registers(said.format(128))
+    for n in (80, 127, 168):
+        with pytest.raises(RuntimeError, match="chain_bwd_kernel.*registers"):
+            build._check_registers(said.format(n))
+
+
 class _Fake(torch.Tensor):
     """A host tensor that reports a CUDA device: the checks in front of a call run without a GPU."""
     @property
