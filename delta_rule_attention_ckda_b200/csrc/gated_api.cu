@@ -727,10 +727,11 @@ ckda_status_t ckda_state_copy(float* S, const int* src, const int* dst, int pair
     if (!aligned16(S) || !aligned4(src) || !aligned4(dst)) return CKDA_ERR_MISALIGNED;
     if (pairs > kCopyMaxPairs || state_floats % 4 != 0 || layers > 65535) return CKDA_ERR_UNSUPPORTED;
     const long long pieces = state_floats / 4;
-    // Slice: about 32 KB of states a CTA (several CTAs per SM overlap their reads and writes),
-    // narrower while that leaves SMs without work, 128 bytes at least.
-    int width = std::max(8, std::min(256, 2048 / pairs));
-    while (width > 8 && ((pieces + width - 1) / width) * layers < 2LL * sm_count()) width /= 2;
+    // Slice: about 32 KB of states a CTA (several CTAs per SM overlap their reads and writes), narrower
+    // while that leaves SMs without work, 128 bytes at least, and whole sectors of 32 bytes, so that no two CTAs
+    // write parts of one.
+    int width = std::max(8, std::min(256, 2048 / pairs) & ~1);
+    while (width > 8 && ((pieces + width - 1) / width) * layers < 2LL * sm_count()) width = std::max(8, width / 2 & ~1);
     if (pieces < width) width = (int)pieces;
     const long long slices = (pieces + width - 1) / width;
     if (slices > 0x7fffffffLL) return CKDA_ERR_UNSUPPORTED;
