@@ -298,10 +298,10 @@ struct Maps {
 template <int DK, bool kBack>
 cudaError_t run_intra(const Call& c, const Maps& m, const ChainIn& in) {
     constexpr size_t smem = intra_smem(DK);
-    cudaError_t e = kernel_ready(intra_kernel<DK>, smem);
+    cudaError_t e = kernel_ready(intra_kernel<DK, kBack>, smem);
     if (e != cudaSuccess) return e;
-    intra_kernel<DK><<<dim3((unsigned)Seqs::slots(c.s.N, c.s.total), (unsigned)c.s.Hk), 128, smem, c.st>>>(
-        m.q, m.k, in, c.g, c.beta, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk, kBack);
+    intra_kernel<DK, kBack><<<dim3((unsigned)Seqs::slots(c.s.N, c.s.total), (unsigned)c.s.Hk), 128, smem, c.st>>>(
+        m.q, m.k, in, c.g, c.beta, c.ws, c.seqs, c.s.Hk, c.s.Hv, c.s.dk);
     return cudaPeekAtLastError();
 }
 

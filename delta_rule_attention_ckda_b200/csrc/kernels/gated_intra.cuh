@@ -1,7 +1,7 @@
 // Chunked gated delta rule, part 1: what a 64-token chunk holds before any state is known, all
 // chunks side by side. With G the in-chunk cumulated log gate and D_ij = e^{G_i - G_j}:
 //   P = tril(D (.) Q K^T),   A = tril(D (.) K K^T, -1),   Z = -(I + A diag(beta))^{-1} A
-// For the backward pass (`apart`) P's diagonal lies in a vector of its own and P holds zeros there.
+// For the backward pass (kApart) P's diagonal lies in a vector of its own and P holds zeros there.
 // Z serves both passes: W = X + Z (beta X) solves the chunk's triangular system forward, and
 // y = dU + Z^T (beta dU) its adjoint, without a division by beta.
 //
@@ -67,10 +67,10 @@ __device__ __forceinline__ void block_product(float (&acc)[2][4], const float* X
     }
 }
 
-template <int DK>
+template <int DK, bool kApart>
 __global__ void __launch_bounds__(128, 4)
 intra_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const ChainIn in,
-             const float* __restrict__ g, const float* __restrict__ beta, ChunkWs ws, Seqs seqs, int Hk, int Hv, int dk, bool apart) {
+             const float* __restrict__ g, const float* __restrict__ beta, ChunkWs ws, Seqs seqs, int Hk, int Hv, int dk) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full;
@@ -210,7 +210,7 @@ intra_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUt
                     const float d = j <= i ? expf((ghi - ghj[e]) + (gli - glj[e])) : 0.f;
                     p[e] = j <= i ? d * qk[nn][2 * half + e] : 0.f;
                     a[e] = j < i ? d * kk[nn][2 * half + e] : 0.f;
-                    if (apart && nn / 2 == warp && j == i) {                             // the backward pass takes the diagonal by itself
+                    if (kApart && nn / 2 == warp && j == i) {                             // the backward pass takes the diagonal by itself
                         ws.vec[wh * VEC + VEC_PD + i] = p[e];
                         p[e] = 0.f;
                     }
