@@ -192,7 +192,8 @@ bool chunked_fits(const Shape& s) { return s.Hk <= 65535 && (long long)Seqs::slo
 // forward chain one after the other (4 us): a pass takes its waves of CTAs times a segment's chunks
 // and 5 or 6 more for its start, a scan a quarter per segment; going back, the chain that keeps its
 // states counts 7/4, the adjoint's two passes 6/4 and 8/4. The longest sequence is not known
-// on the host: the average is taken, back, where segments pay sooner, a quarter more. Segments have
+// on the host: the average is taken, back, where segments pay sooner, a quarter more. A batch of one long
+// and many short sequences is therefore run whole, as long as its longest takes alone. Segments have
 // to gain an eighth. B200, us, whole and in segments: one sequence of 2048 tokens and 16 heads of 128,
 // forward 140 and 112, backward 521 and 306; of 65536, forward 4200 and 1570; 2 of 4096, forward 290
 // and 245, backward 1086 and 740; 1 of 1024, forward 83 and 89 (not taken), backward 257 and 208.
@@ -588,7 +589,7 @@ ckda_status_t ckda_gated_decode_step(const void* q, const void* k, const void* v
 namespace {
 
 // Blocks of the backward pass, which each leave a partial sum of the weights' gradients: fixed by
-// the sizes alone, so those sums have one order.
+// the sizes and the device's number of SMs, so those sums have one order on it.
 constexpr int kPrepMaxBlocks = 148 * 2;
 int prep_blocks(long long units) { return (int)std::max(1LL, std::min(units, (long long)kPrepMaxBlocks)); }
 

@@ -17,9 +17,10 @@
 // The state is split 32 channels at a time, and its product starts on the first (2 to 3% of the
 // time).
 //
-// Measured, 8 x 16 sequences of 4096 tokens: 284 us, 4.4 us a chunk (7500 cycles) of which the
-// products are 2000, the tensor pipe 28% busy; with the states, W and U for the backward pass
-// 376 us (480 while the out warps, which sum <dO, o>, held the whole stage). A chunk's tiles brought to L2 ahead gain 1%: memory is not what it waits for.
+// Measured, 8 x 16 sequences of 4096 tokens: 266 us, 4.2 us a chunk (7500 cycles) of which the
+// products are 2000, the tensor pipe 25% busy; with the states, V - W and U for the backward pass
+// 385 us (100 more while the out warps, which sum <dO, o>, held the whole stage). A chunk's tiles brought
+// to L2 ahead gain 1%: memory is not what it waits for.
 //
 // What hides what: the output's products (P U), its epilogue and its store run under the next
 // chunk's state split; loads run a chunk ahead. A product of N = 64 takes as long as one of
@@ -28,8 +29,8 @@
 // Rounding: raw K, Q, V are exact; every other operand (S, beta X, Z, U, P) is two bf16 terms
 // (2.7e-6 of a value at RMS), o is rounded once at its store. Sums are fp32; S' is formed in
 // registers. Backward: U in three terms, and the adjoint's operands of the state too, because dg
-// sums differences of <dO, o> and <dV, v> (a model of this arithmetic in fp64: dg off by 4e-6 in
-// place of 2.1e-5 where the states are large, by 1.3e-6 in place of 1.4e-5 elsewhere).
+// is a difference of sums (a model of this arithmetic in fp64: dg off by 4e-6 in place of 2.1e-5 where the
+// states are large, by 1.3e-6 in place of 1.4e-5 elsewhere).
 #pragma once
 #include "gated_mma.cuh"
 #include "tc_primitives.cuh"
@@ -818,11 +819,12 @@ segment_result_kernel(SegArgs sg, Seqs seqs, const float* __restrict__ places, b
 //   dS <- e^{G_C} dS + Q^T (e^G (.) dO) - K^T (e^G (.) dV)
 // and the sums that the gradients of beta and g need (see gated_grads.cuh): w.y and what a token's
 // future takes from it, <S', dS> per chunk. P comes without its diagonal, whose part of dU and y,
-// q_i.k_i dO_i, is added where the whole is needed. The layout and roles of the forward chain; the out warps prepare the operand e^G dO and
-// take y from TMEM for dV and the sums. The products that do not wait for dS (P^T dO, Q^T dO)
-// run under the epilogues; the operands of the update carry three terms. Measured as the forward
-// chain: 565 us; the out warps' operand, rows and sums over lanes take all of a chunk's 16000
-// cycles, and 1.9 GB of states and sums are moved (47% of the bandwidth).
+// q_i.k_i dO_i, is added where the whole is needed. The layout and roles of the forward chain; the out
+// warps prepare the operand e^G dO and take y from TMEM for dV and the sums. The products that do not
+// wait for dS (P^T dO, Q^T dO) run under the epilogues; the operands of the update carry three terms.
+// Measured as the forward chain: 592 us (541 with the own part inside y, which left dg without digits under
+// strong gates); the out warps' operand, rows and sums over lanes take all of a chunk's 17000 cycles, and
+// 1.9 GB of states and sums are moved (44% of the bandwidth).
 template <int DK>
 __global__ void __launch_bounds__(kChainThreads, 1)
 chain_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,

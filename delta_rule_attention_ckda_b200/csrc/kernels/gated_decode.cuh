@@ -11,7 +11,7 @@
 // then over the 8 warps in shared memory. Narrow slabs (CW = 32) give few rows enough CTAs to
 // fill the GPU; wide ones (CW = 128) cost fewer reductions per byte.
 //
-// Measured, 256 rows of 16 heads of 128 x 128 (541 MB): 91 us, 91% of the copy bandwidth, at two
+// Measured, 256 rows of 16 heads of 128 x 128 (541 MB): 94 us, 88% of the copy bandwidth, at two
 // blocks an SM, which keep a whole state of 64 KB each in flight; left to three, the loads of
 // a thread are split and it takes 119. 3 rows: 5 us, the launch and one trip to memory and back.
 #pragma once

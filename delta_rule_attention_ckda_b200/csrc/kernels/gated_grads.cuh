@@ -19,7 +19,7 @@
 // under strong gates.
 //
 // dQ and dK are rounded to bf16 at the end, so their operands go in one bf16 term; dg and
-// dbeta come from the chains' fp32 sums. Memory-bound: per chunk and head 157 KB are read (states
+// dbeta come from the chains' fp32 sums. Per chunk and head 157 KB are read (states
 // and cotangents 64, the rest tokens) for 2500 warp products. One CTA of eight warps an SM walks
 // over (chunk, key head) pairs; every tile of the next pair is asked for as soon as the products
 // that read its place are done, so about 100 KB are always on their way. The tiles come by bulk
@@ -29,9 +29,9 @@
 // straight and transposed; then a warp owns 16 tokens and half of the channels. Value heads
 // that share a key head are summed in the accumulators, in head order.
 //
-// Measured, 8192 chunks of 128 x 128 (1.3 GB): 499 us, 40% of the copy bandwidth; 714 before the bulk
+// Measured, 8192 chunks of 128 x 128 (1.3 GB): 487 us, 41% of the copy bandwidth; 714 before the bulk
 // copies. What bounds it now is the warps' own products and fragment loads between barriers (issue
-// 24%, tensor pipe 34%, shared memory 35%) with one CTA an SM by shared memory; sixteen warps
+// 22%, tensor pipe 30%, shared memory 32%) with one CTA an SM by shared memory; sixteen warps
 // spill and are slower.
 #pragma once
 #include "gated_chain.cuh"

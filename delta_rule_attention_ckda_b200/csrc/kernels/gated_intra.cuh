@@ -13,8 +13,8 @@
 //   R = A_IJ + sum_M (A beta)_IM Z_MJ,   Z_IJ = -(R_IJ + sum_M Z_IM beta_M R_MJ),
 // on tf32 products in three passes (operands to 2^-21).
 //
-// Measured, 8192 chunks of 128 channels (436 MB): 157 us, 42% of the copy bandwidth. Phases between
-// block barriers with few products each: the issue slots are 39% busy, shared memory 55%. Four
+// Measured, 8192 chunks of 128 channels (436 MB): 158 us, 42% of the copy bandwidth (164 with P's diagonal
+// apart). Phases between block barriers with few products each: the issue slots are 37% busy, shared memory 51%. Four
 // CTAs an SM by registers and shared memory; with P stored straight from registers five fit,
 // which is no faster, nor is the substitution on four warps in place of two. With row copies instead of tensor copies and three doubling levels: 182 us.
 #pragma once

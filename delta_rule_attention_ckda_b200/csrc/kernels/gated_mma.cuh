@@ -107,14 +107,6 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t&
     lo = upper2(__float_as_uint(x), __float_as_uint(y));
 }
 
-// The left operand of a k-step (16 wide) from two accumulator tiles of the product before.
-__device__ __forceinline__ void operand(const float (&u)[4], const float (&v)[4], uint32_t (&a)[4]) {
-    a[0] = pack2(u[0], u[1]);
-    a[1] = pack2(u[2], u[3]);
-    a[2] = pack2(v[0], v[1]);
-    a[3] = pack2(v[2], v[3]);
-}
-
 // Tiles of 64 tokens as tensor copies write them: blocks of [64 rows][64 channels], rows of 128
 // bytes, the 16-byte pieces of a row exchanged by its number (the 128-byte swizzle).
 __device__ __forceinline__ uint32_t swz(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }

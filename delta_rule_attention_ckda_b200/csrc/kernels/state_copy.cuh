@@ -9,7 +9,7 @@
 // "all reads, then all writes" needs one block barrier and no staging memory. Which pair
 // counts for a destination comes from a small hash table of (destination, last pair).
 //
-// Measured, 96 pairs of 16 states of 128 x 128 (201 MB): 32 us, 96% of the copy bandwidth; 12 layers
+// Measured, 96 pairs of 16 states of 128 x 128 (201 MB): 34 us, 91% of the copy bandwidth; 12 layers
 // of two pairs: 5 us, a launch.
 #pragma once
 #include "gated_common.cuh"

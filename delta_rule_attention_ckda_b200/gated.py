@@ -29,7 +29,6 @@ from ._lib import _device, _dt, _raise, load
 
 NORMS = {"none": 0, "l2": 1, "rms": 2}          # ckda_prep_norm_t
 LAYOUTS = {"half": 0, "interleaved": 1}
-MAX_COPY_PAIRS = 1024
 F32, I32 = torch.float32, torch.int32
 
 

@@ -370,7 +370,12 @@ CKDA_API ckda_status_t ckda_decode_step_ex(const void* q, const void* k, const v
  * - g, beta, their gradients, positions, inv_freq and the indexes in device memory
  *   (cu_seqlens, slots, src, dst) need their own type's alignment only. An index that is out of range or out of order is cut to the tensors or its work is
  *   skipped, never followed, and ckda_get_device_error then returns CKDA_ERR_INDEX.
- * - Results do not depend on the run: every sum has one order.
+ * - Results do not depend on the run: every sum has one order, which the sizes and the device's number
+ *   of SMs fix.
+ * - NaN and infinities of one sequence stay out of the others, and those behind the last reach nothing.
+ *   Within a sequence the tensor cores take 64 tokens at once: a token that is not finite may reach the
+ *   results of the tokens before it in its 64 (counted from the sequence's start), not only of those
+ *   behind it. Tokens that pad a dense batch therefore have to hold finite values.
  */
 
 /*
@@ -388,6 +393,8 @@ CKDA_API size_t ckda_gated_fwd_workspace_bytes(int N, int total, int Hk, int Hv,
  * the current device (a scheduling choice, as ckda_chunk_fwd_segments); 0 where it runs them
  * whole (for tests and reporting). ckda_gated_bwd has a plan of its own, from the same sizes. */
 CKDA_API int ckda_gated_fwd_segment_tokens(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt);
+/* Both plans know the average length only: one long sequence among many short ones is run whole, on
+ * as many SMs as it has heads. Such batches are faster with the long sequence in a call of its own. */
 CKDA_API int ckda_gated_bwd_segment_tokens(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt);
 CKDA_API ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
                                       const float* S0, void* o, float* S_T, const int* cu_seqlens, int N, int T,
@@ -403,6 +410,10 @@ CKDA_API ckda_status_t ckda_gated_fwd(const void* q, const void* k, const void* 
  *   grad_S0 [N][Hv][dk][dv] fp32 out or NULL; may be grad_S_T
  *   workspace: ckda_gated_bwd_workspace_bytes(...) bytes, as above.
  * The forward is recomputed from its inputs; nothing of it need be kept.
+ * Accuracy on the tensor cores: grad_q and grad_k are off by about two roundings to bf16, grad_v by one,
+ * grad_beta and grad_S0 by less than 4e-6 of their norms, grad_g by 0.5 to 2.3e-5 of its norm however
+ * strongly the gates decay. A gate much stronger than the others of its 64 tokens has a gradient that is
+ * small beside theirs; it is that accurate relative to theirs, not to its own size.
  */
 CKDA_API size_t ckda_gated_bwd_workspace_bytes(int N, int total, int Hk, int Hv, int dk, int dv, ckda_dtype_t dt);
 CKDA_API ckda_status_t ckda_gated_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
@@ -446,7 +457,8 @@ typedef enum {
  *   q_weight, k_weight [d] fp32 or NULL (ones)
  *   positions [tokens] int32 (int64 with positions64 = 1), or NULL: row index modulo `period`
  *   inv_freq [rotary / 2] fp64 (may be NULL when rotary is 0)
- * 1 <= d <= CKDA_PREP_MAX_D; rotary even, 0 <= rotary <= d.
+ * 1 <= d <= CKDA_PREP_MAX_D; rotary even, 0 <= rotary <= d. q, k, the weights and the outputs start on 16
+ * bytes, whatever the distance between tokens (CKDA_ERR_MISALIGNED).
  */
 CKDA_API ckda_status_t ckda_qk_prep(const void* q, const void* k, void* q_out, void* k_out, const float* q_weight,
                                     const float* k_weight, const void* positions, int positions64,
